@@ -79,6 +79,7 @@ typedef int mbw_status;
 #define MBW_ERR_UNSUPPORTED 5         /* no kernel for this device or request */
 #define MBW_ERR_CUDA 6                /* a CUDA runtime call failed */
 #define MBW_ERR_DEVICE_TIMEOUT 7      /* a device-side bounded wait gave up */
+#define MBW_ERR_DEVICE_RANGE 8        /* a kernel met a page, slot, position, length or token id out of range */
 
 /* Largest N, K or M a call accepts (MBW_ERR_BAD_SHAPE above it). The kernels
  * index rows and columns in 32-bit integers, and a tile may run up to 256 rows
@@ -285,6 +286,134 @@ mbw_status gemv_fused_awq_g128(const uint8_t *Wq, const void *scales, const uint
                                int64_t M, int64_t N, int64_t K, int repacked, const mbw_fusion *fusion,
                                void *workspace, size_t ws_bytes, mbw_stream_t stream);
 
+/*
+ * 4-bit paged key/value cache: what stands between the QKV product and the
+ * output product of a decode step. `pages` holds num_pages pages of page_size
+ * tokens (16, 32, ... up to 1024, a multiple of 16) of kv_heads heads of
+ * head_dim (64, 128 or 256) dimensions, each value as scale * code + minimum
+ * with a 4-bit code and one fp16 (scale, minimum) pair per token, head and
+ * `group` (32 or 64) dimensions, for K and for V: at head_dim 128, group 64,
+ * 144 bytes per token and head, where bf16 takes 512. The order of the bytes
+ * in a page is the kernels' own (csrc/kv4.cuh); mbw_kv4_gather reads values.
+ * pages: 16-byte aligned, num_pages * mbw_kv4_page_bytes() bytes. A page need
+ * not be cleared before its first use.
+ */
+typedef struct mbw_kv4_cache {
+    void *pages;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t group;
+} mbw_kv4_cache;
+
+/* Bytes of one page; 0 if the sizes are not supported. */
+size_t mbw_kv4_page_bytes(int32_t page_size, int32_t kv_heads, int32_t head_dim, int32_t group);
+
+/*
+ * Position rotation: of the first rotary_dim dimensions of a head (a multiple
+ * of 16, at most head_dim), the pairs (i, i + rotary_dim / 2), or (2i, 2i + 1)
+ * when `interleaved` is 1, turn by the token's position.
+ *   cos_sin   : fp32 [max_pos][rotary_dim], per position the rotary_dim / 2
+ *               cosines, then the sines; 16-byte aligned
+ *   positions : int32 [T], each in [0, max_pos)
+ */
+typedef struct mbw_rope {
+    const float *cos_sin;
+    int64_t max_pos;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    const int32_t *positions;
+} mbw_rope;
+
+/*
+ * mbw_kv4_append -- rotate T tokens' queries and keys and store their keys and
+ * values in the cache, one kernel.
+ *   k, v  : bf16, row t of kv_heads * head_dim values at k + t * k_stride
+ *           (strides in elements, so that they may be parts of one QKV output)
+ *   slots : int64 [T], page * page_size + place in the page; the slots of one
+ *           call are distinct. A negative slot: the token is not stored.
+ *   q     : bf16, row t of q_heads * head_dim values; q_out the same, rotated
+ *           (may be q itself). q_heads = 0: no queries.
+ *   rope  : NULL: nothing is rotated (q is copied).
+ * Keys are rounded to bf16 after the rotation, then quantized like values: per
+ * group, m = fp16(min), s = fp16((max - m) / 15), code = clamp(rint((x - m) /
+ * s), 0, 15), 0 where s = 0, each step one IEEE fp32 operation, ties to even.
+ * A group that holds a NaN, or a value beyond fp16's range, reads as NaN.
+ * Pointers 16-byte aligned, strides multiples of 8. A slot or position past
+ * the end is reported by mbw_check_device_error (MBW_ERR_DEVICE_RANGE); the
+ * token of such a slot is not stored.
+ */
+mbw_status mbw_kv4_append(const mbw_kv4_cache *cache, const void *k, int64_t k_stride, const void *v,
+                          int64_t v_stride, const int64_t *slots, const void *q, int64_t q_stride, void *q_out,
+                          int64_t q_out_stride, int64_t q_heads, const mbw_rope *rope, int64_t T,
+                          mbw_stream_t stream);
+
+/* mbw_kv4_gather -- the values the cache holds at `slots`, rounded to bf16:
+ * k, v : bf16 [T][kv_heads][head_dim]; zeros for a negative slot. */
+mbw_status mbw_kv4_gather(const mbw_kv4_cache *cache, const int64_t *slots, void *k, void *v, int64_t T,
+                          mbw_stream_t stream);
+
+/*
+ * mbw_kv4_attention -- out = softmax(scale * q . K^T) . V over the cache, for
+ * T query tokens of B requests, each query head with the KV head of its group
+ * (q_heads / kv_heads query heads share one).
+ *   q           : bf16, row t of q_heads * head_dim values at q + t * q_stride
+ *   out         : bf16 (fp32 under the fp32 hook), rows out_stride apart
+ *   lse         : fp32 [T][q_heads] natural log of the sum of the exponentials,
+ *                 or NULL
+ *   block_table : int32, request b's pages at block_table + b * table_stride,
+ *                 table_width of them readable
+ *   ctx_lens    : int32 [B], tokens in the cache, the queries' own among them
+ *                 (append first); <= 0: none
+ *   q_starts    : int32 [B + 1], request b's queries are tokens q_starts[b] ..
+ *                 q_starts[b + 1] - 1 (from 0 to T, never falling; a request
+ *                 may have none), or NULL: T / B each
+ *   window      : 0, or the number of last positions a query sees
+ * The last query of a request sits at its last position; each sees the keys up
+ * to its own. A query that sees no key gets zeros (lse: minus infinity). Keys
+ * and values at places a query does not see, or past a request's length, do
+ * not enter, whatever they hold.
+ * workspace: mbw_kv4_attention_workspace_bytes() bytes, zero before its first
+ * use and left so by every call (one workspace per stream). Smaller or NULL:
+ * long contexts are split over fewer CTAs, or none, and take longer.
+ * A page id or length out of range is reported by mbw_check_device_error
+ * (MBW_ERR_DEVICE_RANGE); that request's output is then unspecified.
+ */
+mbw_status mbw_kv4_attention(const mbw_kv4_cache *cache, const void *q, int64_t q_stride, void *out,
+                             int64_t out_stride, float *lse, const int32_t *block_table, int64_t table_stride,
+                             int64_t table_width, const int32_t *ctx_lens, const int32_t *q_starts, int64_t B,
+                             int64_t T, int64_t q_heads, float scale, int64_t window, void *workspace,
+                             size_t ws_bytes, mbw_stream_t stream);
+size_t mbw_kv4_attention_workspace_bytes(int32_t head_dim);
+
+/*
+ * mbw_token_logprobs -- what a row of logits says about tokens, in one read of
+ * the logits (behind the LM head product). Over y = scale * logits:
+ *   logits       : bf16 (fp32 when `fp32` is 1), rows of V, row_stride elements
+ *                  apart; element alignment suffices (16 bytes are read faster)
+ *   targets      : int32 [M] token ids, negative: none; or NULL
+ *   logprob      : fp32 [M] log softmax(y)[target] (0 without a target)
+ *   rank         : int32 [M] the target's place, from 1, among the tokens
+ *                  ordered by logit, then by the lower id (0 without a target)
+ *   entropy      : fp32 [M] -sum p log p, in nats
+ *   top_ids      : int32 [M][top_k] the most likely tokens in that order, -1
+ *                  where fewer have a probability; top_k <= 32
+ *   top_logprobs : fp32 [M][top_k] their log probabilities (minus infinity there)
+ * Any output may be NULL. Logits of minus infinity are masked tokens; in a row
+ * of them alone log probabilities are minus infinity, the entropy 0. A NaN or
+ * plus infinity makes the row's numbers NaN. An id >= V counts as none and is
+ * reported by mbw_check_device_error (MBW_ERR_DEVICE_RANGE).
+ * workspace: mbw_token_logprobs_workspace_bytes() bytes, zero before its first
+ * use and left so by every call (one per stream). Smaller or NULL: few rows
+ * run on fewer CTAs and take longer.
+ */
+mbw_status mbw_token_logprobs(const void *logits, int fp32, int64_t row_stride, const int32_t *targets, int64_t M,
+                              int64_t V, float scale, int32_t top_k, float *logprob, int32_t *rank, float *entropy,
+                              int32_t *top_ids, float *top_logprobs, void *workspace, size_t ws_bytes,
+                              mbw_stream_t stream);
+size_t mbw_token_logprobs_workspace_bytes(void);
+
 /* Bytes of workspace the largest plan of `op` may use for this shape (0 if none). */
 size_t mbw_workspace_bytes(int op, int64_t M, int64_t N, int64_t K);
 
@@ -328,8 +457,10 @@ int mbw_plan_index(int op, int64_t M, int64_t N, int64_t K);
  * into buf (NUL-terminated, truncated to len). Returns MBW_OK. */
 mbw_status mbw_plan_describe(int op, int64_t M, int64_t N, int64_t K, char *buf, size_t len);
 
-/* Read and clear the device-side error flag set by bounded waits inside
- * kernels (synchronizes the current device). MBW_OK or MBW_ERR_DEVICE_TIMEOUT. */
+/* Read and clear the device-side error flags set by bounded waits inside
+ * kernels and by values out of range that the cache and token kernels met
+ * (synchronizes the current device). MBW_OK, MBW_ERR_DEVICE_TIMEOUT or
+ * MBW_ERR_DEVICE_RANGE. */
 mbw_status mbw_check_device_error(void);
 
 /* Self-test of the failure path above. Launches two one-thread kernels on
@@ -344,8 +475,8 @@ mbw_status mbw_selftest_wait_expiry(int64_t tries, mbw_stream_t stream);
 
 /* Host-side fault injection (test hook). The next `count` calls on the
  * calling thread that pass their argument checks and would launch a kernel
- * (the GEMV/GEMM entry points, mbw_repack_int4, mbw_quantize_int8_pc and the
- * dequant helpers) launch nothing and return MBW_ERR_CUDA, as a failed launch
+ * (the GEMV/GEMM entry points, mbw_repack_int4, mbw_quantize_int8_pc, the
+ * dequant helpers, the mbw_kv4_* calls and mbw_token_logprobs) launch nothing and return MBW_ERR_CUDA, as a failed launch
  * would, with mbw_last_error() naming the injection. count = 0 (the default)
  * turns it off; a negative count is MBW_ERR_INVALID_ARG. */
 mbw_status mbw_inject_launch_failures(int count);

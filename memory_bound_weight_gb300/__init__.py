@@ -1,6 +1,7 @@
 """GB300 (sm_103a) weight-streaming GEMV library: y = W.x and Y = X.W^T with
 BF16, INT4 group-64, AWQ-style INT4 group-128 and symmetric per-channel INT8
-weights.
+weights; and, around these products in a decode step, a 4-bit paged key/value
+cache with its attention, and the log probabilities of tokens.
 
 The compute path is libmbw.so (C ABI in include/mbw.h); this package is its
 binding. Submodules ``inputs`` and ``workloads`` (synthetic data and byte
@@ -13,6 +14,8 @@ _EXPORTS = (
     "launch_count", "check_device_error", "selftest_wait_expiry", "inject_launch_failures", "output_fp32", "MbwError",
     "OP_GEMV_BF16", "OP_GEMV_INT4_G64", "OP_GEMV_INT4_AWQ_G128", "OP_GEMM_SKINNY_BF16",
     "OP_GEMV_INT8_PC",
+    "Kv4Cache", "kv4_page_bytes", "kv4_append", "kv4_gather", "kv4_attention", "kv4_attention_workspace",
+    "token_logprobs", "token_logprobs_workspace", "TokenLogprobs",
 )
 
 
@@ -24,6 +27,10 @@ def __getattr__(name):
         from . import _binding
 
         return getattr(_binding, name)
+    if name == "rope_table":
+        from .rope import rope_table
+
+        return rope_table
     if name in _PLAN_FILES:
         from . import plans
 

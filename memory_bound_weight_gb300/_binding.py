@@ -6,6 +6,7 @@ If the library is missing the calls raise; there is no fallback path.
 """
 from __future__ import annotations
 
+import collections
 import contextlib
 import ctypes
 import os
@@ -27,6 +28,7 @@ REPACKED = 0x800
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _ST = ctypes.c_int
 
@@ -38,6 +40,19 @@ class MbwFusion(ctypes.Structure):
     """struct mbw_fusion of include/mbw.h."""
     _fields_ = [("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float), ("residual", ctypes.c_void_p),
                 ("up_weights", ctypes.c_void_p), ("up_scales", ctypes.c_void_p), ("up_zeros", ctypes.c_void_p)]
+
+
+class MbwKv4Cache(ctypes.Structure):
+    """struct mbw_kv4_cache of include/mbw.h."""
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class MbwRope(ctypes.Structure):
+    """struct mbw_rope of include/mbw.h."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p)]
+
 
 # name -> (argtypes, restype)
 SIGNATURES = {
@@ -52,6 +67,15 @@ SIGNATURES = {
     "gemv_fused": ([ctypes.c_int, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.POINTER(MbwFusion), _P, _SZ, _P], _ST),
     "gemv_fused_awq_g128": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.POINTER(MbwFusion), _P, _SZ,
                              _P], _ST),
+    "mbw_kv4_page_bytes": ([_I32, _I32, _I32, _I32], _SZ),
+    "mbw_kv4_append": ([_P, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _I64, _P], _ST),
+    "mbw_kv4_gather": ([_P, _P, _P, _P, _I64, _P], _ST),
+    "mbw_kv4_attention": ([_P, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, ctypes.c_float, _I64,
+                           _P, _SZ, _P], _ST),
+    "mbw_kv4_attention_workspace_bytes": ([_I32], _SZ),
+    "mbw_token_logprobs": ([_P, ctypes.c_int, _I64, _P, _I64, _I64, ctypes.c_float, _I32, _P, _P, _P, _P, _P, _P, _SZ,
+                            _P], _ST),
+    "mbw_token_logprobs_workspace_bytes": ([], _SZ),
     "mbw_workspace_bytes": ([ctypes.c_int, _I64, _I64, _I64], _SZ),
     "mbw_dequant_int4_g64": ([_P, _P, _P, _I64, _I64, _P], _ST),
     "mbw_dequant_int4_awq_g128": ([_P, _P, _P, _P, _I64, _I64, _P], _ST),
@@ -446,6 +470,195 @@ def dequant_int4_awq_g128(Wq, scales, zeros):
     check("mbw_dequant_int4_awq_g128", lib().mbw_dequant_int4_awq_g128(
         Wq.data_ptr(), scales.data_ptr(), zeros.data_ptr(), out.data_ptr(), N, K, _stream_ptr(Wq.device)))
     return out
+
+
+class Kv4Cache:
+    """4-bit paged key/value cache over `pages`, a contiguous uint8 tensor (num_pages,
+    kv4_page_bytes(page_size, kv_heads, head_dim, group)) that the caller owns."""
+
+    __slots__ = ("pages", "kv_heads", "head_dim", "page_size", "group", "_c")
+
+    def __init__(self, pages, kv_heads, head_dim, page_size=16, group=64):
+        torch = _torch()
+        _need(pages, "pages", torch.uint8, 2)
+        size = kv4_page_bytes(page_size, kv_heads, head_dim, group)
+        if pages.shape[1] != size:
+            raise ValueError(f"pages must have {size} bytes per page, got {pages.shape[1]}")
+        self.pages, self.kv_heads, self.head_dim, self.page_size, self.group = pages, kv_heads, head_dim, page_size, group
+        self._c = MbwKv4Cache(pages.data_ptr(), pages.shape[0], page_size, kv_heads, head_dim, group)
+
+
+def kv4_page_bytes(page_size, kv_heads, head_dim, group=64):
+    """Bytes of one page of a Kv4Cache (page_size a multiple of 16 up to 1024, head_dim 64, 128 or 256, group 32 or 64)."""
+    if (page_size % 16 or not 16 <= page_size <= 1024 or not 1 <= kv_heads <= 1024 or head_dim not in (64, 128, 256)
+            or group not in (32, 64)):
+        raise ValueError("page_size must be a multiple of 16 up to 1024, head_dim 64, 128 or 256, group 32 or 64, "
+                         "kv_heads 1 to 1024")
+    return kv_heads * (page_size // 16) * (16 * head_dim + 128 * (head_dim // group))
+
+
+def _need_rows(t, name, heads, dim):
+    """bf16 (T, heads, dim), possibly rows of a wider matrix; returns the row stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+        raise ValueError(f"{name} must have shape (T, {'heads' if heads is None else heads}, {dim}), got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (t.shape[1] > 1 and st[1] != dim):
+        raise ValueError(f"{name} must have contiguous rows of heads")
+    return st[0] if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def kv4_append(cache, k, v, slots, q=None, positions=None, cos_sin=None, interleaved=False, q_out=None):
+    """Rotate T tokens' queries and keys by their position and store keys and values in the cache.
+    k, v bf16 (T, kv_heads, head_dim), q bf16 (T, q_heads, head_dim) or None, each possibly a part of a
+    wider QKV output; slots int64 (T,), page * page_size + place in the page, negative: not stored.
+    positions int32 (T,) and cos_sin fp32 (max_pos, rotary_dim) (see rope_table) together, or neither:
+    no rotation. Returns the rotated queries (`q_out`, which may be q, or a new tensor), None without q."""
+    torch = _torch()
+    hk, d = cache.kv_heads, cache.head_dim
+    ks, vs = _need_rows(k, "k", hk, d), _need_rows(v, "v", hk, d)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of tokens")
+    _need(slots, "slots", torch.int64, 1)
+    _need_shape(slots, "slots", (T,))
+    qp = op = None
+    qs = os_ = hq = 0
+    if q is not None:
+        qs, hq = _need_rows(q, "q", None, d), q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError("q and k must have the same number of tokens")
+        if q_out is None:
+            q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+            os_ = hq * d
+        else:
+            os_ = _need_rows(q_out, "q_out", hq, d)
+            if q_out.shape[0] != T:
+                raise ValueError("q_out and q must have the same number of tokens")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rope = None
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("positions and cos_sin go together")
+    if positions is not None:
+        _need(positions, "positions", torch.int32, 1)
+        _need_shape(positions, "positions", (T,))
+        _need(cos_sin, "cos_sin", torch.float32, 2)
+        rope = ctypes.byref(MbwRope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
+                                    positions.data_ptr()))
+    _on_current_device(cache.pages, k, v, slots, q, q_out, positions, cos_sin)
+    check("mbw_kv4_append", lib().mbw_kv4_append(ctypes.byref(cache._c), k.data_ptr(), ks, v.data_ptr(), vs,
+                                                 slots.data_ptr(), qp, qs, op, os_, hq, rope, T,
+                                                 _stream_ptr(k.device)))
+    return q_out
+
+
+def kv4_gather(cache, slots):
+    """The keys and values the cache holds at `slots` int64 (T,), each bf16 (T, kv_heads, head_dim); zeros for a
+    negative slot."""
+    torch = _torch()
+    _need(slots, "slots", torch.int64, 1)
+    _on_current_device(cache.pages, slots)
+    shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    check("mbw_kv4_gather", lib().mbw_kv4_gather(ctypes.byref(cache._c), slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                                 shape[0], _stream_ptr(slots.device)))
+    return k, v
+
+
+def kv4_attention_workspace(head_dim, device="cuda"):
+    """A workspace for kv4_attention (zero, as it has to be before its first use); one per stream."""
+    torch = _torch()
+    return torch.zeros(int(lib().mbw_kv4_attention_workspace_bytes(head_dim)), dtype=torch.uint8, device=device)
+
+
+def kv4_attention(cache, q, block_table, ctx_lens, q_starts=None, scale=None, window=0, out=None, return_lse=False,
+                  workspace=None):
+    """Attention of q bf16 (T, q_heads, head_dim), possibly a part of a wider matrix, over the cache.
+    block_table int32 (B, width): each request's pages; ctx_lens int32 (B,): its tokens in the cache, the
+    queries' own among them; q_starts int32 (B + 1,): where its queries begin in q, or None: T / B each.
+    A query sees the keys up to its own position, with `window` > 0 only that many. scale: head_dim ** -0.5
+    by default. Returns out (T, q_heads, head_dim), with return_lse also fp32 (T, q_heads). workspace: from
+    kv4_attention_workspace; without one, long contexts are not split and take longer."""
+    torch = _torch()
+    d = cache.head_dim
+    qs, (T, hq) = _need_rows(q, "q", None, d), q.shape[:2]
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(ctx_lens, "ctx_lens", torch.int32, 1)
+    B, width = block_table.shape
+    _need_shape(ctx_lens, "ctx_lens", (B,))
+    if q_starts is not None:
+        _need(q_starts, "q_starts", torch.int32, 1)
+        _need_shape(q_starts, "q_starts", (B + 1,))
+    if out is None or _out_dtype() != torch.bfloat16:
+        out = _alloc_out((T, hq, d), q, out)
+        os_ = hq * d
+    else:
+        os_ = _need_rows(out, "out", hq, d)
+        if out.shape[0] != T:
+            raise ValueError("out and q must have the same number of tokens")
+    lse = torch.empty((T, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    _on_current_device(cache.pages, q, block_table, ctx_lens, q_starts, out, workspace)
+    wp, wn = _ws(workspace)
+    check("mbw_kv4_attention", lib().mbw_kv4_attention(
+        ctypes.byref(cache._c), q.data_ptr(), qs, out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
+        block_table.data_ptr(), width, width, ctx_lens.data_ptr(), None if q_starts is None else q_starts.data_ptr(), B, T,
+        hq, d ** -0.5 if scale is None else scale, window, wp, wn, _stream_ptr(q.device)))
+    return (out, lse) if return_lse else out
+
+
+TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprob rank entropy top_ids top_logprobs")
+
+
+def token_logprobs_workspace(device="cuda"):
+    """A workspace for token_logprobs (zero, as it has to be before its first use); one per stream."""
+    torch = _torch()
+    return torch.zeros(int(lib().mbw_token_logprobs_workspace_bytes()), dtype=torch.uint8, device=device)
+
+
+def token_logprobs(logits, targets=None, top_k=0, scale=1.0, workspace=None):
+    """What logits bf16 or fp32 (M, V) (rows may be apart) say about tokens, over scale * logits: the log
+    probability fp32 (M,) and rank int32 (M,) of targets int32 (M,) (None without), the entropy fp32 (M,) in
+    nats, the top_k (<= 32) most likely ids int32 (M, top_k) and their log probabilities fp32 (M, top_k).
+    workspace: from token_logprobs_workspace; without one, few rows take longer."""
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"logits must be {torch.bfloat16} or {torch.float32}, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must have 2 dimensions and contiguous rows")
+    M, V = logits.shape
+    dev = logits.device
+    lp = rank = None
+    if targets is not None:
+        _need(targets, "targets", torch.int32, 1)
+        _need_shape(targets, "targets", (M,))
+        lp = torch.empty(M, dtype=torch.float32, device=dev)
+        rank = torch.empty(M, dtype=torch.int32, device=dev)
+    ent = torch.empty(M, dtype=torch.float32, device=dev)
+    if not 0 <= top_k <= 32:
+        raise ValueError("top_k must be 0 to 32")
+    ids = torch.empty((M, top_k), dtype=torch.int32, device=dev)
+    tlp = torch.empty((M, top_k), dtype=torch.float32, device=dev)
+    _on_current_device(logits, targets, workspace)
+    wp, wn = _ws(workspace)
+    check("mbw_token_logprobs", lib().mbw_token_logprobs(
+        logits.data_ptr(), int(logits.dtype == torch.float32), logits.stride(0) if M > 1 else V,
+        None if targets is None else targets.data_ptr(), M, V, scale, top_k, None if lp is None else lp.data_ptr(),
+        None if rank is None else rank.data_ptr(), ent.data_ptr(), ids.data_ptr(), tlp.data_ptr(), wp, wn,
+        _stream_ptr(dev)))
+    return TokenLogprobs(lp, rank, ent, ids, tlp)
 
 
 def autotune(op: int, M: int, N: int, K: int) -> None:

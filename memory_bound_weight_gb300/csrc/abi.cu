@@ -126,6 +126,17 @@ static mbw_status awq_call(const char* fn, int op, const uint8_t* Wq, const void
     return run_simt(FMT_AWQ, op, Wq, (const uint16_t*)scales, zeros, (const uint16_t*)X, Y, M, N, K, stream);
 }
 
+// The sizes of a 4-bit cache (its pages' pointer is checked by the calls that use it).
+static mbw_status check_cache(const char* fn, const mbw_kv4_cache* c) {
+    if (!c) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL cache");
+    if (mbw_kv4_page_bytes(c->page_size, c->kv_heads, c->head_dim, c->group) == 0)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": page_size must be a multiple of 16 up to 1024, head_dim 64, "
+                                                         "128 or 256, group 32 or 64, kv_heads 1 to 1024");
+    if (c->num_pages < 1) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": num_pages must be positive");
+    if (c->num_pages > MBW_MAX_DIM) return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": at most MBW_MAX_DIM pages");
+    return MBW_OK;
+}
+
 }  // namespace mbw
 
 using namespace mbw;
@@ -335,6 +346,209 @@ mbw_status gemm_skinny_bf16(const void* X, const void* W, void* Y, int64_t M, in
                     M, N, K, (cudaStream_t)stream);
 }
 
+size_t mbw_kv4_page_bytes(int32_t page_size, int32_t kv_heads, int32_t head_dim, int32_t group) {
+    if (page_size < 16 || page_size > 1024 || page_size % 16 != 0 || kv_heads < 1 || kv_heads > 1024) return 0;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || (group != 32 && group != 64)) return 0;
+    return (size_t)kv_heads * (size_t)(page_size / 16) * (size_t)(16 * head_dim + 128 * (head_dim / group));
+}
+
+mbw_status mbw_kv4_append(const mbw_kv4_cache* cache, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int64_t* slots, const void* q, int64_t q_stride, void* q_out,
+                          int64_t q_out_stride, int64_t q_heads, const mbw_rope* rope, int64_t T,
+                          mbw_stream_t stream) {
+    const char* fn = "mbw_kv4_append";
+    mbw_status st = check_cache(fn, cache);
+    if (st != MBW_OK) return st;
+    if (T < 0 || q_heads < 0) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+    if (T > MBW_MAX_DIM || q_heads > 65536)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": at most MBW_MAX_DIM tokens and 65536 query heads");
+    if (T == 0) return MBW_OK;
+    if (!cache->pages || !k || !v || !slots || (q_heads > 0 && (!q || !q_out)))
+        return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    const int64_t kvw = (int64_t)cache->kv_heads * cache->head_dim, qw = q_heads * cache->head_dim;
+    if (k_stride < kvw || v_stride < kvw || (q_heads > 0 && (q_stride < qw || q_out_stride < qw)))
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": a row stride is shorter than the row");
+    if (!aligned(cache->pages, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || k_stride % 8 ||
+        v_stride % 8 || (q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || q_stride % 8 || q_out_stride % 8)))
+        return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": pages, k, v, q and q_out must be 16-byte aligned, slots "
+                                                          "8-byte, strides multiples of 8 elements");
+    Kv4AppendArgs a{};
+    if (rope) {
+        if (!rope->cos_sin || !rope->positions)
+            return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": rope without cos_sin or positions");
+        if (rope->interleaved != 0 && rope->interleaved != 1)
+            return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": interleaved must be 0 or 1");
+        if (rope->max_pos < 1) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": max_pos must be positive");
+        if (rope->rotary_dim < 16 || rope->rotary_dim % 16 != 0 || rope->rotary_dim > cache->head_dim)
+            return fail(MBW_ERR_BAD_SHAPE,
+                        std::string(fn) + ": rotary_dim must be a multiple of 16, at most head_dim");
+        if (!aligned(rope->cos_sin, 16) || !aligned(rope->positions, 4))
+            return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": cos_sin must be 16-byte aligned, positions 4-byte");
+        a.cos_sin = rope->cos_sin;
+        a.positions = rope->positions;
+        a.max_pos = rope->max_pos;
+        a.rotary = rope->rotary_dim;
+        a.interleaved = rope->interleaved;
+    }
+    a.pages = static_cast<uint8_t*>(cache->pages);
+    a.num_slots = cache->num_pages * cache->page_size;
+    a.page_size = cache->page_size;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.group = cache->group;
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.q_heads = (int)q_heads;
+    a.slots = slots;
+    a.T = T;
+    if (take_injected_failure("append launch")) return MBW_ERR_CUDA;
+    cudaError_t e = launch_kv4_append(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MBW_OK : cuda_fail(e, "append launch");
+}
+
+mbw_status mbw_kv4_gather(const mbw_kv4_cache* cache, const int64_t* slots, void* k, void* v, int64_t T,
+                          mbw_stream_t stream) {
+    const char* fn = "mbw_kv4_gather";
+    mbw_status st = check_cache(fn, cache);
+    if (st != MBW_OK) return st;
+    if (T < 0) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+    if (T > MBW_MAX_DIM) return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": at most MBW_MAX_DIM tokens");
+    if (T == 0) return MBW_OK;
+    if (!cache->pages || !slots || !k || !v) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    if (!aligned(cache->pages, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))
+        return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": pages, k and v must be 16-byte aligned, slots 8-byte");
+    Kv4GatherArgs a{};
+    a.pages = static_cast<const uint8_t*>(cache->pages);
+    a.num_slots = cache->num_pages * cache->page_size;
+    a.page_size = cache->page_size;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.group = cache->group;
+    a.slots = slots;
+    a.k = static_cast<uint16_t*>(k);
+    a.v = static_cast<uint16_t*>(v);
+    a.T = T;
+    if (take_injected_failure("gather launch")) return MBW_ERR_CUDA;
+    cudaError_t e = launch_kv4_gather(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MBW_OK : cuda_fail(e, "gather launch");
+}
+
+size_t mbw_kv4_attention_workspace_bytes(int32_t head_dim) {
+    return (head_dim == 64 || head_dim == 128 || head_dim == 256) ? kv4_attention_workspace(head_dim) : 0;
+}
+
+mbw_status mbw_kv4_attention(const mbw_kv4_cache* cache, const void* q, int64_t q_stride, void* out,
+                             int64_t out_stride, float* lse, const int32_t* block_table, int64_t table_stride,
+                             int64_t table_width, const int32_t* ctx_lens, const int32_t* q_starts, int64_t B,
+                             int64_t T, int64_t q_heads, float scale, int64_t window, void* workspace,
+                             size_t ws_bytes, mbw_stream_t stream) {
+    const char* fn = "mbw_kv4_attention";
+    mbw_status st = check_cache(fn, cache);
+    if (st != MBW_OK) return st;
+    if (B < 0 || T < 0 || table_stride < 0 || table_width < 0 || window < 0)
+        return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+    if (q_heads < 1 || q_heads % cache->kv_heads != 0)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": q_heads must be a positive multiple of kv_heads");
+    if (B > (1 << 20) || T > MBW_MAX_DIM || q_heads > 65536 || T * q_heads > MBW_MAX_DIM)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": at most 2^20 requests and MBW_MAX_DIM query rows");
+    if (table_width * cache->page_size > MBW_MAX_DIM)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": at most MBW_MAX_DIM tokens per request");
+    if (T == 0) return MBW_OK;
+    if (B == 0) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": queries of no request");
+    if (!q_starts && T % B != 0)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": without q_starts T must be a multiple of B");
+    if (!cache->pages || !q || !out || !ctx_lens || (table_width > 0 && !block_table))
+        return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f)
+        return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": scale must be finite");
+    const int64_t qw = q_heads * cache->head_dim;
+    if (q_stride < qw || out_stride < qw)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": a row stride is shorter than the row");
+    if (B > 1 && table_stride < table_width)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": table_stride is shorter than table_width");
+    if (!aligned(cache->pages, 16) || !aligned(q, 16) || !aligned(out, 16) || q_stride % 8 || out_stride % 8 ||
+        !aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(q_starts, 4) || !aligned(lse, 4) ||
+        !aligned(workspace, 16))
+        return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": pages, q, out and workspace must be 16-byte aligned, "
+                                                          "strides multiples of 8 elements, the rest 4-byte");
+    Kv4AttnArgs a{};
+    a.pages = static_cast<const uint8_t*>(cache->pages);
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.group = cache->group;
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_stride = q_stride;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.lse = lse;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.table_width = (int)table_width;
+    a.ctx_lens = ctx_lens;
+    a.q_starts = q_starts;
+    a.B = (int)B;
+    a.T = (int)T;
+    a.q_heads = (int)q_heads;
+    a.scale = scale;
+    a.window = (int)(window < MBW_MAX_DIM ? window : 0);  // no context is longer
+    a.out_f32 = g_out_f32;
+    a.workspace = workspace;
+    a.ws_bytes = workspace ? ws_bytes : 0;
+    if (take_injected_failure("attention launch")) return MBW_ERR_CUDA;
+    cudaError_t e = launch_kv4_attention(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MBW_OK : cuda_fail(e, "attention launch");
+}
+
+size_t mbw_token_logprobs_workspace_bytes(void) { return token_logprobs_workspace(); }
+
+mbw_status mbw_token_logprobs(const void* logits, int fp32, int64_t row_stride, const int32_t* targets, int64_t M,
+                              int64_t V, float scale, int32_t top_k, float* logprob, int32_t* rank, float* entropy,
+                              int32_t* top_ids, float* top_logprobs, void* workspace, size_t ws_bytes,
+                              mbw_stream_t stream) {
+    const char* fn = "mbw_token_logprobs";
+    if (M < 0 || V < 0 || top_k < 0) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": negative size");
+    if (fp32 != 0 && fp32 != 1) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": fp32 must be 0 or 1");
+    if (M > MBW_MAX_DIM || V > MBW_MAX_DIM)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": M and V must be at most MBW_MAX_DIM");
+    if (top_k > 32) return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": top_k must be at most 32");
+    if (!(scale > 0.f) || scale > 3.0e38f)
+        return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": scale must be positive and finite");
+    if (M == 0) return MBW_OK;
+    if (V == 0) return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": V must be positive");
+    if (row_stride < V) return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": row_stride is shorter than the row");
+    if (!logits) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    if (!aligned(logits, fp32 ? 4 : 2) || !aligned(targets, 4) || !aligned(logprob, 4) || !aligned(rank, 4) ||
+        !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4) || !aligned(workspace, 16))
+        return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": workspace must be 16-byte aligned, the rest element-wise");
+    LogprobArgs a{};
+    a.logits = logits;
+    a.fp32 = fp32;
+    a.row_stride = row_stride;
+    a.targets = targets;
+    a.M = M;
+    a.V = V;
+    a.scale = scale;
+    a.top_k = (top_ids || top_logprobs) ? top_k : 0;
+    a.logprob = logprob;
+    a.rank = rank;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.workspace = workspace;
+    a.ws_bytes = workspace ? ws_bytes : 0;
+    if (take_injected_failure("logprobs launch")) return MBW_ERR_CUDA;
+    cudaError_t e = launch_token_logprobs(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MBW_OK : cuda_fail(e, "logprobs launch");
+}
+
 size_t mbw_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
     (void)op;
     (void)M;
@@ -380,8 +594,13 @@ mbw_status mbw_check_device_error(void) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     const int f = tma_take_fault();
     const int f2 = tc_take_fault();
-    if (f < 0 || f2 < 0) return cuda_fail(cudaGetLastError(), "reading the device fault flag");
+    const int r = kv4_cache_take_range(), r2 = kv4_attn_take_range(), r3 = logprobs_take_range();
+    if (f < 0 || f2 < 0 || r < 0 || r2 < 0 || r3 < 0)
+        return cuda_fail(cudaGetLastError(), "reading the device fault flag");
     if (f || f2) return fail(MBW_ERR_DEVICE_TIMEOUT, "a bounded wait inside a kernel expired");
+    if (r) return fail(MBW_ERR_DEVICE_RANGE, "a cache slot or position was out of range");
+    if (r2) return fail(MBW_ERR_DEVICE_RANGE, "a page id, context length or query offset was out of range");
+    if (r3) return fail(MBW_ERR_DEVICE_RANGE, "a target token id was out of range");
     return MBW_OK;
 }
 
@@ -412,6 +631,7 @@ const char* mbw_status_string(mbw_status s) {
         case MBW_ERR_UNSUPPORTED: return "MBW_ERR_UNSUPPORTED";
         case MBW_ERR_CUDA: return "MBW_ERR_CUDA";
         case MBW_ERR_DEVICE_TIMEOUT: return "MBW_ERR_DEVICE_TIMEOUT";
+        case MBW_ERR_DEVICE_RANGE: return "MBW_ERR_DEVICE_RANGE";
         default: return "MBW_ERR_UNKNOWN";
     }
 }

@@ -238,6 +238,82 @@ cudaError_t launch_quantize_int8_pc(const uint16_t* W, int8_t* Wq, float* scales
 // Load-time INT4 repack (quantize.cu): N x K/8 words, in place allowed.
 cudaError_t launch_repack_int4(const uint8_t* Wq, uint8_t* Wr, int64_t N, int64_t K, cudaStream_t s);
 
+// 4-bit paged key/value cache (kv4_cache.cu, kv4_attention.cu; layout in kv4.cuh).
+struct Kv4AppendArgs {
+    uint8_t* pages;
+    int64_t num_slots;  // num_pages * page_size
+    int page_size, kv_heads, head_dim, group;
+    const uint16_t* k;  // bf16 [T] rows of kv_heads * head_dim, row strides in elements
+    const uint16_t* v;
+    const uint16_t* q;  // bf16 [T] rows of q_heads * head_dim, or NULL with q_heads = 0
+    uint16_t* q_out;
+    int64_t k_stride, v_stride, q_stride, q_out_stride;
+    int q_heads;
+    const int64_t* slots;    // [T], negative: not stored
+    const float* cos_sin;    // [max_pos][rotary]: rotary / 2 cosines, then the sines; NULL: no rotation
+    const int32_t* positions;  // [T]
+    int64_t max_pos;
+    int rotary, interleaved;
+    int64_t T;
+};
+struct Kv4GatherArgs {
+    const uint8_t* pages;
+    int64_t num_slots;
+    int page_size, kv_heads, head_dim, group;
+    const int64_t* slots;
+    uint16_t* k;  // bf16 [T][kv_heads][head_dim]
+    uint16_t* v;
+    int64_t T;
+};
+struct Kv4AttnArgs {
+    const uint8_t* pages;
+    int64_t num_pages;
+    int page_size, kv_heads, head_dim, group;
+    const uint16_t* q;  // bf16 [T] rows of q_heads * head_dim
+    int64_t q_stride;
+    void* out;  // bf16 or fp32 [T] rows of q_heads * head_dim
+    int64_t out_stride;
+    float* lse;  // [T][q_heads] or NULL
+    const int32_t* table;  // [B] rows of page ids
+    int64_t table_stride;
+    int table_width;
+    const int32_t* ctx_lens;  // [B]
+    const int32_t* q_starts;  // [B + 1] or NULL (T / B queries each)
+    int B, T, q_heads;
+    float scale;
+    int window;  // 0: none
+    int out_f32;
+    void* workspace;
+    size_t ws_bytes;
+};
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
+cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
+cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s);
+size_t kv4_attention_workspace(int head_dim);
+int kv4_cache_take_range();  // 1 if a slot or position was out of range since the last call (and clear it)
+int kv4_attn_take_range();
+
+// Log probabilities of tokens (logprobs.cu).
+struct LogprobArgs {
+    const void* logits;  // bf16 or fp32 [M] rows of V
+    int fp32;
+    int64_t row_stride;
+    const int32_t* targets;  // [M] or NULL
+    int64_t M, V;
+    float scale;
+    int top_k;
+    float* logprob;  // each output may be NULL
+    int32_t* rank;
+    float* entropy;
+    int32_t* top_ids;      // [M][top_k]
+    float* top_logprobs;
+    void* workspace;
+    size_t ws_bytes;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t s);
+size_t token_logprobs_workspace();
+int logprobs_take_range();
+
 // Plan cache (plan.cu).
 Plan plan_lookup(int op, int64_t M, int64_t N, int64_t K, cudaStream_t s);
 Plan plan_default(int op, int64_t M, int64_t N, int64_t K);
