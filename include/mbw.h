@@ -376,7 +376,7 @@ mbw_status mbw_kv4_gather(const mbw_kv4_cache *cache, const int64_t *slots, void
  * not enter, whatever they hold.
  * workspace: mbw_kv4_attention_workspace_bytes() bytes, zero before its first
  * use and left so by every call (one workspace per stream). Smaller or NULL:
- * long contexts are split over fewer CTAs, or none, and take longer.
+ * contexts are not split over CTAs, and long ones take longer.
  * A page id or length out of range is reported by mbw_check_device_error
  * (MBW_ERR_DEVICE_RANGE); that request's output is then unspecified.
  */
