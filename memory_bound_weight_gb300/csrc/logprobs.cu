@@ -11,8 +11,16 @@
 // probability 0; a row of them alone has log probabilities of minus infinity
 // and entropy 0. A NaN or plus infinity makes the row's numbers NaN.
 //
-// One CTA per row; one pass for the maximum, one for the sums and the rank,
-// one per top token.
+// One read of the logits. A row is cut into pieces, one CTA each, where there
+// are few rows. A warp keeps one maximum for all its lanes, so that its common
+// path is, per 16-byte load, one vote and the sums: 6.5 instructions per logit,
+// two of them on the special-function pipe or its neighbours (the exponential
+// alone takes 73% of that pipe at the copy bandwidth, with 16-bit logits). The
+// rare path, taken when a logit passes the warp's gate, moves the maximum and
+// inserts into the warp's list of top tokens, one entry per lane. The gate is
+// the k-th best so far, of the CTA, so it is passed some k ln(n) times. Lists
+// are joined by counting, for each entry, the better ones. Pieces of a row meet
+// in the workspace; the CTA that arrives last joins them in their order.
 #include <cuda_runtime.h>
 
 #include <math_constants.h>
@@ -26,7 +34,11 @@ namespace {
 
 __device__ int g_logprobs_range;  // a target was not below V
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxTop = 32;        // a warp's list is one entry per lane
+constexpr int kPieces = 8192;      // pieces that the workspace holds
+constexpr int kMaxSplit = 256;     // pieces of a row, one per thread of the CTA that joins them
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct Cand {  // a logit and its index; better: larger, then the lower index
     float x;
@@ -34,105 +46,447 @@ struct Cand {  // a logit and its index; better: larger, then the lower index
 };
 __device__ __forceinline__ bool better(float x, int i, float y, int j) { return x > y || (x == y && i < j); }
 
-__device__ Cand block_best(Cand c, Cand* sm) {
-    for (int o = 16; o > 0; o >>= 1) {
-        const float x = __shfl_xor_sync(0xFFFFFFFFu, c.x, o);
-        const int i = __shfl_xor_sync(0xFFFFFFFFu, c.i, o);
-        if (better(x, i, c.x, c.i)) c.x = x, c.i = i;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = c;
-    __syncthreads();
-    c = sm[0];
-    for (int w = 1; w < kThreads / 32; ++w)
-        if (better(sm[w].x, sm[w].i, c.x, c.i)) c = sm[w];
-    return c;
-}
+struct Stats {  // of some of a row's logits, in powers of two of (x - x_best) * scale
+    float best;  // the largest, minus infinity where there is none
+    int best_i;
+    float s, t;  // sum of e and of e log2 e over the others
+    int before;  // logits ahead of the target
+};
+struct __align__(16) Piece {
+    Stats st;
+    Cand top[kMaxTop];
+};
 
-template <typename T>
-__device__ T block_sum(T v, T* sm) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-    for (int w = 0; w < kThreads / 32; ++w) v += sm[w];
-    return v;
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
 
 __device__ __forceinline__ float logit(const uint16_t* p, int64_t i) { return bf16lo_to_f32(p[i]); }
 __device__ __forceinline__ float logit(const float* p, int64_t i) { return p[i]; }
 
+// What the kernel does with the 16 bytes of a load, by type: the logits, the largest (a NaN is passed over), how many
+// are above a threshold, and bits of all minus infinity.
+struct Bf16Load {
+    static constexpr int E = 8;
+    static constexpr uint32_t kNone = 0xFF80FF80u;
+    static __device__ __forceinline__ void spread(uint4 v, float* x) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo_to_f32(w[i]), x[2 * i + 1] = bf16hi_to_f32(w[i]);
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float largest(uint4 v, const float*) {
+        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+        return fmaxf(bf16lo_to_f32(m), bf16hi_to_f32(m));
+    }
+    static __device__ __forceinline__ uint32_t above2(uint32_t a, uint32_t b) {  // 1 or 0 in bf16
+        uint32_t r;
+        asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float2 above(uint4 v, const float*, uint32_t thr) {
+        const uint32_t n = add(add(above2(v.x, thr), above2(v.y, thr)), add(above2(v.z, thr), above2(v.w, thr)));
+        return make_float2(bf16lo_to_f32(n), bf16hi_to_f32(n));
+    }
+    static __device__ __forceinline__ uint32_t threshold(uint16_t x) { return x | (uint32_t)x << 16; }
+    // the threshold that everything not below x is above (x finite or plus infinity)
+    static __device__ __forceinline__ uint32_t threshold_below(uint16_t x) {
+        return threshold((x & 0x7FFF) == 0 ? 0x8001 : x & 0x8000 ? x + 1 : x - 1);
+    }
+};
+struct F32Load {
+    static constexpr int E = 4;
+    static constexpr uint32_t kNone = 0xFF800000u;
+    static __device__ __forceinline__ void spread(uint4 v, float* x) {
+        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ float largest(uint4, const float* x) {
+        return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    }
+    static __device__ __forceinline__ float above1(float a, float b) {
+        float r;
+        asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float2 above(uint4, const float* x, uint32_t thr) {
+        const float t = __uint_as_float(thr);
+        return add2(make_float2(above1(x[0], t), above1(x[1], t)), make_float2(above1(x[2], t), above1(x[3], t)));
+    }
+    static __device__ __forceinline__ uint32_t threshold(float x) { return __float_as_uint(x); }
+    static __device__ __forceinline__ uint32_t threshold_below(float x) {
+        const uint32_t b = __float_as_uint(x);
+        return x == 0.f ? 0x80000001u : b >> 31 ? b + 1 : b - 1;
+    }
+};
 template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(LogprobArgs a) {
-    __shared__ Cand sc[kThreads / 32];
-    __shared__ float sf[kThreads / 32];
-    __shared__ int si[kThreads / 32];
+struct LoadOf;
+template <>
+struct LoadOf<uint16_t> { using type = Bf16Load; };
+template <>
+struct LoadOf<float> { using type = F32Load; };
+
+// b behind a: the sums taken to the larger maximum, the smaller one's term added.
+__device__ __forceinline__ void merge(Stats& a, const Stats& b, float c2) {
+    const bool swap = better(b.best, b.best_i, a.best, a.best_i);
+    const float hi = swap ? b.best : a.best, lo = swap ? a.best : b.best;
+    const float s_hi = swap ? b.s : a.s, t_hi = swap ? b.t : a.t, s_lo = swap ? a.s : b.s, t_lo = swap ? a.t : b.t;
+    const bool none = lo == -CUDART_INF_F;
+    const float d = none ? 0.f : max_nan((lo - hi) * c2, -1000.f), f = none ? 0.f : exp2_fast(d);
+    if (swap) a.best = b.best, a.best_i = b.best_i;
+    a.s = s_hi + f * (s_lo + 1.f);
+    a.t = t_hi + f * (t_lo + d * s_lo + d);
+    a.before += b.before;
+}
+
+// Rank of candidate j of n in shared memory: how many are better. Ties cannot be: indexes differ.
+__device__ __forceinline__ int place(const Cand* c, int n, Cand x) {
+    int r = 0;
+    for (int j = 0; j < n; ++j) r += better(c[j].x, c[j].i, x.x, x.i);
+    return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs a, int split) {
+    using L = typename LoadOf<T>::type;
+    constexpr int E = L::E, AHEAD = 4;  // loads of a thread in flight
+    __shared__ Stats sm_stats[kWarps];
+    __shared__ Cand sm_cand[kMaxTop * kMaxTop];  // the warps' lists; later the entries of a row's pieces that can win
+    __shared__ Cand sm_top[kMaxTop];
+    __shared__ int sm_tau;  // k-th best logit of some warp of the CTA, as an ordered whole number
+    __shared__ Cand sm_bound;    // the K-th best head of a row's pieces
+    __shared__ int sm_n, sm_lists, sm_last, sm_list[kMaxTop];
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t r = blockIdx.x;
-    const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = a.top_k;
+    const unsigned row = blockIdx.x / (unsigned)split, piece = blockIdx.x - row * split;
+    const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
     const int V = (int)a.V;
-    int t = a.targets ? a.targets[r] : -1;
-    if (t >= V) {
-        if (threadIdx.x == 0) atomicExch(&g_logprobs_range, 1);
-        t = -1;
-    }
-    Cand best = {-CUDART_INF_F, 0x7FFFFFFF};
-    float nan = 0.f;
-    for (int i = threadIdx.x; i < V; i += kThreads) {
-        const float v = logit(x, i);
-        if (v != v) nan = v;
-        if (better(v, i, best.x, best.i)) best = {v, i};
-    }
-    best = block_best(best, sc);
-    nan = block_sum(nan, sf);
-    const bool none = best.x == -CUDART_INF_F;
-    const float top = best.x, xt = t >= 0 ? logit(x, t) : 0.f;
-    float s = 0.f, e = 0.f;
-    int before = 0;
-    for (int i = threadIdx.x; i < V; i += kThreads) {
-        const float v = logit(x, i);
-        if (better(v, i, xt, t)) ++before;
-        if (i == best.i || v == -CUDART_INF_F) continue;
-        const float y = (v - top) * a.scale, p = expf(y);
-        if (p > 0.f) s += p, e -= p * y;
-    }
-    s = block_sum(s, sf) + nan + (none ? 0.f : top - top);
-    e = block_sum(e, sf);
-    before = block_sum(before, si);
-    const float lse = log1pf(s);
-    if (threadIdx.x == 0) {
-        if (a.logprob) a.logprob[r] = t < 0 ? 0.f : none ? -CUDART_INF_F + nan : (xt - top) * a.scale - lse;
-        if (a.rank) a.rank[r] = t < 0 ? 0 : 1 + before;
-        if (a.entropy) a.entropy[r] = none ? nan : lse + e / (1.f + s);
-    }
-    for (int k = 0; k < a.top_k; ++k) {
-        if (k > 0) {  // the best one behind the last
-            const Cand last = best;
-            best = {-CUDART_INF_F, 0x7FFFFFFF};
-            for (int i = threadIdx.x; i < V; i += kThreads) {
-                const float v = logit(x, i);
-                if (better(last.x, last.i, v, i) && better(v, i, best.x, best.i)) best = {v, i};
+    const float c2 = a.scale * kLog2e;
+
+    // Loads are of 16 aligned bytes: load v holds the logits v * E - skew ...; those of [full0, full1) lie in the row
+    const int skew = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const uint4* xv = reinterpret_cast<const uint4*>(x - skew);
+    const unsigned loads = ((unsigned)V + skew + E - 1) / E, each = loads / split, rest = loads - each * split;
+    const int v0 = (int)(piece * each + min(piece, rest)), v1 = v0 + (int)(each + (piece < rest));
+    const int full0 = skew ? 1 : 0, full1 = (int)(((unsigned)V + skew) / E), last = min(v1, full1);
+    // Load v; minus infinity past the piece, and for what of the row's first and last 16 bytes is not its own (and is
+    // not read).
+    auto load = [&](int v) {
+        uint4 raw = make_uint4(L::kNone, L::kNone, L::kNone, L::kNone);
+        if (v >= full0 && v < last) {
+            raw = ld_stream16(xv + v);
+        } else if (v < v1) {
+            uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int64_t i = (int64_t)v * E - skew + j;
+                if (i < 0 || i >= V) continue;
+                if (sizeof(T) == 4)
+                    w[j & 3] = __float_as_uint(logit(x, i));
+                else
+                    w[j >> 1] = __byte_perm(w[j >> 1], __float_as_uint(logit(x, i)) >> 16, j & 1 ? 0x5410 : 0x3254);
             }
-            best = block_best(best, sc);
+            raw = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (threadIdx.x == 0) {
-            const bool no = best.x == -CUDART_INF_F;
-            if (a.top_ids) a.top_ids[r * a.top_k + k] = no ? -1 : best.i;
-            if (a.top_logprobs)
-                a.top_logprobs[r * a.top_k + k] = no ? -CUDART_INF_F + nan : (best.x - top) * a.scale - lse;
+        return raw;
+    };
+    uint4 ring[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) ring[u] = load(v0 + u * kThreads + tid);
+    if (tid == 0) sm_tau = INT_MAX, sm_n = 0;
+    __syncthreads();
+
+    int target = a.targets ? a.targets[row] : -1;
+    if (target >= V) {
+        if (tid == 0) atomicExch(&g_logprobs_range, 1);
+        target = -1;
+    }
+    const int tv = target < 0 ? INT_MAX : (int)(((unsigned)target + skew) / E);
+    const float xt = target < 0 ? CUDART_INF_F : logit(x, target);
+    const bool dead = xt == -CUDART_INF_F;  // a masked target: behind all logits of lower index
+    // Ahead of the target are, at lower indexes, the logits not below it, at higher ones those above it; the load that
+    // holds the target counts as one of higher indexes, and is put right at the end. (Of a dead target's lower ones
+    // none is counted: minus infinity plus one bit is a NaN.)
+    const uint32_t after = L::threshold(target < 0 ? T(L::kNone) : x[target]);
+    const uint32_t until = target < 0 ? after : L::threshold_below(x[target]);
+
+    Stats st = {-CUDART_INF_F, INT_MAX, 0.f, 0.f, 0};
+    float2 s2 = make_float2(0.f, 0.f), t2 = s2, n2 = s2;
+    float ref = 0.f;  // what is subtracted: best, 0 while there is none
+    Cand mine = {-CUDART_INF_F, INT_MAX};  // the warp's list, in order: entry `lane`
+    float gate = -CUDART_INF_F;  // no logit up to this one moves the maximum or enters the list
+
+    // Logits as ordered whole numbers (a NaN below all), and back.
+    auto tau_of = [](float v) {  // an ordered whole number, and back
+        const int b = __float_as_int(fmaxf(v, -CUDART_INF_F) + 0.f);  // zeros of both signs tie
+        return b < 0 ? b ^ 0x7FFFFFFF : b;
+    };
+
+    constexpr int kNoTau = (int)0x807FFFFF;  // of minus infinity
+    auto value_of = [](int t) { return __int_as_float(t < 0 ? t ^ 0x7FFFFFFF : t); };
+    // A first gate: each warp holds ceil(K / 8) lanes whose largest logit is at least t, so the least t of the warps is
+    // not above the K-th best logit of the CTA.
+    if (K > 0) {
+        float e[E];
+        L::spread(ring[0], e);
+        int big = tau_of(L::largest(ring[0], e)), t = kNoTau;
+        for (int r = 0; r < (K + kWarps - 1) / kWarps; ++r) {
+            t = __reduce_max_sync(0xFFFFFFFFu, big);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, big == t);
+            if (lane == __ffs(who) - 1) big = kNoTau;
         }
+        if (lane == 0) atomicMin(&sm_tau, t);
+        __syncthreads();
+    }
+
+    // One load of every lane.
+    auto take = [&](int v, uint4 raw) {
+        float e[E];
+        L::spread(raw, e);
+        const int i0 = v * E - skew;
+        const float big = L::largest(raw, e);
+        n2 = add2(n2, L::above(raw, e, v < tv ? until : after));
+        if (__any_sync(0xFFFFFFFFu, big > gate)) {
+            int own = -1;  // the lane's logit that is the maximum
+            if (__any_sync(0xFFFFFFFFu, big > st.best)) {  // ---- the maximum ----
+                const float wm = value_of(__reduce_max_sync(0xFFFFFFFFu, tau_of(big)));
+                int at = INT_MAX;
+#pragma unroll
+                for (int j = E - 1; j >= 0; --j)
+                    if (e[j] == wm) at = i0 + j;
+                at = __reduce_min_sync(0xFFFFFFFFu, at);
+                const bool none = st.best == -CUDART_INF_F;
+                const float d = none ? 0.f : max_nan((st.best - wm) * c2, -1000.f), f = none ? 0.f : exp2_fast(d);
+                // f = 0 keeps a NaN that the sums hold
+                t2 = make_float2(f * (t2.x + d * s2.x), f * (t2.y + d * s2.y));
+                s2 = make_float2(f * s2.x, f * s2.y);
+                if (lane == 0) s2.x += f, t2.x += f * d;
+                st.best = wm, st.best_i = at, ref = wm;
+                own = at - i0;
+            }
+            gate = st.best;
+            if (K > 0) {  // ---- the list ----
+                const float kth = __shfl_sync(0xFFFFFFFFu, mine.x, K - 1);
+                const float floor = value_of(*reinterpret_cast<volatile int*>(&sm_tau));
+                // behind this warp's K-th, or below the gate of all: not among the K best
+                uint32_t has = 0;
+                if (big > kth && big >= floor) {
+#pragma unroll
+                    for (int j = 0; j < E; ++j) has |= (uint32_t)(e[j] > kth && e[j] >= floor) << j;
+                }
+                uint32_t lanes = __ballot_sync(0xFFFFFFFFu, has != 0);
+                float now = kth;
+                if (lanes) {
+                    do {
+                        const int from = __ffs(lanes) - 1;
+                        const int ci = __shfl_sync(0xFFFFFFFFu, i0 + __ffs(has) - 1, from);
+                        if (lane == from) has &= has - 1;
+                        const float cx = logit(x, ci);
+                        const int pos = __popc(__ballot_sync(0xFFFFFFFFu, better(mine.x, mine.i, cx, ci)));
+                        const float ux = __shfl_up_sync(0xFFFFFFFFu, mine.x, 1);
+                        const int ui = __shfl_up_sync(0xFFFFFFFFu, mine.i, 1);
+                        if (lane > pos) mine.x = ux, mine.i = ui;
+                        if (lane == pos) mine.x = cx, mine.i = ci;
+                        lanes = __ballot_sync(0xFFFFFFFFu, has != 0);
+                    } while (lanes);
+                    now = __shfl_sync(0xFFFFFFFFu, mine.x, K - 1);
+                    if (lane == 0 && now > floor) atomicMax(&sm_tau, tau_of(now));
+                }
+                // a logit equal to another warp's K-th may still be ahead of it, one equal to this warp's not
+                const int fb = __float_as_int(floor);
+                const float below = floor == -CUDART_INF_F ? floor : floor == 0.f ? -1.4012985e-45f : __int_as_float(fb > 0 ? fb - 1 : fb + 1);
+                gate = fminf(fmaxf(now, below), st.best);
+            }
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (j == own) e[j] = -CUDART_INF_F;  // it is not summed
+        }
+        const float2 r2 = make_float2(-ref, -ref), cc = make_float2(c2, c2);
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            float2 y = mul2(add2(make_float2(e[j], e[j + 1]), r2), cc);
+            y.x = max_nan(y.x, -1000.f), y.y = max_nan(y.y, -1000.f);
+            float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            s2 = add2(s2, p);
+            t2 = fma2(p, y, t2);
+        }
+    };
+
+#pragma unroll 1
+    for (int base = v0; base < v1; base += kThreads) {
+        const uint4 raw = ring[0];
+#pragma unroll
+        for (int u = 0; u + 1 < AHEAD; ++u) ring[u] = ring[u + 1];
+        ring[AHEAD - 1] = load(base + AHEAD * kThreads + tid);
+        take(base + tid, raw);
+    }
+    int before = (int)(n2.x + n2.y);
+    if (tid == 0 && tv >= v0 && tv < v1)  // the target's own load
+        for (int i = max(tv * E - skew, 0); i < target; ++i) {
+            const float v = logit(x, i);
+            before += dead ? -(v > xt) : v == xt;
+        }
+
+    // ---- the warps' numbers and lists ----
+    st.s = warp_sum(s2.x + s2.y);
+    st.t = warp_sum(t2.x + t2.y);
+    st.before = __reduce_add_sync(0xFFFFFFFFu, before);
+    if (lane == 0) sm_stats[warp] = st;
+    __syncthreads();
+    // The lanes' numbers joined over n lanes, a power of two.
+    auto joined = [&](Stats sum, int n) {
+        for (int o = n / 2; o > 0; o >>= 1) {
+            Stats q;
+            q.best = __shfl_xor_sync(0xFFFFFFFFu, sum.best, o), q.best_i = __shfl_xor_sync(0xFFFFFFFFu, sum.best_i, o);
+            q.s = __shfl_xor_sync(0xFFFFFFFFu, sum.s, o), q.t = __shfl_xor_sync(0xFFFFFFFFu, sum.t, o);
+            q.before = __shfl_xor_sync(0xFFFFFFFFu, sum.before, o);
+            merge(sum, q, c2);
+        }
+        return sum;
+    };
+    Stats all = {-CUDART_INF_F, INT_MAX, 0.f, 0.f, 0};
+    if (warp == 0) all = joined(sm_stats[lane % kWarps], kWarps);
+    // The first K of what is in sm_cand, by rank, into sm_top; the rest of it empty.
+    auto rank = [&]() {
+        const int n = sm_n;
+        for (int j = tid; j < n; j += kThreads) {
+            const Cand c = sm_cand[j];
+            const int r = place(sm_cand, n, c);
+            if (r < K) sm_top[r] = c;
+        }
+        if (tid >= n && tid < K) sm_top[tid] = {-CUDART_INF_F, INT_MAX};
+        __syncthreads();
+    };
+    if (K > 0) {
+        const int tau = sm_tau;  // entries below it are not among the K best; the order of the others does not matter
+        if (lane < K && mine.i != INT_MAX && tau_of(mine.x) >= tau) sm_cand[atomicAdd(&sm_n, 1)] = mine;
+        __syncthreads();
+        rank();
+    }
+
+    if (split > 1) {
+        uint32_t* counters = static_cast<uint32_t*>(a.workspace);
+        Piece* pieces = reinterpret_cast<Piece*>(counters + kPieces);
+        Piece* own = pieces + blockIdx.x;
+        if (tid == 0) own->st = all;
+        if (tid < K) own->top[tid] = sm_top[tid];
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();  // the piece before its count
+            sm_last = atomicInc(counters + row, split - 1) == (unsigned)split - 1;  // back to 0 behind the last
+            __threadfence();
+            sm_n = sm_lists = 0;
+            sm_bound = {-CUDART_INF_F, INT_MAX};
+        }
+        __syncthreads();
+        if (!sm_last) return;
+        const Piece* of = pieces + (int64_t)row * split;
+        Cand head = {-CUDART_INF_F, INT_MAX};
+        if (K > 0) {
+            if (tid < split) head = {__ldcg(&of[tid].top[0].x), __ldcg(&of[tid].top[0].i)};
+            sm_cand[tid] = head;
+        }
+        if (warp == 0) {  // the pieces in their order, 32 at a time to the warp's lanes, then those
+            Stats sum = {-CUDART_INF_F, INT_MAX, 0.f, 0.f, 0};
+            for (int p = lane; p < split; p += 32) {
+                Stats q;
+                q.best = __ldcg(&of[p].st.best), q.best_i = __ldcg(&of[p].st.best_i), q.s = __ldcg(&of[p].st.s);
+                q.t = __ldcg(&of[p].st.t), q.before = __ldcg(&of[p].st.before);
+                merge(sum, q, c2);
+            }
+            all = joined(sum, 32);
+        }
+        __syncthreads();
+        if (K > 0) {
+            // Only the pieces with the K best heads can hold one of the row's K best, in entries not behind the K-th.
+            if (head.i != INT_MAX) {
+                const int r = place(sm_cand, split, head);
+                if (r < K) sm_list[atomicAdd(&sm_lists, 1)] = tid;
+                if (r == K - 1) sm_bound = head;
+            }
+            __syncthreads();
+            const int entries = sm_lists * K;
+            const Cand bound = sm_bound;
+            for (int j = tid; j < entries; j += kThreads) {
+                const Cand* at = &of[sm_list[j / K]].top[j % K];
+                const Cand e = {__ldcg(&at->x), __ldcg(&at->i)};
+                if (e.i != INT_MAX && !better(bound.x, bound.i, e.x, e.i)) sm_cand[atomicAdd(&sm_n, 1)] = e;
+            }
+            __syncthreads();
+            rank();
+        }
+    }
+
+    if (warp != 0) return;
+    const bool none = all.best == -CUDART_INF_F;
+    const float s = all.s + (none ? 0.f : all.best - all.best);  // plus infinity gives NaN
+    const float lse = log1pf(s);
+    if (tid == 0) {
+        if (a.logprob) a.logprob[row] = target < 0 ? 0.f : none ? -CUDART_INF_F + s : (xt - all.best) * a.scale - lse;
+        if (a.rank) a.rank[row] = target < 0 ? 0 : 1 + all.before + (dead ? target : 0);
+        if (a.entropy) a.entropy[row] = none ? s : lse - kLn2 * all.t / (1.f + s);
+    }
+    if (tid < K) {
+        const Cand c = sm_top[tid];
+        const bool no = c.i == INT_MAX;
+        if (a.top_ids) a.top_ids[(int64_t)row * K + tid] = no ? -1 : c.i;
+        if (a.top_logprobs) a.top_logprobs[(int64_t)row * K + tid] = no ? -CUDART_INF_F + s : (c.x - all.best) * a.scale - lse;
     }
 }
 
 }  // namespace
 
-size_t token_logprobs_workspace() { return 0; }
+size_t token_logprobs_workspace() { return kPieces * sizeof(uint32_t) + (size_t)kPieces * sizeof(Piece); }
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
+    // Pieces of at least 2048 logits, as many as fill the GPU several times over.
+    int64_t split = 1;
+    if (a.ws_bytes >= token_logprobs_workspace()) {
+        const int64_t want = (int64_t)device_sm_count() * 8;
+        split = (want + a.M / 2) / a.M;
+        if (split > a.V / 2048) split = a.V / 2048;
+        if (split > kMaxSplit) split = kMaxSplit;
+        if (split * a.M > kPieces) split = kPieces / a.M;
+        if (split < 1) split = 1;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.M, 1, 1);
+    cfg.gridDim = dim3((unsigned)(a.M * split), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attrs[1];
@@ -141,7 +495,7 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
     cfg.attrs = attrs;
     cfg.numAttrs = 1;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, a.fp32 ? token_logprobs_kernel<float> : token_logprobs_kernel<uint16_t>, a);
+    return cudaLaunchKernelEx(&cfg, a.fp32 ? token_logprobs_kernel<float> : token_logprobs_kernel<uint16_t>, a, (int)split);
 }
 
 int logprobs_take_range() {
