@@ -38,6 +38,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;        // a warp's list is one entry per lane
 constexpr int kPieces = 8192;      // pieces that the workspace holds
 constexpr int kMaxSplit = 256;     // pieces of a row, one per thread of the CTA that joins them
+constexpr int kNoTau = (int)0x807FFFFF;  // minus infinity as an ordered whole number
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct Cand {  // a logit and its index; better: larger, then the lower index
@@ -74,12 +75,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;}"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 r;
     asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
@@ -106,9 +101,20 @@ struct Bf16Load {
         asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
-    static __device__ __forceinline__ float largest(uint4 v, const float*) {
-        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
-        return fmaxf(bf16lo_to_f32(m), bf16hi_to_f32(m));
+    static __device__ __forceinline__ uint32_t largest2(uint4 v) { return max2(max2(v.x, v.y), max2(v.z, v.w)); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max2(a, b); }
+    static __device__ __forceinline__ float value(uint32_t m) { return fmaxf(bf16lo_to_f32(m), bf16hi_to_f32(m)); }
+    // not below `low`, a pair (a NaN stays one)
+    static __device__ __forceinline__ uint4 at_least(uint4 v, uint32_t low) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(low));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the next bf16 pair below a finite x
+    static __device__ __forceinline__ uint32_t below(float x) {
+        const uint32_t b = __float_as_uint(x) >> 16;
+        return threshold((uint16_t)(x > 0.f ? (b == 0 ? 0x8001 : b - 1) : (b | 0x8000) + 1));
     }
     static __device__ __forceinline__ uint32_t above2(uint32_t a, uint32_t b) {  // 1 or 0 in bf16
         uint32_t r;
@@ -120,10 +126,12 @@ struct Bf16Load {
         asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
-    static __device__ __forceinline__ float2 above(uint4 v, const float*, uint32_t thr) {
-        const uint32_t n = add(add(above2(v.x, thr), above2(v.y, thr)), add(above2(v.z, thr), above2(v.w, thr)));
-        return make_float2(bf16lo_to_f32(n), bf16hi_to_f32(n));
+    static __device__ __forceinline__ float least(uint32_t low) { return bf16lo_to_f32(low); }
+    // Counts of the logits above a threshold, a pair; at most 4 each per load, exact up to 256.
+    static __device__ __forceinline__ uint32_t above(uint4 v, uint32_t thr, uint32_t n) {
+        return add(n, add(add(above2(v.x, thr), above2(v.y, thr)), add(above2(v.z, thr), above2(v.w, thr))));
     }
+    static __device__ __forceinline__ float count(uint32_t n) { return bf16lo_to_f32(n) + bf16hi_to_f32(n); }
     static __device__ __forceinline__ uint32_t threshold(uint16_t x) { return x | (uint32_t)x << 16; }
     // the threshold that everything not below x is above (x finite or plus infinity)
     static __device__ __forceinline__ uint32_t threshold_below(uint16_t x) {
@@ -136,18 +144,29 @@ struct F32Load {
     static __device__ __forceinline__ void spread(uint4 v, float* x) {
         x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     }
-    static __device__ __forceinline__ float largest(uint4, const float* x) {
-        return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    static __device__ __forceinline__ uint32_t largest2(uint4 v) {
+        return __float_as_uint(fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))));
     }
-    static __device__ __forceinline__ float above1(float a, float b) {
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    static __device__ __forceinline__ float value(uint32_t m) { return __uint_as_float(m); }
+    static __device__ __forceinline__ uint4 at_least(uint4 v, uint32_t low) {
+        const float l = __uint_as_float(low);
+        return make_uint4(__float_as_uint(max_nan(__uint_as_float(v.x), l)), __float_as_uint(max_nan(__uint_as_float(v.y), l)),
+                          __float_as_uint(max_nan(__uint_as_float(v.z), l)), __float_as_uint(max_nan(__uint_as_float(v.w), l)));
+    }
+    static __device__ __forceinline__ uint32_t below(float x) { return __float_as_uint(x); }
+    static __device__ __forceinline__ float least(uint32_t low) { return __uint_as_float(low); }
+    static __device__ __forceinline__ float above1(uint32_t a, uint32_t b) {
         float r;
-        asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+        asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
         return r;
     }
-    static __device__ __forceinline__ float2 above(uint4, const float* x, uint32_t thr) {
-        const float t = __uint_as_float(thr);
-        return add2(make_float2(above1(x[0], t), above1(x[1], t)), make_float2(above1(x[2], t), above1(x[3], t)));
+    static __device__ __forceinline__ uint32_t above(uint4 v, uint32_t thr, uint32_t n) {
+        return __float_as_uint(__uint_as_float(n) + ((above1(v.x, thr) + above1(v.y, thr)) + (above1(v.z, thr) + above1(v.w, thr))));
     }
+    static __device__ __forceinline__ float count(uint32_t n) { return __uint_as_float(n); }
     static __device__ __forceinline__ uint32_t threshold(float x) { return __float_as_uint(x); }
     static __device__ __forceinline__ uint32_t threshold_below(float x) {
         const uint32_t b = __float_as_uint(x);
@@ -174,23 +193,28 @@ __device__ __forceinline__ void merge(Stats& a, const Stats& b, float c2) {
     a.before += b.before;
 }
 
-// Rank of candidate j of n in shared memory: how many are better. Ties cannot be: indexes differ.
+// How many of n candidates in shared memory (a multiple of 2, the rest of the last pair no candidate) are better.
 __device__ __forceinline__ int place(const Cand* c, int n, Cand x) {
     int r = 0;
-    for (int j = 0; j < n; ++j) r += better(c[j].x, c[j].i, x.x, x.i);
+#pragma unroll 4
+    for (int j = 0; j < n; j += 2) {
+        const int4 v = *reinterpret_cast<const int4*>(c + j);
+        r += better(__int_as_float(v.x), v.y, x.x, x.i);
+        r += better(__int_as_float(v.z), v.w, x.x, x.i);
+    }
     return r;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs a, int split) {
+__global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs a, int split) {
     using L = typename LoadOf<T>::type;
     constexpr int E = L::E, AHEAD = 4;  // loads of a thread in flight
     __shared__ Stats sm_stats[kWarps];
-    __shared__ Cand sm_cand[kMaxTop * kMaxTop];  // the warps' lists; later the entries of a row's pieces that can win
+    __shared__ __align__(16) Cand sm_cand[kMaxTop * kMaxTop + 2];  // the warps' lists; later the entries of a row's pieces that can win
     __shared__ Cand sm_top[kMaxTop];
     __shared__ int sm_tau;  // k-th best logit of some warp of the CTA, as an ordered whole number
     __shared__ Cand sm_bound;    // the K-th best head of a row's pieces
-    __shared__ int sm_n, sm_lists, sm_last, sm_list[kMaxTop];
+    __shared__ int sm_seed, sm_n, sm_lists, sm_last, sm_list[kMaxTop];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = a.top_k;
@@ -204,15 +228,18 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     const uint4* xv = reinterpret_cast<const uint4*>(x - skew);
     const unsigned loads = ((unsigned)V + skew + E - 1) / E, each = loads / split, rest = loads - each * split;
     const int v0 = (int)(piece * each + min(piece, rest)), v1 = v0 + (int)(each + (piece < rest));
-    const int full0 = skew ? 1 : 0, full1 = (int)(((unsigned)V + skew) / E), last = min(v1, full1);
-    // Load v; minus infinity past the piece, and for what of the row's first and last 16 bytes is not its own (and is
-    // not read).
+    // A row's first and last 16 bytes may not all be its own: such loads are made logit by logit, by one thread in a
+    // turn of their own before and behind the others, minus infinity in the place of what is not the row's.
+    const int full0 = skew ? 1 : 0, full1 = (int)(((unsigned)V + skew) / E), first = max(v0, full0), last = min(v1, full1);
+    const uint4 none4 = make_uint4(L::kNone, L::kNone, L::kNone, L::kNone);
     auto load = [&](int v) {
-        uint4 raw = make_uint4(L::kNone, L::kNone, L::kNone, L::kNone);
-        if (v >= full0 && v < last) {
-            raw = ld_stream16(xv + v);
-        } else if (v < v1) {
-            uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint4 raw = none4;
+        if (v < last) raw = ld_stream16(xv + v);
+        return raw;
+    };
+    auto load_part = [&](int v) {
+        uint32_t w[4] = {none4.x, none4.y, none4.z, none4.w};
+        if (tid == 0) {
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 const int64_t i = (int64_t)v * E - skew + j;
@@ -222,14 +249,14 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
                 else
                     w[j >> 1] = __byte_perm(w[j >> 1], __float_as_uint(logit(x, i)) >> 16, j & 1 ? 0x5410 : 0x3254);
             }
-            raw = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        return raw;
+        return make_uint4(w[0], w[1], w[2], w[3]);
     };
+    const bool head_part = v0 < first, tail_part = v1 > max(first, last);  // a row of one load is all head
     uint4 ring[AHEAD];
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) ring[u] = load(v0 + u * kThreads + tid);
-    if (tid == 0) sm_tau = INT_MAX, sm_n = 0;
+    for (int u = 0; u < AHEAD; ++u) ring[u] = load(first + u * kThreads + tid);
+    if (tid == 0) sm_tau = kNoTau, sm_seed = INT_MAX, sm_n = 0;
     __syncthreads();
 
     int target = a.targets ? a.targets[row] : -1;
@@ -247,8 +274,15 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     const uint32_t until = target < 0 ? after : L::threshold_below(x[target]);
 
     Stats st = {-CUDART_INF_F, INT_MAX, 0.f, 0.f, 0};
-    float2 s2 = make_float2(0.f, 0.f), t2 = s2, n2 = s2;
-    float ref = 0.f;  // what is subtracted: best, 0 while there is none
+    float2 s2 = make_float2(0.f, 0.f), t2 = s2;
+    float counted = 0.f;
+    // y = (x - best) * c2 as x c2 + shift in one operation. shift is off by -lag, for all logits alike, which is put
+    // right when best moves and at the end. Logits are first raised to `low`, where y is below -150 and finite: their
+    // e is 0, and 0 times it. Where best is beyond 1e37 (a row that is masked throughout with the type's lowest
+    // value), plainly.
+    float shift = 0.f, lag = 0.f;
+    uint32_t low = 0;
+    bool plain = true;
     Cand mine = {-CUDART_INF_F, INT_MAX};  // the warp's list, in order: entry `lane`
     float gate = -CUDART_INF_F;  // no logit up to this one moves the maximum or enters the list
 
@@ -258,32 +292,39 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
         return b < 0 ? b ^ 0x7FFFFFFF : b;
     };
 
-    constexpr int kNoTau = (int)0x807FFFFF;  // of minus infinity
     auto value_of = [](int t) { return __int_as_float(t < 0 ? t ^ 0x7FFFFFFF : t); };
-    // A first gate: each warp holds ceil(K / 8) lanes whose largest logit is at least t, so the least t of the warps is
-    // not above the K-th best logit of the CTA.
-    if (K > 0) {
-        float e[E];
-        L::spread(ring[0], e);
-        int big = tau_of(L::largest(ring[0], e)), t = kNoTau;
-        for (int r = 0; r < (K + kWarps - 1) / kWarps; ++r) {
-            t = __reduce_max_sync(0xFFFFFFFFu, big);
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, big == t);
-            if (lane == __ffs(who) - 1) big = kNoTau;
-        }
-        if (lane == 0) atomicMin(&sm_tau, t);
-        __syncthreads();
-    }
 
-    // One load of every lane.
+    auto settle = [&]() {  // the sums as if y had been exact
+        const float f = exp2_fast(lag);
+        t2 = make_float2(f * fmaf(lag, s2.x, t2.x), f * fmaf(lag, s2.y, t2.y));
+        s2 = make_float2(f * s2.x, f * s2.y);
+    };
+    auto sum_plain = [&](const float* e) {
+        const float ref = st.best == -CUDART_INF_F ? 0.f : st.best;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const float y = max_nan((e[j] - ref) * c2, -1000.f), p = exp2_fast(y);
+            s2.x += p, t2.x = fmaf(p, y, t2.x);
+        }
+    };
+    auto sum_fast = [&](const float* e) {
+        const float2 sh = make_float2(shift, shift), cc = make_float2(c2, c2);
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            const float2 y = fma2(make_float2(e[j], e[j + 1]), cc, sh), p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            s2 = add2(s2, p);
+            t2 = fma2(p, y, t2);
+        }
+    };
+
+    // One load of every lane, where some logit may move the maximum or enter the list.
     auto take = [&](int v, uint4 raw) {
         float e[E];
         L::spread(raw, e);
         const int i0 = v * E - skew;
-        const float big = L::largest(raw, e);
-        n2 = add2(n2, L::above(raw, e, v < tv ? until : after));
+        const float big = L::value(L::largest2(raw));
+        int own = -1;  // the lane's logit that is the maximum
         if (__any_sync(0xFFFFFFFFu, big > gate)) {
-            int own = -1;  // the lane's logit that is the maximum
             if (__any_sync(0xFFFFFFFFu, big > st.best)) {  // ---- the maximum ----
                 const float wm = value_of(__reduce_max_sync(0xFFFFFFFFu, tau_of(big)));
                 int at = INT_MAX;
@@ -293,11 +334,16 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
                 at = __reduce_min_sync(0xFFFFFFFFu, at);
                 const bool none = st.best == -CUDART_INF_F;
                 const float d = none ? 0.f : max_nan((st.best - wm) * c2, -1000.f), f = none ? 0.f : exp2_fast(d);
+                if (!plain) settle();
                 // f = 0 keeps a NaN that the sums hold
                 t2 = make_float2(f * (t2.x + d * s2.x), f * (t2.y + d * s2.y));
                 s2 = make_float2(f * s2.x, f * s2.y);
                 if (lane == 0) s2.x += f, t2.x += f * d;
-                st.best = wm, st.best_i = at, ref = wm;
+                st.best = wm, st.best_i = at;
+                shift = -wm * c2, lag = fmaf(-wm, c2, -shift);
+                const float cut = wm - 160.f / c2;
+                plain = !(fabsf(shift) < 1e37f) || !(cut > -1e37f) || !(wm < 1e37f);
+                low = L::below(cut);
                 own = at - i0;
             }
             gate = st.best;
@@ -315,9 +361,14 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
                 if (lanes) {
                     do {
                         const int from = __ffs(lanes) - 1;
-                        const int ci = __shfl_sync(0xFFFFFFFFu, i0 + __ffs(has) - 1, from);
+                        const int b = __ffs(has) - 1;
+                        float mx = e[0];
+#pragma unroll
+                        for (int j = 1; j < E; ++j)
+                            if (b == j) mx = e[j];
+                        const int ci = __shfl_sync(0xFFFFFFFFu, i0 + b, from);
+                        const float cx = __shfl_sync(0xFFFFFFFFu, mx, from);
                         if (lane == from) has &= has - 1;
-                        const float cx = logit(x, ci);
                         const int pos = __popc(__ballot_sync(0xFFFFFFFFu, better(mine.x, mine.i, cx, ci)));
                         const float ux = __shfl_up_sync(0xFFFFFFFFu, mine.x, 1);
                         const int ui = __shfl_up_sync(0xFFFFFFFFu, mine.i, 1);
@@ -333,30 +384,82 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
                 const float below = floor == -CUDART_INF_F ? floor : floor == 0.f ? -1.4012985e-45f : __int_as_float(fb > 0 ? fb - 1 : fb + 1);
                 gate = fminf(fmaxf(now, below), st.best);
             }
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (j == own) e[j] = -CUDART_INF_F;  // it is not summed
         }
-        const float2 r2 = make_float2(-ref, -ref), cc = make_float2(c2, c2);
+        if (!plain) L::spread(L::at_least(raw, low), e);
+        const float out = plain ? -CUDART_INF_F : L::least(low);  // the maximum itself is not summed
 #pragma unroll
-        for (int j = 0; j < E; j += 2) {
-            float2 y = mul2(add2(make_float2(e[j], e[j + 1]), r2), cc);
-            y.x = max_nan(y.x, -1000.f), y.y = max_nan(y.y, -1000.f);
-            float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-            s2 = add2(s2, p);
-            t2 = fma2(p, y, t2);
-        }
+        for (int j = 0; j < E; ++j)
+            if (j == own) e[j] = out;
+        if (plain)
+            sum_plain(e);
+        else
+            sum_fast(e);
     };
 
 #pragma unroll 1
-    for (int base = v0; base < v1; base += kThreads) {
-        const uint4 raw = ring[0];
+    for (int phase = head_part ? 0 : 1; phase < (tail_part ? 3 : 2); ++phase) {
+        int base = first + tid, end = last;
+        if (phase != 1) {  // one load, of thread 0
+            base = phase == 0 ? v0 : v1 - 1;
+            end = base + 1;
+            ring[0] = load_part(base);
 #pragma unroll
-        for (int u = 0; u + 1 < AHEAD; ++u) ring[u] = ring[u + 1];
-        ring[AHEAD - 1] = load(base + AHEAD * kThreads + tid);
-        take(base + tid, raw);
+            for (int u = 1; u < AHEAD; ++u) ring[u] = none4;
+        } else {
+            if (head_part) {
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) ring[u] = load(base + u * kThreads);
+            }
+            if (K > 0) {
+                // A first gate: each warp holds ceil(K / 8) lanes whose largest logit is at least t, so the least t of
+                // the warps is not above the K-th best logit of the CTA.
+                int big = tau_of(L::value(L::largest2(ring[0]))), t = kNoTau;
+                for (int r = 0; r < (K + kWarps - 1) / kWarps; ++r) {
+                    t = __reduce_max_sync(0xFFFFFFFFu, big);
+                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, big == t);
+                    if (lane == __ffs(who) - 1) big = kNoTau;
+                }
+                if (lane == 0) atomicMin(&sm_seed, t);
+                __syncthreads();
+                if (tid == 0) atomicMax(&sm_tau, sm_seed);
+                __syncthreads();
+            }
+        }
+        const int step = phase == 1 ? tid : 0;
+#pragma unroll 1
+        for (; base - step < end; base += kThreads * AHEAD) {
+            uint4 next[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) next[u] = phase == 1 ? load(base + (AHEAD + u) * kThreads) : none4;
+            uint32_t most = L::largest2(ring[0]), n = 0;
+#pragma unroll
+            for (int u = 1; u < AHEAD; ++u) most = L::larger(most, L::largest2(ring[u]));
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) n = L::above(ring[u], base + u * kThreads < tv ? until : after, n);
+            counted += L::count(n);
+            if (plain || __any_sync(0xFFFFFFFFu, L::value(most) > gate)) {
+#pragma unroll 1
+                for (int u = 0; u < AHEAD; ++u) {
+                    uint4 raw = ring[0];
+#pragma unroll
+                    for (int i = 1; i < AHEAD; ++i)
+                        if (u == i) raw = ring[i];
+                    take(base + u * kThreads, raw);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    float e[E];
+                    L::spread(L::at_least(ring[u], low), e);
+                    sum_fast(e);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) ring[u] = next[u];
+        }
     }
-    int before = (int)(n2.x + n2.y);
+    if (!plain) settle();
+    int before = (int)counted;
     if (tid == 0 && tv >= v0 && tv < v1)  // the target's own load
         for (int i = max(tv * E - skew, 0); i < target; ++i) {
             const float v = logit(x, i);
@@ -385,6 +488,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     // The first K of what is in sm_cand, by rank, into sm_top; the rest of it empty.
     auto rank = [&]() {
         const int n = sm_n;
+        if (tid == 0 && (n & 1)) sm_cand[n] = {-CUDART_INF_F, INT_MAX};
+        __syncthreads();
         for (int j = tid; j < n; j += kThreads) {
             const Cand c = sm_cand[j];
             const int r = place(sm_cand, n, c);
@@ -420,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
         Cand head = {-CUDART_INF_F, INT_MAX};
         if (K > 0) {
             if (tid < split) head = {__ldcg(&of[tid].top[0].x), __ldcg(&of[tid].top[0].i)};
-            sm_cand[tid] = head;
+            sm_cand[tid] = head;  // those past split are no candidates
         }
         if (warp == 0) {  // the pieces in their order, 32 at a time to the warp's lanes, then those
             Stats sum = {-CUDART_INF_F, INT_MAX, 0.f, 0.f, 0};
@@ -475,15 +580,17 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
 size_t token_logprobs_workspace() { return kPieces * sizeof(uint32_t) + (size_t)kPieces * sizeof(Piece); }
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
-    // Pieces of at least 2048 logits, as many as fill the GPU several times over.
+    // Pieces of at least 2048 logits, in whole waves of three CTAs per SM as far as that goes: a piece costs what its
+    // logits do and as much as some 20,000 more.
     int64_t split = 1;
     if (a.ws_bytes >= token_logprobs_workspace()) {
-        const int64_t want = (int64_t)device_sm_count() * 8;
-        split = (want + a.M / 2) / a.M;
-        if (split > a.V / 2048) split = a.V / 2048;
-        if (split > kMaxSplit) split = kMaxSplit;
-        if (split * a.M > kPieces) split = kPieces / a.M;
-        if (split < 1) split = 1;
+        const int64_t slots = 3 * (int64_t)device_sm_count();
+        int64_t most = a.V / 2048, best = -1;
+        if (most > kMaxSplit) most = kMaxSplit;
+        for (int64_t n = 1; n <= most && (n == 1 || n * a.M <= kPieces); ++n) {
+            const int64_t cost = (a.M * n + slots - 1) / slots * (a.V / n + 20000);
+            if (best < 0 || cost < best) best = cost, split = n;
+        }
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.M * split), 1, 1);
