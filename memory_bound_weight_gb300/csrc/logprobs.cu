@@ -126,7 +126,15 @@ struct Bf16Load {
         asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
-    static __device__ __forceinline__ float least(uint32_t low) { return bf16lo_to_f32(low); }
+    static __device__ __forceinline__ float half(uint32_t w, int j) { return j & 1 ? bf16hi_to_f32(w) : bf16lo_to_f32(w); }
+    // `low` in the place of logit j, where the load has it
+    static __device__ __forceinline__ uint4 put(uint4 v, int j, uint32_t low) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j >> 1 == i) w[i] = __byte_perm(w[i], low, j & 1 ? 0x5410 : 0x3254);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
     // Counts of the logits above a threshold, a pair; at most 4 each per load, exact up to 256.
     static __device__ __forceinline__ uint32_t above(uint4 v, uint32_t thr, uint32_t n) {
         return add(n, add(add(above2(v.x, thr), above2(v.y, thr)), add(above2(v.z, thr), above2(v.w, thr))));
@@ -157,7 +165,10 @@ struct F32Load {
                           __float_as_uint(max_nan(__uint_as_float(v.z), l)), __float_as_uint(max_nan(__uint_as_float(v.w), l)));
     }
     static __device__ __forceinline__ uint32_t below(float x) { return __float_as_uint(x); }
-    static __device__ __forceinline__ float least(uint32_t low) { return __uint_as_float(low); }
+    static __device__ __forceinline__ float half(uint32_t w, int) { return __uint_as_float(w); }
+    static __device__ __forceinline__ uint4 put(uint4 v, int j, uint32_t low) {
+        return make_uint4(j == 0 ? low : v.x, j == 1 ? low : v.y, j == 2 ? low : v.z, j == 3 ? low : v.w);
+    }
     static __device__ __forceinline__ float above1(uint32_t a, uint32_t b) {
         float r;
         asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
@@ -299,14 +310,6 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         t2 = make_float2(f * fmaf(lag, s2.x, t2.x), f * fmaf(lag, s2.y, t2.y));
         s2 = make_float2(f * s2.x, f * s2.y);
     };
-    auto sum_plain = [&](const float* e) {
-        const float ref = st.best == -CUDART_INF_F ? 0.f : st.best;
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const float y = max_nan((e[j] - ref) * c2, -1000.f), p = exp2_fast(y);
-            s2.x += p, t2.x = fmaf(p, y, t2.x);
-        }
-    };
     auto sum_fast = [&](const float* e) {
         const float2 sh = make_float2(shift, shift), cc = make_float2(c2, c2);
 #pragma unroll
@@ -317,83 +320,88 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         }
     };
 
-    // One load of every lane, where some logit may move the maximum or enter the list.
-    auto take = [&](int v, uint4 raw) {
-        float e[E];
-        L::spread(raw, e);
-        const int i0 = v * E - skew;
-        const float big = L::value(L::largest2(raw));
-        int own = -1;  // the lane's logit that is the maximum
-        if (__any_sync(0xFFFFFFFFu, big > gate)) {
-            if (__any_sync(0xFFFFFFFFu, big > st.best)) {  // ---- the maximum ----
-                const float wm = value_of(__reduce_max_sync(0xFFFFFFFFu, tau_of(big)));
-                int at = INT_MAX;
+    // Logit j (0 .. AHEAD * E - 1) of the thread's loads in hand.
+    auto pick = [&](int j) {
+        uint32_t w = ring[0].x;
 #pragma unroll
-                for (int j = E - 1; j >= 0; --j)
-                    if (e[j] == wm) at = i0 + j;
-                at = __reduce_min_sync(0xFFFFFFFFu, at);
-                const bool none = st.best == -CUDART_INF_F;
-                const float d = none ? 0.f : max_nan((st.best - wm) * c2, -1000.f), f = none ? 0.f : exp2_fast(d);
-                if (!plain) settle();
-                // f = 0 keeps a NaN that the sums hold
-                t2 = make_float2(f * (t2.x + d * s2.x), f * (t2.y + d * s2.y));
-                s2 = make_float2(f * s2.x, f * s2.y);
-                if (lane == 0) s2.x += f, t2.x += f * d;
-                st.best = wm, st.best_i = at;
-                shift = -wm * c2, lag = fmaf(-wm, c2, -shift);
-                const float cut = wm - 160.f / c2;
-                plain = !(fabsf(shift) < 1e37f) || !(cut > -1e37f) || !(wm < 1e37f);
-                low = L::below(cut);
-                own = at - i0;
-            }
-            gate = st.best;
-            if (K > 0) {  // ---- the list ----
-                const float kth = __shfl_sync(0xFFFFFFFFu, mine.x, K - 1);
-                const float floor = value_of(*reinterpret_cast<volatile int*>(&sm_tau));
-                // behind this warp's K-th, or below the gate of all: not among the K best
-                uint32_t has = 0;
-                if (big > kth && big >= floor) {
+        for (int u = 0; u < AHEAD; ++u) {
+            const uint32_t r[4] = {ring[u].x, ring[u].y, ring[u].z, ring[u].w};
 #pragma unroll
-                    for (int j = 0; j < E; ++j) has |= (uint32_t)(e[j] > kth && e[j] >= floor) << j;
-                }
-                uint32_t lanes = __ballot_sync(0xFFFFFFFFu, has != 0);
-                float now = kth;
-                if (lanes) {
-                    do {
-                        const int from = __ffs(lanes) - 1;
-                        const int b = __ffs(has) - 1;
-                        float mx = e[0];
-#pragma unroll
-                        for (int j = 1; j < E; ++j)
-                            if (b == j) mx = e[j];
-                        const int ci = __shfl_sync(0xFFFFFFFFu, i0 + b, from);
-                        const float cx = __shfl_sync(0xFFFFFFFFu, mx, from);
-                        if (lane == from) has &= has - 1;
-                        const int pos = __popc(__ballot_sync(0xFFFFFFFFu, better(mine.x, mine.i, cx, ci)));
-                        const float ux = __shfl_up_sync(0xFFFFFFFFu, mine.x, 1);
-                        const int ui = __shfl_up_sync(0xFFFFFFFFu, mine.i, 1);
-                        if (lane > pos) mine.x = ux, mine.i = ui;
-                        if (lane == pos) mine.x = cx, mine.i = ci;
-                        lanes = __ballot_sync(0xFFFFFFFFu, has != 0);
-                    } while (lanes);
-                    now = __shfl_sync(0xFFFFFFFFu, mine.x, K - 1);
-                    if (lane == 0 && now > floor) atomicMax(&sm_tau, tau_of(now));
-                }
-                // a logit equal to another warp's K-th may still be ahead of it, one equal to this warp's not
-                const int fb = __float_as_int(floor);
-                const float below = floor == -CUDART_INF_F ? floor : floor == 0.f ? -1.4012985e-45f : __int_as_float(fb > 0 ? fb - 1 : fb + 1);
-                gate = fminf(fmaxf(now, below), st.best);
-            }
+            for (int i = 0; i < 4; ++i)
+                if (j / (E / 4) == 4 * u + i) w = r[i];
         }
-        if (!plain) L::spread(L::at_least(raw, low), e);
-        const float out = plain ? -CUDART_INF_F : L::least(low);  // the maximum itself is not summed
+        return L::half(w, j);
+    };
+    // Some of the loads in hand holds a logit past the gate. `base`: the first one's number, the others kThreads apart.
+    auto past_gate = [&](int base, float big, int& excluded) {
+        if (__any_sync(0xFFFFFFFFu, big > st.best)) {  // ---- the maximum ----
+            const float wm = value_of(__reduce_max_sync(0xFFFFFFFFu, tau_of(big)));
+            int at = INT_MAX, own = -1;
+            if (big == wm) {
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (j == own) e[j] = out;
-        if (plain)
-            sum_plain(e);
-        else
-            sum_fast(e);
+                for (int u = AHEAD - 1; u >= 0; --u) {
+                    float e[E];
+                    L::spread(ring[u], e);
+#pragma unroll
+                    for (int j = E - 1; j >= 0; --j)
+                        if (e[j] == wm) own = u * E + j;
+                }
+                at = (base + own / E * kThreads) * E - skew + own % E;
+            }
+            const int first_at = __reduce_min_sync(0xFFFFFFFFu, at);
+            if (at != first_at) own = -1;
+            const bool none = st.best == -CUDART_INF_F;
+            const float d = none ? 0.f : max_nan((st.best - wm) * c2, -1000.f), f = none ? 0.f : exp2_fast(d);
+            if (!plain) settle();
+            // f = 0 keeps a NaN that the sums hold
+            t2 = make_float2(f * (t2.x + d * s2.x), f * (t2.y + d * s2.y));
+            s2 = make_float2(f * s2.x, f * s2.y);
+            if (lane == 0) s2.x += f, t2.x += f * d;
+            st.best = wm, st.best_i = first_at;
+            shift = -wm * c2, lag = fmaf(-wm, c2, -shift);
+            const float cut = wm - 160.f / c2;
+            plain = !(fabsf(shift) < 1e37f) || !(cut > -1e37f) || !(wm < 1e37f);
+            low = L::below(cut);
+            excluded = own;
+        }
+        gate = st.best;
+        if (K > 0) {  // ---- the list ----
+            const float kth = __shfl_sync(0xFFFFFFFFu, mine.x, K - 1);
+            const float floor = value_of(*reinterpret_cast<volatile int*>(&sm_tau));
+            // behind this warp's K-th, or below the gate of all: not among the K best
+            uint32_t has = 0;
+            if (big > kth && big >= floor) {
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    float e[E];
+                    L::spread(ring[u], e);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) has |= (uint32_t)(e[j] > kth && e[j] >= floor) << (u * E + j);
+                }
+            }
+            uint32_t lanes = __ballot_sync(0xFFFFFFFFu, has != 0);
+            float now = kth;
+            if (lanes) {
+                do {
+                    const int from = __ffs(lanes) - 1, b = __ffs(has) - 1;
+                    const int ci = __shfl_sync(0xFFFFFFFFu, (base + b / E * kThreads) * E - skew + b % E, from);
+                    const float cx = __shfl_sync(0xFFFFFFFFu, pick(b), from);
+                    if (lane == from) has &= has - 1;
+                    const int pos = __popc(__ballot_sync(0xFFFFFFFFu, better(mine.x, mine.i, cx, ci)));
+                    const float ux = __shfl_up_sync(0xFFFFFFFFu, mine.x, 1);
+                    const int ui = __shfl_up_sync(0xFFFFFFFFu, mine.i, 1);
+                    if (lane > pos) mine.x = ux, mine.i = ui;
+                    if (lane == pos) mine.x = cx, mine.i = ci;
+                    lanes = __ballot_sync(0xFFFFFFFFu, has != 0);
+                } while (lanes);
+                now = __shfl_sync(0xFFFFFFFFu, mine.x, K - 1);
+                if (lane == 0 && now > floor) atomicMax(&sm_tau, tau_of(now));
+            }
+            // a logit equal to another warp's K-th may still be ahead of it, one equal to this warp's not
+            const int fb = __float_as_int(floor);
+            const float below = floor == -CUDART_INF_F ? floor : floor == 0.f ? -1.4012985e-45f : __int_as_float(fb > 0 ? fb - 1 : fb + 1);
+            gate = fminf(fmaxf(now, below), st.best);
+        }
     };
 
 #pragma unroll 1
@@ -413,7 +421,10 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
             if (K > 0) {
                 // A first gate: each warp holds ceil(K / 8) lanes whose largest logit is at least t, so the least t of
                 // the warps is not above the K-th best logit of the CTA.
-                int big = tau_of(L::value(L::largest2(ring[0]))), t = kNoTau;
+                uint32_t most = L::largest2(ring[0]);
+#pragma unroll
+                for (int u = 1; u < AHEAD; ++u) most = L::larger(most, L::largest2(ring[u]));
+                int big = tau_of(L::value(most)), t = kNoTau;
                 for (int r = 0; r < (K + kWarps - 1) / kWarps; ++r) {
                     t = __reduce_max_sync(0xFFFFFFFFu, big);
                     const uint32_t who = __ballot_sync(0xFFFFFFFFu, big == t);
@@ -437,20 +448,21 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) n = L::above(ring[u], base + u * kThreads < tv ? until : after, n);
             counted += L::count(n);
-            if (plain || __any_sync(0xFFFFFFFFu, L::value(most) > gate)) {
-#pragma unroll 1
-                for (int u = 0; u < AHEAD; ++u) {
-                    uint4 raw = ring[0];
-#pragma unroll
-                    for (int i = 1; i < AHEAD; ++i)
-                        if (u == i) raw = ring[i];
-                    take(base + u * kThreads, raw);
+            int excluded = -1;  // the maximum itself is not summed
+            if (__any_sync(0xFFFFFFFFu, L::value(most) > gate)) past_gate(base, L::value(most), excluded);
+            if (plain) {
+                for (int j = 0; j < AHEAD * E; ++j) {
+                    const float ref = st.best == -CUDART_INF_F ? 0.f : st.best;
+                    const float y = j == excluded ? -1000.f : max_nan((pick(j) - ref) * c2, -1000.f), p = exp2_fast(y);
+                    s2.x += p, t2.x = fmaf(p, y, t2.x);
                 }
             } else {
 #pragma unroll
                 for (int u = 0; u < AHEAD; ++u) {
+                    uint4 v = L::at_least(ring[u], low);
+                    if (excluded >= 0) v = L::put(v, excluded - u * E, low);
                     float e[E];
-                    L::spread(L::at_least(ring[u], low), e);
+                    L::spread(v, e);
                     sum_fast(e);
                 }
             }
