@@ -47,10 +47,10 @@ struct Cand {  // a logit and its index; better: larger, then the lower index
 };
 __device__ __forceinline__ bool better(float x, int i, float y, int j) { return x > y || (x == y && i < j); }
 
-struct Stats {  // of some of a row's logits, in powers of two of (x - x_best) * scale
-    float best;  // the largest, minus infinity where there is none
-    int best_i;
-    float s, t;  // sum of e and of e log2 e over the others
+struct Stats {  // of some of a row's logits, in powers of two of (x - ref) * scale
+    float ref;   // the largest, or one larger than all of them; minus infinity where there is none
+    int own;     // the index of the logit that is ref and is not in the sums; none: ref belongs to others
+    float s, t;  // sum of e and of e log2 e
     int before;  // logits ahead of the target
 };
 struct __align__(16) Piece {
@@ -191,16 +191,17 @@ struct LoadOf<uint16_t> { using type = Bf16Load; };
 template <>
 struct LoadOf<float> { using type = F32Load; };
 
-// b behind a: the sums taken to the larger maximum, the smaller one's term added.
+// b joined to a: the sums taken to the larger ref, the term of a smaller one that was left out added.
 __device__ __forceinline__ void merge(Stats& a, const Stats& b, float c2) {
-    const bool swap = better(b.best, b.best_i, a.best, a.best_i);
-    const float hi = swap ? b.best : a.best, lo = swap ? a.best : b.best;
+    const bool swap = better(b.ref, b.own, a.ref, a.own);
+    const float hi = swap ? b.ref : a.ref, lo = swap ? a.ref : b.ref;
     const float s_hi = swap ? b.s : a.s, t_hi = swap ? b.t : a.t, s_lo = swap ? a.s : b.s, t_lo = swap ? a.t : b.t;
     const bool none = lo == -CUDART_INF_F;
+    const float one = (swap ? a.own : b.own) != INT_MAX ? 1.f : 0.f;
     const float d = none ? 0.f : max_nan((lo - hi) * c2, -1000.f), f = none ? 0.f : exp2_fast(d);
-    if (swap) a.best = b.best, a.best_i = b.best_i;
-    a.s = s_hi + f * (s_lo + 1.f);
-    a.t = t_hi + f * (t_lo + d * s_lo + d);
+    if (swap) a.ref = b.ref, a.own = b.own;
+    a.s = s_hi + f * (s_lo + one);
+    a.t = t_hi + f * (t_lo + d * (s_lo + one));
     a.before += b.before;
 }
 
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     __shared__ Cand sm_top[kMaxTop];
     __shared__ int sm_tau;  // k-th best logit of some warp of the CTA, as an ordered whole number
     __shared__ Cand sm_bound;    // the K-th best head of a row's pieces
-    __shared__ int sm_seed, sm_n, sm_lists, sm_last, sm_list[kMaxTop];
+    __shared__ int sm_ref, sm_seed, sm_n, sm_lists, sm_last, sm_list[kMaxTop];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = a.top_k;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     uint4 ring[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) ring[u] = load(first + u * kThreads + tid);
-    if (tid == 0) sm_tau = kNoTau, sm_seed = INT_MAX, sm_n = 0;
+    if (tid == 0) sm_tau = sm_ref = kNoTau, sm_seed = INT_MAX, sm_n = 0;
     __syncthreads();
 
     int target = a.targets ? a.targets[row] : -1;
@@ -332,39 +333,46 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         }
         return L::half(w, j);
     };
+    auto refer = [&](float x) {
+        st.ref = x;
+        shift = -x * c2, lag = fmaf(-x, c2, -shift);
+        const float cut = x - 160.f / c2;
+        plain = !(fabsf(shift) < 1e37f) || !(cut > -1e37f) || !(x < 1e37f);
+        low = L::below(cut);
+    };
+    // Where the largest of the loads in hand is, among equals the first: its number in them, and its index.
+    auto where = [&](int base, float x, int& own, int& at) {
+        own = -1, at = INT_MAX;
+#pragma unroll
+        for (int u = AHEAD - 1; u >= 0; --u) {
+            float e[E];
+            L::spread(ring[u], e);
+#pragma unroll
+            for (int j = E - 1; j >= 0; --j)
+                if (e[j] == x) own = u * E + j;
+        }
+        if (own >= 0) at = (base + own / E * kThreads) * E - skew + own % E;
+    };
     // Some of the loads in hand holds a logit past the gate. `base`: the first one's number, the others kThreads apart.
     auto past_gate = [&](int base, float big, int& excluded) {
-        if (__any_sync(0xFFFFFFFFu, big > st.best)) {  // ---- the maximum ----
+        if (__any_sync(0xFFFFFFFFu, big > st.ref)) {  // ---- the maximum ----
             const float wm = value_of(__reduce_max_sync(0xFFFFFFFFu, tau_of(big)));
             int at = INT_MAX, own = -1;
-            if (big == wm) {
-#pragma unroll
-                for (int u = AHEAD - 1; u >= 0; --u) {
-                    float e[E];
-                    L::spread(ring[u], e);
-#pragma unroll
-                    for (int j = E - 1; j >= 0; --j)
-                        if (e[j] == wm) own = u * E + j;
-                }
-                at = (base + own / E * kThreads) * E - skew + own % E;
-            }
+            if (big == wm) where(base, wm, own, at);
             const int first_at = __reduce_min_sync(0xFFFFFFFFu, at);
             if (at != first_at) own = -1;
-            const bool none = st.best == -CUDART_INF_F;
-            const float d = none ? 0.f : max_nan((st.best - wm) * c2, -1000.f), f = none ? 0.f : exp2_fast(d);
+            const bool none = st.ref == -CUDART_INF_F;
+            const float d = none ? 0.f : max_nan((st.ref - wm) * c2, -1000.f), f = none ? 0.f : exp2_fast(d);
             if (!plain) settle();
+            if (lane == 0 && st.own != INT_MAX) s2.x += 1.f;
             // f = 0 keeps a NaN that the sums hold
             t2 = make_float2(f * (t2.x + d * s2.x), f * (t2.y + d * s2.y));
             s2 = make_float2(f * s2.x, f * s2.y);
-            if (lane == 0) s2.x += f, t2.x += f * d;
-            st.best = wm, st.best_i = first_at;
-            shift = -wm * c2, lag = fmaf(-wm, c2, -shift);
-            const float cut = wm - 160.f / c2;
-            plain = !(fabsf(shift) < 1e37f) || !(cut > -1e37f) || !(wm < 1e37f);
-            low = L::below(cut);
+            st.own = first_at;
+            refer(wm);
             excluded = own;
         }
-        gate = st.best;
+        gate = st.ref;
         if (K > 0) {  // ---- the list ----
             const float kth = __shfl_sync(0xFFFFFFFFu, mine.x, K - 1);
             const float floor = value_of(*reinterpret_cast<volatile int*>(&sm_tau));
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
             // a logit equal to another warp's K-th may still be ahead of it, one equal to this warp's not
             const int fb = __float_as_int(floor);
             const float below = floor == -CUDART_INF_F ? floor : floor == 0.f ? -1.4012985e-45f : __int_as_float(fb > 0 ? fb - 1 : fb + 1);
-            gate = fminf(fmaxf(now, below), st.best);
+            gate = fminf(fmaxf(now, below), st.ref);
         }
     };
 
@@ -418,23 +426,33 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
 #pragma unroll
                 for (int u = 0; u < AHEAD; ++u) ring[u] = load(base + u * kThreads);
             }
-            if (K > 0) {
-                // A first gate: each warp holds ceil(K / 8) lanes whose largest logit is at least t, so the least t of
-                // the warps is not above the K-th best logit of the CTA.
-                uint32_t most = L::largest2(ring[0]);
+            // The CTA's largest logit so far is what its other warps refer to at first: each with its own largest, they
+            // would have to move it some three times more. And a first gate for the lists: each warp holds
+            // ceil(K / 8) lanes whose largest logit is at least t, so the least t of the warps is not above the K-th
+            // best logit of the CTA.
+            uint32_t most = L::largest2(ring[0]);
 #pragma unroll
-                for (int u = 1; u < AHEAD; ++u) most = L::larger(most, L::largest2(ring[u]));
-                int big = tau_of(L::value(most)), t = kNoTau;
-                for (int r = 0; r < (K + kWarps - 1) / kWarps; ++r) {
-                    t = __reduce_max_sync(0xFFFFFFFFu, big);
-                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, big == t);
-                    if (lane == __ffs(who) - 1) big = kNoTau;
-                }
-                if (lane == 0) atomicMin(&sm_seed, t);
-                __syncthreads();
-                if (tid == 0) atomicMax(&sm_tau, sm_seed);
-                __syncthreads();
+            for (int u = 1; u < AHEAD; ++u) most = L::larger(most, L::largest2(ring[u]));
+            const float big = L::value(most);
+            int o = tau_of(big), t = __reduce_max_sync(0xFFFFFFFFu, o);
+            const int top = t;
+            for (int r = 1; r < (K + kWarps - 1) / kWarps; ++r) {
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, o == t);
+                if (lane == __ffs(who) - 1) o = kNoTau;
+                t = __reduce_max_sync(0xFFFFFFFFu, o);
             }
+            if (lane == 0) {
+                atomicMax(&sm_ref, top);
+                if (K > 0) atomicMin(&sm_seed, t);
+            }
+            __syncthreads();
+            const int ref = sm_ref;
+            if (tid == 0 && K > 0) atomicMax(&sm_tau, sm_seed);
+            if (top != ref && st.ref == -CUDART_INF_F) {
+                refer(value_of(ref));
+                if (K == 0) gate = st.ref;
+            }
+            __syncthreads();
         }
         const int step = phase == 1 ? tid : 0;
 #pragma unroll 1
@@ -452,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
             if (__any_sync(0xFFFFFFFFu, L::value(most) > gate)) past_gate(base, L::value(most), excluded);
             if (plain) {
                 for (int j = 0; j < AHEAD * E; ++j) {
-                    const float ref = st.best == -CUDART_INF_F ? 0.f : st.best;
+                    const float ref = st.ref == -CUDART_INF_F ? 0.f : st.ref;
                     const float y = j == excluded ? -1000.f : max_nan((pick(j) - ref) * c2, -1000.f), p = exp2_fast(y);
                     s2.x += p, t2.x = fmaf(p, y, t2.x);
                 }
@@ -488,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     auto joined = [&](Stats sum, int n) {
         for (int o = n / 2; o > 0; o >>= 1) {
             Stats q;
-            q.best = __shfl_xor_sync(0xFFFFFFFFu, sum.best, o), q.best_i = __shfl_xor_sync(0xFFFFFFFFu, sum.best_i, o);
+            q.ref = __shfl_xor_sync(0xFFFFFFFFu, sum.ref, o), q.own = __shfl_xor_sync(0xFFFFFFFFu, sum.own, o);
             q.s = __shfl_xor_sync(0xFFFFFFFFu, sum.s, o), q.t = __shfl_xor_sync(0xFFFFFFFFu, sum.t, o);
             q.before = __shfl_xor_sync(0xFFFFFFFFu, sum.before, o);
             merge(sum, q, c2);
@@ -543,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
             Stats sum = {-CUDART_INF_F, INT_MAX, 0.f, 0.f, 0};
             for (int p = lane; p < split; p += 32) {
                 Stats q;
-                q.best = __ldcg(&of[p].st.best), q.best_i = __ldcg(&of[p].st.best_i), q.s = __ldcg(&of[p].st.s);
+                q.ref = __ldcg(&of[p].st.ref), q.own = __ldcg(&of[p].st.own), q.s = __ldcg(&of[p].st.s);
                 q.t = __ldcg(&of[p].st.t), q.before = __ldcg(&of[p].st.before);
                 merge(sum, q, c2);
             }
@@ -571,11 +589,11 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     }
 
     if (warp != 0) return;
-    const bool none = all.best == -CUDART_INF_F;
-    const float s = all.s + (none ? 0.f : all.best - all.best);  // plus infinity gives NaN
+    const bool none = all.ref == -CUDART_INF_F;
+    const float s = all.s + (none ? 0.f : all.ref - all.ref);  // plus infinity gives NaN
     const float lse = log1pf(s);
     if (tid == 0) {
-        if (a.logprob) a.logprob[row] = target < 0 ? 0.f : none ? -CUDART_INF_F + s : (xt - all.best) * a.scale - lse;
+        if (a.logprob) a.logprob[row] = target < 0 ? 0.f : none ? -CUDART_INF_F + s : (xt - all.ref) * a.scale - lse;
         if (a.rank) a.rank[row] = target < 0 ? 0 : 1 + all.before + (dead ? target : 0);
         if (a.entropy) a.entropy[row] = none ? s : lse - kLn2 * all.t / (1.f + s);
     }
@@ -583,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         const Cand c = sm_top[tid];
         const bool no = c.i == INT_MAX;
         if (a.top_ids) a.top_ids[(int64_t)row * K + tid] = no ? -1 : c.i;
-        if (a.top_logprobs) a.top_logprobs[(int64_t)row * K + tid] = no ? -CUDART_INF_F + s : (c.x - all.best) * a.scale - lse;
+        if (a.top_logprobs) a.top_logprobs[(int64_t)row * K + tid] = no ? -CUDART_INF_F + s : (c.x - all.ref) * a.scale - lse;
     }
 }
 
