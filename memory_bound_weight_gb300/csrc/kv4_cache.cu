@@ -42,6 +42,18 @@ __device__ __forceinline__ float rot_exact(float a, float c, float b, float s) {
     return x == x ? x : h;  // an infinity stays one: the remainders of infinite products are NaN
 }
 
+// The same for two values of a query, which are only rounded: a c + b s with the second product's remainder taken
+// along (Kahan's form; Jeannerod, Louvet and Muller 2013: at most 1.5 ulp off), in pairs of fp32: five instructions
+// for two values, where rot_exact takes twenty-six. NaN for an infinity, as its scores would be.
+__device__ __forceinline__ void rot_near2(const float* a, const float* c, const float* b, const float* s, float* z) {
+    asm("{.reg .b64 a, c, b, s, n, w, m, e;\n"
+        " mov.b64 a, {%2, %3};\n mov.b64 c, {%4, %5};\n mov.b64 b, {%6, %7};\n mov.b64 s, {%8, %9};\n mov.b64 n, {%10, %11};\n"
+        " mul.rn.f32x2 w, b, s;\n mul.rn.f32x2 m, b, n;\n"   // the product and its negative
+        " fma.rn.f32x2 e, b, s, m;\n fma.rn.f32x2 w, a, c, w;\n add.rn.f32x2 w, w, e;\n mov.b64 {%0, %1}, w;}"
+        : "=f"(z[0]), "=f"(z[1])
+        : "f"(a[0]), "f"(a[1]), "f"(c[0]), "f"(c[1]), "f"(b[0]), "f"(b[1]), "f"(s[0]), "f"(s[1]), "f"(-s[0]), "f"(-s[1]));
+}
+
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -51,6 +63,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+
+// Page and place of a slot; 32-bit division where it does.
+__device__ __forceinline__ int64_t page_of(int64_t slot, int page_size, int& place) {
+    const int64_t page = slot >> 32 ? slot / page_size : (int64_t)((uint32_t)slot / (uint32_t)page_size);
+    place = (int)(slot - page * page_size);
+    return page;
 }
 
 __device__ __forceinline__ void unpack8(uint4 v, float* x) {
@@ -91,12 +110,17 @@ __device__ __forceinline__ uint32_t quantize8(const float* x, uint32_t& meta) {
     const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, m), 15.0f));
     const float s = __half2float(sh);
     meta = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(mh) << 16);
+    // (x - m) / s, correctly rounded, as Markstein (IBM J. Res. Dev. 1990) gets it from the correctly rounded
+    // reciprocal: q = d r, q + (d - q s) r. One reciprocal for eight quotients. (Where s is infinite or no number, so
+    // is the group's value, whatever its codes.)
+    const float r = s != 0.f ? __frcp_rn(s) : 0.f;
+    // Clamped before it is rounded, which gives the same; 1.5 2^23 more puts the rounded value into the low bits.
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float n = 0.f;
-        if (s != 0.f) n = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], m), s)), 0.f), 15.f);
-        codes |= (uint32_t)n << (4 * i);
+        const float d = __fsub_rn(x[i], m), q = __fmul_rn(d, r);
+        const float n = fminf(fmaxf(__fmaf_rn(__fmaf_rn(-q, s, d), r, q), 0.f), 15.f);
+        codes |= (__float_as_uint(__fadd_rn(n, 12582912.f)) & 15u) << (4 * i);
     }
     return codes;
 }
@@ -114,20 +138,36 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t v, int lane) {
 }
 
 // One thread holds 8 dimensions of a head row, D / 8 neighbouring lanes a row;
-// a CTA takes one token and `rows` of its Hq + 2 Hkv rows from row0 on.
+// a CTA, or each of its warps, takes one token and `rows` of its Hq + 2 Hkv
+// rows from row0 on.
 template <int D, int G>
-__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendArgs a, int rows) {
-    constexpr int LPR = D / 8, SLOTS = kAppendThreads / LPR;
+__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendArgs a, int rows, int tokens) {
+    constexpr int LPR = D / 8;
+    const int SLOTS = kAppendThreads / LPR / tokens;  // rows at a time
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 31, l = threadIdx.x % LPR, sub = threadIdx.x / LPR;
+    const int tid = tokens > 1 ? threadIdx.x & 31 : threadIdx.x;  // among the token's threads
+    const int64_t t = (int64_t)blockIdx.x * tokens + (tokens > 1 ? threadIdx.x >> 5 : 0);
+    if (t >= a.T) return;  // a whole warp
+    const int lane = threadIdx.x & 31, l = threadIdx.x % LPR, sub = tid / LPR;
     const int total = a.q_heads + 2 * a.kv_heads;
     const int row0 = blockIdx.y * rows, row1 = min(row0 + rows, total);
 
+    // One row of each slot at a time, the next one's load under way: queries, then keys and values.
+    const int q1 = min(row1, a.q_heads), kv0 = max(row0, a.q_heads) - a.q_heads, kv1 = row1 - a.q_heads;
+    const uint16_t* q_at = a.q + t * a.q_stride + 8 * l;
+    uint16_t* q_to = a.q_out + t * a.q_out_stride + 8 * l;
+    const uint16_t* k_at = a.k + t * a.k_stride + 8 * l;  // row r < kv_heads, then the values' rows
+    const uint16_t* v_at = a.v + t * a.v_stride - (int64_t)a.kv_heads * D + 8 * l;
+    auto load_q = [&](int r) { return r < q1 ? *reinterpret_cast<const uint4*>(q_at + r * D) : make_uint4(0, 0, 0, 0); };
+    auto load_kv = [&](int r) {
+        return r < kv1 ? *reinterpret_cast<const uint4*>((r < a.kv_heads ? k_at : v_at) + r * D) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 q_next = load_q(row0 + sub), kv_next = load_kv(kv0 + sub);
+
     int64_t slot = a.slots[t];
     if (slot >= a.num_slots) {
-        if (threadIdx.x == 0) atomicExch(&g_kv4_cache_range, 1);
+        if (tid == 0) atomicExch(&g_kv4_cache_range, 1);
         slot = -1;
     }
     // cos and sin of the lane's 8 dimensions; sin carries the sign of its term
@@ -137,7 +177,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendArg
     if (a.cos_sin) {
         int64_t pos = a.positions[t];
         if (pos < 0 || pos >= a.max_pos) {
-            if (threadIdx.x == 0) atomicExch(&g_kv4_cache_range, 1);
+            if (tid == 0) atomicExch(&g_kv4_cache_range, 1);
             pos = 0;
         }
         const float* cs = a.cos_sin + pos * a.rotary;
@@ -167,92 +207,106 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendArg
             }
         }
     }
-    const int64_t page = slot < 0 ? 0 : slot / a.page_size;
-    const int in_page = slot < 0 ? 0 : (int)(slot - page * a.page_size);
+    int in_page;
+    const int64_t page = page_of(slot < 0 ? 0 : slot, a.page_size, in_page);
     const int tok = in_page & 15, nblk = a.page_size / 16;
 
-    for (int r0 = row0; r0 < row1; r0 += SLOTS) {  // uniform over the warp: the shuffles below need every lane
-        const int r = r0 + sub;
-        const bool on = r < row1;
-        const int kind = r < a.q_heads ? 0 : r < a.q_heads + a.kv_heads ? 1 : 2;
-        const int h = kind == 0 ? r : kind == 1 ? r - a.q_heads : r - a.q_heads - a.kv_heads;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (on) {
-            const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-            raw = *reinterpret_cast<const uint4*>(src + (int64_t)h * D + 8 * l);
+    const int from = lane - l % 32 + partner;  // LPR <= 32 and rows start at multiples of LPR
+    // The row's other components of the lane's pairs; every lane of the warp takes part.
+    auto partners = [&](uint4 raw, const float* x, float* y) {
+        if (a.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+        } else {
+            raw.x = __shfl_sync(0xFFFFFFFFu, raw.x, from);
+            raw.y = __shfl_sync(0xFFFFFFFFu, raw.y, from);
+            raw.z = __shfl_sync(0xFFFFFFFFu, raw.z, from);
+            raw.w = __shfl_sync(0xFFFFFFFFu, raw.w, from);
+            unpack8(raw, y);
         }
-        uint4 other;
-        const int from = (lane - l % 32) + partner;  // LPR <= 32 and rows start at multiples of LPR
-        other.x = __shfl_sync(0xFFFFFFFFu, raw.x, from);
-        other.y = __shfl_sync(0xFFFFFFFFu, raw.y, from);
-        other.z = __shfl_sync(0xFFFFFFFFu, raw.z, from);
-        other.w = __shfl_sync(0xFFFFFFFFu, raw.w, from);
+    };
+    for (int r0 = row0; r0 < q1; r0 += SLOTS) {  // the same for a token's threads: the shuffles need every lane
+        const int r = r0 + sub;
+        uint4 raw = q_next;
+        q_next = load_q(r + SLOTS);
+        if (a.cos_sin) {
+            float x[8], y[8], z[8];
+            unpack8(raw, x);
+            partners(raw, x, y);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) rot_near2(x + i, c + i, y + i, s + i, z + i);
+            if (rotated) raw = pack8(z);
+        }
+        if (r < q1) *reinterpret_cast<uint4*>(q_to + r * D) = raw;
+    }
+    for (int r0 = kv0; r0 < kv1; r0 += SLOTS) {
+        const int r = r0 + sub;
+        uint4 raw = kv_next;
+        kv_next = load_kv(r + SLOTS);
+        const bool key = r < a.kv_heads;
         float x[8];
         unpack8(raw, x);
-        if (kind < 2 && rotated) {
+        if (a.cos_sin && r0 < a.kv_heads) {
             float y[8], z[8];
-            unpack8(other, y);
+            partners(raw, x, y);
+            if (key && rotated) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = rot_exact(x[i], c[i], a.interleaved ? x[i ^ 1] : y[i], s[i]);
-            raw = pack8(z);
-            unpack8(raw, x);
+                for (int i = 0; i < 8; ++i) z[i] = rot_exact(x[i], c[i], y[i], s[i]);
+                unpack8(pack8(z), x);
+            }
         }
         uint32_t meta;
-        uint32_t codes = quantize8<G>(x, meta);
+        const uint32_t codes = quantize8<G>(x, meta);
         const uint32_t turned = transpose_nibbles(codes, lane);
-        if (!on) continue;
-        if (kind == 0) {
-            *reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + (int64_t)h * D + 8 * l) = raw;
-        } else if (slot >= 0) {
-            uint8_t* blk = a.pages + ((page * a.kv_heads + h) * nblk + in_page / 16) * (int64_t)kv4_block_bytes(D, G);
-            if (kind == 1)
-                *reinterpret_cast<uint32_t*>(blk + kv4_k_word(D, tok, l)) = codes;
-            else
-                *reinterpret_cast<uint32_t*>(blk + kv4_v_word(D, tok, l % 8, l / 8)) = turned;
-            if (l % (G / 8) == 0) *reinterpret_cast<uint32_t*>(blk + kv4_meta(D, G, tok, l / (G / 8), kind - 1)) = meta;
+        if (r < kv1 && slot >= 0) {
+            uint8_t* blk = a.pages + ((page * a.kv_heads + (key ? r : r - a.kv_heads)) * nblk + in_page / 16) *
+                                         (int64_t)kv4_block_bytes(D, G);
+            *reinterpret_cast<uint32_t*>(blk + (key ? kv4_k_word(D, tok, l) : kv4_v_word(D, tok, l % 8, l / 8))) = key ? codes : turned;
+            if (l % (G / 8) == 0) *reinterpret_cast<uint32_t*>(blk + kv4_meta(D, G, tok, l / (G / 8), !key)) = meta;
         }
     }
 }
 
-// One thread per 8 dimensions of one (token, head): K from its word, V from the
-// eight words that hold its dimensions.
+// One thread per 8 dimensions of one (token, head): K from its word; V's words are read one a lane and transposed
+// over 8 lanes, as they were written.
 template <int D, int G>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(Kv4GatherArgs a) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr int LPR = D / 8;
     const int64_t n = a.T * a.kv_heads * LPR;
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        const int l = (int)(i % LPR);
-        const int64_t row = i / LPR;  // token * kv_heads + head
-        const int64_t t = row / a.kv_heads;
+    const int lane = threadIdx.x & 31;
+    for (int64_t i0 = blockIdx.x * (int64_t)blockDim.x; i0 < n; i0 += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t i = i0 + threadIdx.x;
+        const bool on = i < n;  // whole rows of lanes: n is a multiple of LPR
+        const int l = threadIdx.x % LPR;
+        const int64_t row = on ? i / LPR : 0;  // token * kv_heads + head
+        const int64_t t = row >> 32 ? row / a.kv_heads : (int64_t)((uint32_t)row / (uint32_t)a.kv_heads);
         const int h = (int)(row - t * a.kv_heads);
         int64_t slot = a.slots[t];
         if (slot >= a.num_slots) {
             atomicExch(&g_kv4_cache_range, 1);
             slot = -1;
         }
+        int in_page;
+        const int64_t page = page_of(slot < 0 ? 0 : slot, a.page_size, in_page);  // a padding token reads slot 0 and drops it
+        const int tok = in_page & 15;
+        const uint8_t* blk = a.pages + ((page * a.kv_heads + h) * (a.page_size / 16) + in_page / 16) *
+                                           (int64_t)kv4_block_bytes(D, G);
+        const float2 mk = kv4_pair(*reinterpret_cast<const uint32_t*>(blk + kv4_meta(D, G, tok, 8 * l / G, 0)));
+        const float2 mv = kv4_pair(*reinterpret_cast<const uint32_t*>(blk + kv4_meta(D, G, tok, 8 * l / G, 1)));
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(blk + kv4_k_word(D, tok, l));
+        const uint32_t vw = transpose_nibbles(*reinterpret_cast<const uint32_t*>(blk + kv4_v_word(D, tok, l % 8, l / 8)), lane);
         float k[8], v[8];
-        if (slot < 0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) k[j] = v[j] = 0.f;
-        } else {
-            const int64_t page = slot / a.page_size;
-            const int in_page = (int)(slot - page * a.page_size), tok = in_page & 15;
-            const uint8_t* blk = a.pages + ((page * a.kv_heads + h) * (a.page_size / 16) + in_page / 16) *
-                                               (int64_t)kv4_block_bytes(D, G);
-            const float2 mk = kv4_pair(*reinterpret_cast<const uint32_t*>(blk + kv4_meta(D, G, tok, 8 * l / G, 0)));
-            const float2 mv = kv4_pair(*reinterpret_cast<const uint32_t*>(blk + kv4_meta(D, G, tok, 8 * l / G, 1)));
-            const uint32_t kw = *reinterpret_cast<const uint32_t*>(blk + kv4_k_word(D, tok, l));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t vw = *reinterpret_cast<const uint32_t*>(blk + kv4_v_word(D, tok, j, l / 8));
-                k[j] = fmaf(mk.x, (float)((kw >> (4 * j)) & 15u), mk.y);
-                v[j] = fmaf(mv.x, (float)((vw >> (4 * (l % 8))) & 15u), mv.y);
-            }
+        for (int j = 0; j < 8; ++j) {
+            k[j] = slot < 0 ? 0.f : fmaf(mk.x, (float)((kw >> (4 * j)) & 15u), mk.y);
+            v[j] = slot < 0 ? 0.f : fmaf(mv.x, (float)((vw >> (4 * j)) & 15u), mv.y);
         }
-        *reinterpret_cast<uint4*>(a.k + row * D + 8 * l) = pack8(k);
-        *reinterpret_cast<uint4*>(a.v + row * D + 8 * l) = pack8(v);
+        if (on) {
+            *reinterpret_cast<uint4*>(a.k + row * D + 8 * l) = pack8(k);
+            *reinterpret_cast<uint4*>(a.v + row * D + 8 * l) = pack8(v);
+        }
     }
 }
 
@@ -278,11 +332,20 @@ cudaError_t launch_pdl(F* fn, dim3 grid, int threads, cudaStream_t s, const A& a
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
-    const int slots = kAppendThreads / (a.head_dim / 8);
+    // Few tokens: a CTA of 4 warps takes the rows it holds at a time, so that a token is done soonest. Many: one warp
+    // takes a whole token, and what is done once per token and thread is done for all its rows (8192 tokens of 28 + 8
+    // rows: 1030 instructions a warp and 4 warps a token become some 2800).
     const int total = a.q_heads + 2 * a.kv_heads;
-    const int groups = (total + slots - 1) / slots;
+    const int tokens = a.T >= (int64_t)device_sm_count() * 16 ? kAppendThreads / 32 : 1;
+    const int slots = kAppendThreads / (a.head_dim / 8);
+    int rows = slots;
+    if (tokens > 1)
+        rows = total;
+    else
+        while (rows < total && a.T * ((total + rows - 1) / rows) > (int64_t)device_sm_count() * 16) rows += slots;
+    const int groups = (total + rows - 1) / rows;
     auto fn = KV4_FOR(a.head_dim, a.group, kv4_append_kernel);
-    return launch_pdl(fn, dim3((unsigned)a.T, (unsigned)groups), kAppendThreads, s, a, slots);
+    return launch_pdl(fn, dim3((unsigned)((a.T + tokens - 1) / tokens), (unsigned)groups), kAppendThreads, s, a, rows, tokens);
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s) {
