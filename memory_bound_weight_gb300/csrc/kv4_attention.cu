@@ -33,14 +33,19 @@
 // per pair and an OR into 16 + n, and with HADD2 to n - 8.
 //
 // Work. A block of 16 tokens of one KV head is 2304 bytes in one piece (D =
-// 128, G = 64), read once; each warp streams blocks of its own through a ring
-// of shared memory (cp.async) with its own softmax state. The grid is one wave;
-// the blocks of all (request, KV head, query tile) items are one line, cut
-// into equal shares (each CTA derives the same cut from the lengths on the
-// device), so ragged batches and single long contexts load every SM alike. An
-// item cut between CTAs leaves its parts in the workspace, and the CTA that
-// arrives last joins them in their order, so the result does not depend on who
-// that is.
+// 128, G = 64), read once; each warp streams blocks through a ring of shared
+// memory of its own (cp.async) with its own softmax state. The blocks of all
+// (request, KV head, query tile) items are one line, cut into equal shares for
+// the workers of a one-wave grid, each item lengthened by what an item costs
+// besides its blocks. The cut is made on the device from the lengths, so a
+// captured call follows them. An item cut between workers leaves its parts in
+// the workspace, and the worker that arrives last joins them in their order, so
+// that the result does not depend on who that is.
+//   Many items: each warp is a worker, and no warp waits for another. (With the
+// four warps of a CTA as one worker, joining them at every item, 64 requests of
+// 300 to 16000 tokens took 82 us.)
+//   Few items, each cut many times: a CTA of 16 warps is one, and its warps are
+// joined in shared memory, so that fewer parts go through the workspace.
 #include <cuda_runtime.h>
 
 #include <math_constants.h>
@@ -110,48 +115,76 @@ __device__ __forceinline__ void load_meta(const uint8_t* p, uint32_t* m) {
 }
 
 struct Request {
-    int q0, nq, ctx, fb, units, qt;
-    long long cost;  // units of all its items
+    int q0, nq, ctx;  // its queries and its length
+    int fb;           // first block that a query sees
+    uint32_t units;   // of the line
+    uint32_t tiles;   // items: KV heads x query tiles
+    int qt;           // query tiles
 };
 
-template <int D, int G, int NT, int NW, int NB, int DEPTH>
+// COOP: the NW warps of a CTA are one worker; else each warp is.
+template <int D, int G, int NT, int NW, int NB, int DEPTH, bool COOP>
 struct Shape {
     static constexpr int NG = D / G, J = D / 32, BB = kv4_block_bytes(D, G), ROWS = 8 * NT;
-    static constexpr int U = NW * NB;  // blocks of a unit: one step of every warp
+    static constexpr int WORKERS = COOP ? 1 : NW;       // of a CTA
+    static constexpr int STEP = (COOP ? NW : 1) * NB;   // blocks that a worker takes at a time
     static constexpr int STAGE = NB * BB, RING = NW * DEPTH * STAGE;
-    static constexpr int PAD = 68;  // floats of a merge row: 64 dimensions, 4 to spread the banks
-    static constexpr int MERGE = NW * 8 * PAD * 4;
-    static constexpr int QS = NT > 1 ? J * NT * 512 : 0;
-    static constexpr int QSUM = NT > 1 ? (NG + 1) * ROWS * 4 : 0;
-    static constexpr int SMEM = RING + MERGE + QS + QSUM + 2 * NW * ROWS * 4;
-    static constexpr int MOST = RING / (4 * ROWS) - 2;  // most parts whose factors the drained ring holds
-    static constexpr int PART = ROWS * (D + 2);  // floats of a part: rows of D, then M and L of each
+    static constexpr int PAD = D + 4;  // floats of a row that warps are joined in: 4 to spread the banks
+    static constexpr int QS = NT > 1 ? WORKERS * J * NT * 512 : 0;
+    static constexpr int QSUM = NT > 1 ? WORKERS * (NG + 1) * ROWS * 4 : 0;
+    static constexpr int JOIN = COOP ? NW * 8 * PAD * 4 : 0;  // over the ring, which is drained then
+    static constexpr int BUF = RING > JOIN ? RING : JOIN;
+    static constexpr int SMEM = BUF + QS + QSUM + (COOP ? 2 * (NW + 1) * ROWS * 4 : 0) + (NW * 32 + 1) * 4;
+    static constexpr int PART = ROWS * (D + 2);  // floats of a part: its sums, then m and l of each row
 };
 
-template <int D, int G, int NT, int NW, int NB, int DEPTH, int OCC>
-__global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs a, int split) {
-    using S = Shape<D, G, NT, NW, NB, DEPTH>;
+// The workspace begins with a counter of finished parts per worker; an item cut between workers has that of its first.
+constexpr int kCounters = 4096;
+
+template <int D, int G, int NT, int NW, int NB, int DEPTH, int OCC, bool COOP>
+__global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs a, int split, int shift) {
+    using S = Shape<D, G, NT, NW, NB, DEPTH, COOP>;
     constexpr int NG = S::NG, J = S::J, BB = S::BB, ROWS = S::ROWS, THREADS = NW * 32, NV = D / 64;
     // V's codes as they are and 8 sum w from a constant tile; or, where several n-tiles share their unpacking, n - 8
     constexpr bool RAW = NT == 1;
+    // What an item costs besides its blocks, and the least share of a worker, in units: below it the parts' way through
+    // the workspace takes longer than the blocks.
+    constexpr uint32_t EXTRA = COOP ? 1 : 2, LEAST = COOP ? 4 : 6;
     extern __shared__ __align__(16) uint8_t smem[];
-    float* buf = reinterpret_cast<float*>(smem + S::RING);  // [NW][8][PAD]
-    uint4* qs = reinterpret_cast<uint4*>(smem + S::RING + S::MERGE);
-    float* qsums = reinterpret_cast<float*>(smem + S::RING + S::MERGE + S::QS);
-    float* sm_m = reinterpret_cast<float*>(smem + S::RING + S::MERGE + S::QS + S::QSUM);
-    float* sm_l = sm_m + NW * ROWS;
-    __shared__ long long sh_scan[NW + 1];
-    __shared__ long long sh_found[2];
-    __shared__ int sh_last[2];
-
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int own = COOP ? 0 : warp;  // the worker in the CTA
+    uint4* qs = reinterpret_cast<uint4*>(smem + S::BUF) + own * J * NT * 32;
+    float* qsums = reinterpret_cast<float*>(smem + S::BUF + S::QS) + own * (NG + 1) * ROWS;
+    float* sm_m = reinterpret_cast<float*>(smem + S::BUF + S::QS + S::QSUM);  // [NW + 1][ROWS], the last joined
+    float* sm_l = sm_m + (NW + 1) * ROWS;
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + S::SMEM) - (THREADS + 1);  // of the line, per thread's requests
+    struct Pending {  // an item of which the worker wrote a part
+        int q0, nq, h, f0;
+        uint32_t first, n;
+    };
+    __shared__ Pending sh_pend[S::WORKERS][2];  // one that begins before the worker's share, one that begins within
+    __shared__ uint32_t sh_scan[NW], sh_items[NW];
+    __shared__ uint32_t sh_last[S::WORKERS][2];
+    auto sync = [&]() {  // the worker's threads
+        if (COOP)
+            __syncthreads();
+        else
+            __syncwarp();
+    };
+
     const int gq = a.q_heads / a.kv_heads, bpp = a.page_size / 16;
     const float sl2 = fabsf(a.scale) * 1.44269504088896340736f;
+    uint32_t* counters = static_cast<uint32_t*>(a.workspace);
+    float* parts = reinterpret_cast<float*>(counters + kCounters);
     bool bad = false;
+    if ((COOP ? tid : lane) < 2) sh_pend[own][COOP ? tid : lane].n = 0;
 
     pdl_launch_dependents();
     pdl_wait();
 
+    // ---- the line: per item, EXTRA and its units of STEP << shift blocks ----
+    const int unit = S::STEP << shift;
+    const int cap = a.table_width * a.page_size;  // at most MBW_MAX_DIM
     auto request = [&](int b) {
         Request r;
         int q0, q1;
@@ -164,132 +197,81 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             const int n = a.T / a.B;
             q0 = b * n, q1 = q0 + n;
         }
-        const long long cap = (long long)a.table_width * a.page_size;
         int ctx = max(a.ctx_lens[b], 0);
-        if (ctx > cap) bad = true, ctx = (int)cap;
+        if (ctx > cap) bad = true, ctx = cap;
         r.q0 = q0, r.nq = q1 - q0, r.ctx = ctx;
         r.fb = a.window ? max(0, ctx - r.nq - a.window + 1) / 16 : 0;
-        const int nblk = (ctx + 15) / 16 - r.fb;
-        r.units = max(1, (nblk + S::U - 1) / S::U);
-        r.qt = (int)(((long long)r.nq * gq + ROWS - 1) / ROWS);
-        r.cost = (long long)r.units * r.qt * a.kv_heads;
+        r.units = max(1u, ((uint32_t)((ctx + 15) / 16 - r.fb) + unit - 1) / unit);
+        r.qt = ((uint32_t)r.nq * gq + ROWS - 1) / ROWS;  // at most MBW_MAX_DIM query rows
+        r.tiles = (uint32_t)r.qt * a.kv_heads;
         return r;
     };
-    // exclusive prefix of v over the CTA's threads, and the total
-    auto scan = [&](long long v, long long& total) {
-        long long x = v;
+    const int stride = (a.B + THREADS - 1) / THREADS;  // requests per thread
+    uint32_t W, items = 0;
+    {
+        uint32_t x = 0, n = 0;
+        for (int i = 0; i < stride; ++i) {
+            const int b = tid * stride + i;
+            if (b < a.B) {
+                const Request r = request(b);
+                x += r.tiles * (r.units + EXTRA), n += r.tiles;
+            }
+        }
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        uint32_t sum = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-            if (lane >= o) x += y;
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += y;
         }
+        if (lane == 31) sh_scan[warp] = sum, sh_items[warp] = n;
         __syncthreads();
-        if (lane == 31) sh_scan[warp] = x;
-        __syncthreads();
-        long long before = 0;
-        total = 0;
+        uint32_t before = 0;
+        W = 0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            if (w < warp) before += sh_scan[w];
-            total += sh_scan[w];
+            const uint32_t y = sh_scan[w];
+            if (w < warp) before += y;
+            W += y, items += sh_items[w];
         }
-        return before + x - v;
-    };
-
-    // ---- this CTA's share [u0, u1) of the units of all items ----
-    long long W = 0, mine = 0, excl = 0;
-    for (int base = 0; base < a.B; base += THREADS) {
-        mine = base + tid < a.B ? request(base + tid).cost : 0;
-        long long total;
-        excl = scan(mine, total);
-        W += total;
-    }
-    const long long C = W < gridDim.x ? W : gridDim.x;
-    if ((long long)blockIdx.x >= C) {
-        if (bad) atomicExch(&g_kv4_attn_range, 1);
-        return;
-    }
-    const long long u0 = (long long)blockIdx.x * W / C, u1 = ((long long)blockIdx.x + 1) * W / C;
-    {
-        long long run = 0;
-        for (int base = 0; base < a.B; base += THREADS) {
-            long long total = W;
-            if (a.B > THREADS) {
-                mine = base + tid < a.B ? request(base + tid).cost : 0;
-                excl = scan(mine, total);
-            }
-            if (u0 >= run + excl && u0 < run + excl + mine) sh_found[0] = base + tid, sh_found[1] = run + excl;
-            run += total;
-            if (run > u0) break;  // the same for every thread
-        }
+        prefix[tid] = before + sum - x;
+        if (tid == 0) prefix[THREADS] = W;
         __syncthreads();
     }
-    int b = (int)sh_found[0];
-    long long start = sh_found[1];  // units before request b
-    Request rq = request(b);
-
-    // ---- segments: what this CTA takes of one item ----
-    struct Segment {
-        int q0, nq, ctx, h, f0;   // the request's queries and length, KV head, first query row of the tile
-        int bs, be, nsteps;       // blocks, and this warp's steps over them
-        int pos_lo, pos_hi;       // positions of the tile's first and last query
-        bool whole;               // the item is this CTA's alone
-        long long iu0;            // the item's first unit
-        int units;
-        const int32_t* table;
+    // as many workers as items at least; worker i of C has the places [i each + min(i, rest), ...)
+    const uint32_t all = gridDim.x * S::WORKERS, C = max(1u, min(all, max(items, W / LEAST))), each = W / C, rest = W - each * C;
+    const uint32_t me = COOP ? blockIdx.x : warp * gridDim.x + blockIdx.x;  // neighbours on different SMs
+    auto start_of = [&](uint32_t i) { return i * each + min(i, rest); };
+    auto owner_of = [&](uint32_t p) {
+        const uint32_t big = rest * (each + 1);
+        return p < big ? p / (each + 1) : rest + (p - big) / each;
     };
-    long long u = u0;
-    auto next_segment = [&](Segment& sg) {
-        while (u < u1) {
-            while (u >= start + rq.cost) {
-                start += rq.cost;
-                rq = request(++b);
-            }
-            const long long item = (u - start) / rq.units, iu0 = start + item * rq.units;
-            const int s0 = (int)(u - iu0);
-            int s1 = rq.units;
-            if (split) {
-                if (u1 - iu0 < s1) s1 = (int)(u1 - iu0);
-            } else if (s0 != 0) {  // its first unit is another CTA's, and so is the item
-                u = iu0 + rq.units;
-                continue;
-            }
-            u = iu0 + s1;
-            sg.q0 = rq.q0, sg.nq = rq.nq, sg.ctx = rq.ctx, sg.iu0 = iu0, sg.units = rq.units;
-            sg.h = (int)(item / rq.qt), sg.f0 = (int)(item % rq.qt) * ROWS;
-            sg.whole = s0 == 0 && s1 == rq.units;
-            const int i_last = min(rq.nq - 1, (sg.f0 + ROWS - 1) / gq);
-            sg.pos_lo = rq.ctx - rq.nq + sg.f0 / gq, sg.pos_hi = rq.ctx - rq.nq + i_last;
-            const int k_lo = a.window ? max(0, sg.pos_lo - a.window + 1) : 0;
-            sg.bs = max(rq.fb + s0 * S::U, k_lo / 16);
-            sg.be = max(sg.bs, min(rq.fb + s1 * S::U, (sg.pos_hi + 16) / 16));
-            sg.nsteps = sg.be > sg.bs + warp * NB ? (sg.be - sg.bs - warp * NB + S::U - 1) / S::U : 0;
-            sg.table = a.table + (long long)b * a.table_stride;
-            return true;
-        }
-        return false;
-    };
+    uint32_t pos = me < C ? start_of(me) : W;
+    const uint32_t end = me < C ? start_of(me + 1) : W;
 
     // ---- copies: the lane's block offset among the 32 of the steps win * 32 / NB ..., -1 past the end ----
-    constexpr int SPW = 32 / NB;
-    auto offsets = [&](const Segment& sg, int win) -> long long {
+    constexpr int SPW = 32 / NB, STRIDE = COOP ? NW : 1;
+    const int at = COOP ? warp : 0;  // the warp's place in a step
+    int bs = 0, be = 0, nsteps = 0, h = 0;
+    const int32_t* table = a.table;
+    auto offsets = [&](int win) -> long long {
         const int k = win * SPW + lane / NB;
-        const int blk = sg.bs + (k * NW + warp) * NB + lane % NB;
-        if (k >= sg.nsteps || blk >= sg.be) return -1;
+        const int blk = bs + (k * STRIDE + at) * NB + lane % NB;
+        if (k >= nsteps || blk >= be) return -1;
         const int p = blk / bpp;
-        int page = sg.table[p];
+        int page = table[p];
         if (page < 0 || page >= a.num_pages) bad = true, page = 0;
-        return (((long long)page * a.kv_heads + sg.h) * bpp + (blk - p * bpp)) * BB;
+        return (((long long)page * a.kv_heads + h) * bpp + (blk - p * bpp)) * BB;
     };
     const uint8_t* my_ring = smem + warp * DEPTH * S::STAGE;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(my_ring) + lane * 16;
     const uint8_t* pages = a.pages + lane * 16;
     long long off = -1, off_next = -1;
-    auto issue = [&](const Segment& sg, int k) {
-        if (k < sg.nsteps) {
+    auto issue = [&](int k) {
+        if (k < nsteps) {
             if (k % SPW == 0) {
-                off = k == 0 ? offsets(sg, 0) : off_next;
-                if (k + SPW < sg.nsteps) off_next = offsets(sg, k / SPW + 1);
+                off = k == 0 ? offsets(0) : off_next;
+                if (k + SPW < nsteps) off_next = offsets(k / SPW + 1);
             }
 #pragma unroll
             for (int sub = 0; sub < NB; ++sub) {
@@ -307,38 +289,215 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         cp_async_commit();
     };
 
-    struct Pending {  // an item of which this CTA wrote a part
-        int q0, nq, h, f0, parts0, parts;
-    };
-    __shared__ Pending pend[2];  // the one that begins before this CTA's share, the one that begins within
-    if (tid < 2) pend[tid].parts = 0;
+    float o[NT][D / 16][4], z[RAW ? NG : 1][4], r[NT][NG][2], M[NT][2], L[NT][2];
 
-    // dimensions d .. d + 3 of query row f: the sum of the weighted values, the maximum and the sum of the weights
-    auto store = [&](int q0, int h, int f, int d, float4 s, float m, float l) {
-        const int qi = f / gq;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const long long row = q0 + qi;
-        const int head = h * gq + f - qi * gq;
-        const long long at = row * a.out_stride + (long long)head * D + d;
-        if (a.out_f32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
-        } else {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(s.x * inv, s.y * inv);
-            const __nv_bfloat162 q = __floats2bfloat162_rn(s.z * inv, s.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+    // Outputs of rows f0 .. f0 + ROWS - 1 from the sums in o, by one warp.
+    auto store = [&](int q0, int nq, int hh, int f0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float inv[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                inv[e] = L[nt][e] == 0.f ? 0.f : 1.f / L[nt][e];
+                const int f = f0 + 8 * nt + 2 * c + e, qi = f / gq;
+                if (f >= nq * gq) continue;
+                const long long row = q0 + qi;
+                const int head = hh * gq + f - qi * gq;
+                if (a.lse && g == 0)
+                    a.lse[row * a.q_heads + head] =
+                        L[nt][e] == 0.f ? -CUDART_INF_F : (M[nt][e] + log2f(L[nt][e]) - 2.f) * 0.69314718055994530942f;
+                if (a.out_f32) {
+                    float* to = static_cast<float*>(a.out) + row * a.out_stride + (long long)head * D + g;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) to[16 * i] = o[nt][i][e] * inv[e], to[16 * i + 8] = o[nt][i][2 + e] * inv[e];
+                }
+            }
+            if (a.out_f32) continue;
+            // pairs of columns of a dimension become pairs of dimensions of column g
+            const int f = f0 + 8 * nt + g, qi = f / gq;
+            uint16_t* to = static_cast<uint16_t*>(a.out) + (long long)(q0 + qi) * a.out_stride + (long long)(hh * gq + f - qi * gq) * D + 2 * c;
+            const bool there = f < nq * gq;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(o[nt][i][2 * t] * inv[0], o[nt][i][2 * t + 1] * inv[1]);
+                    const uint32_t w = transpose8x8(*reinterpret_cast<const uint32_t*>(&v));
+                    if (there) *reinterpret_cast<uint32_t*>(to + 16 * i + 8 * t) = w;
+                }
         }
-        if (a.lse && d == 0)
-            a.lse[row * a.q_heads + head] = l == 0.f ? -CUDART_INF_F : (m + log2f(l) - 2.f) * 0.69314718055994530942f;
+    };
+    // A part is the o of a warp as it lies in its lanes, then M and L of each row.
+    auto put_part = [&](uint32_t slot) {
+        float* part = parts + (long long)slot * S::PART;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                reinterpret_cast<float4*>(part)[(nt * (D / 16) + i) * 32 + lane] = make_float4(o[nt][i][0], o[nt][i][1], o[nt][i][2], o[nt][i][3]);
+            if (g == 0) {
+                *reinterpret_cast<float2*>(part + ROWS * D + 8 * nt + 2 * c) = make_float2(M[nt][0], M[nt][1]);
+                *reinterpret_cast<float2*>(part + ROWS * D + ROWS + 8 * nt + 2 * c) = make_float2(L[nt][0], L[nt][1]);
+            }
+        }
+    };
+    // Adds the part of a slot to o, M and L.
+    auto add_part = [&](uint32_t slot) {
+        const float* part = parts + (long long)slot * S::PART;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float2 m = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + 8 * nt + 2 * c));
+            const float2 l = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + ROWS + 8 * nt + 2 * c));
+            float4 v[D / 16];
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part) + (nt * (D / 16) + i) * 32 + lane);
+            const float m0 = fmaxf(M[nt][0], m.x), m1 = fmaxf(M[nt][1], m.y);
+            const float f0 = M[nt][0] == -CUDART_INF_F ? 0.f : exp2_fast(M[nt][0] - m0), f1 = M[nt][1] == -CUDART_INF_F ? 0.f : exp2_fast(M[nt][1] - m1);
+            const float x0 = m.x == -CUDART_INF_F ? 0.f : exp2_fast(m.x - m0), x1 = m.y == -CUDART_INF_F ? 0.f : exp2_fast(m.y - m1);
+            M[nt][0] = m0, M[nt][1] = m1;
+            L[nt][0] = fmaf(L[nt][0], f0, l.x * x0), L[nt][1] = fmaf(L[nt][1], f1, l.y * x1);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                o[nt][i][0] = fmaf(o[nt][i][0], f0, v[i].x * x0), o[nt][i][1] = fmaf(o[nt][i][1], f1, v[i].y * x1);
+                o[nt][i][2] = fmaf(o[nt][i][2], f0, v[i].z * x0), o[nt][i][3] = fmaf(o[nt][i][3], f1, v[i].w * x1);
+            }
+        }
+    };
+    auto clear = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                r[nt][gr][0] = r[nt][gr][1] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[RAW ? gr : 0][e] = 0.f;
+            }
+            M[nt][0] = M[nt][1] = -CUDART_INF_F;
+            L[nt][0] = L[nt][1] = 0.f;
+        }
+    };
+    // COOP: the sums of the CTA's warps joined into warp 0's, through shared memory (over the rings).
+    auto join_warps = [&]() {
+        float* buf = reinterpret_cast<float*>(smem);  // [NW][8][PAD]
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (g == 0) {
+                    sm_m[warp * ROWS + 8 * nt + 2 * c + e] = M[nt][e];
+                    sm_l[warp * ROWS + 8 * nt + 2 * c + e] = L[nt][e];
+                }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = 8 * nt + 2 * c + e;
+                float m = -CUDART_INF_F;
+                for (int w = g; w < NW; w += 8) m = fmaxf(m, sm_m[w * ROWS + col]);
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
+                const float f = M[nt][e] == -CUDART_INF_F ? 0.f : exp2_fast(M[nt][e] - m);
+                if (warp == 0) {
+                    float l = 0.f;
+                    for (int w = g; w < NW; w += 8) {
+                        const float mw = sm_m[w * ROWS + col];
+                        l = fmaf(mw == -CUDART_INF_F ? 0.f : exp2_fast(mw - m), sm_l[w * ROWS + col], l);
+                    }
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, w);
+                    M[nt][e] = m, L[nt][e] = l;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    buf[(warp * 8 + 2 * c + e) * S::PAD + 16 * i + g] = o[nt][i][e] * f;
+                    buf[(warp * 8 + 2 * c + e) * S::PAD + 16 * i + g + 8] = o[nt][i][2 + e] * f;
+                }
+            }
+            __syncthreads();
+            // the sum over the warps into warp 0's place, every thread some of it
+            for (int i = tid; i < 2 * D; i += THREADS) {
+                float* to = buf + i / (D / 4) * S::PAD + i % (D / 4) * 4;
+                float4 s = *reinterpret_cast<const float4*>(to);
+#pragma unroll
+                for (int w = 1; w < NW; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(to + w * 8 * S::PAD);
+                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                }
+                *reinterpret_cast<float4*>(to) = s;
+            }
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[nt][i][e] = buf[(2 * c + (e & 1)) * S::PAD + 16 * i + g + 8 * (e >> 1)];
+            }
+            if (NT > 1) __syncthreads();
+        }
     };
 
-    Segment sg;
-    bool more = next_segment(sg);
-    if (more)
-        for (int k = 0; k < DEPTH - 1; ++k) issue(sg, k);
+    while (pos < end) {
+        // ---- the item at pos, and what of it is this worker's ----
+        int b;
+        uint32_t base;
+        {   // the thread whose requests hold it, by two ballots over the prefixes
+            const uint32_t hi = __ballot_sync(0xFFFFFFFFu, prefix[lane * NW] <= pos);
+            const int t0 = (31 - __clz(hi)) * NW;
+            const uint32_t lo = __ballot_sync(0xFFFFFFFFu, lane < NW && prefix[t0 + (lane < NW ? lane : 0)] <= pos);
+            const int t = t0 + 31 - __clz(lo);
+            base = prefix[t], b = t * stride;
+            if (stride > 1) {  // 32 of its requests at a time
+                for (;; b += 32) {
+                    uint32_t n = 0;
+                    if (b + lane < a.B && b + lane < (t + 1) * stride) {
+                        const Request q = request(b + lane);
+                        n = q.tiles * (q.units + EXTRA);
+                    }
+                    uint32_t sum = n;
+#pragma unroll
+                    for (int w = 1; w < 32; w <<= 1) {
+                        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, w);
+                        if (lane >= w) sum += y;
+                    }
+                    const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + sum > pos);
+                    if (past) {
+                        const int l = __ffs(past) - 1;
+                        base += __shfl_sync(0xFFFFFFFFu, sum - n, l), b += l;
+                        break;
+                    }
+                    base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+                }
+            }
+        }
+        const Request rq = request(b);
+        const uint32_t len = rq.units + EXTRA, item = (pos - base) / len, i0 = base + item * len, in = pos - i0;
+        const uint32_t u0 = in > EXTRA ? in - EXTRA : 0;
+        uint32_t u1 = rq.units;
+        if (split)
+            u1 = min(u1, max(end - i0, EXTRA) - EXTRA);
+        else if (in > EXTRA)  // its first unit is another worker's, and so is the item
+            u1 = 0;
+        pos = i0 + len;
+        if (u1 <= u0) continue;
+        const int q0 = rq.q0, nq = rq.nq, ctx = rq.ctx;
+        h = (int)(item / (uint32_t)rq.qt);
+        const int f0 = (int)(item - (uint32_t)h * rq.qt) * ROWS;
+        const int pos_lo = ctx - nq + f0 / gq, pos_hi = ctx - nq + min(nq - 1, (f0 + ROWS - 1) / gq);
+        {
+            const int k_lo = a.window ? max(0, pos_lo - a.window + 1) : 0;
+            bs = max(rq.fb + (int)u0 * unit, k_lo / 16);
+            be = (int)min((long long)rq.fb + (long long)u1 * unit, (long long)max(pos_hi + 16, 0) / 16);
+            be = max(bs, be);
+            nsteps = be > bs + at * NB ? (be - bs - at * NB + S::STEP - 1) / S::STEP : 0;
+            table = a.table + (long long)b * a.table_stride;
+        }
+        for (int k = 0; k < DEPTH - 1; ++k) issue(k);
 
-    while (more) {
-        const int f0 = sg.f0, nsteps = sg.nsteps, bs = sg.bs, be = sg.be, h = sg.h;
         // ---- the queries as B operands, and their sums over each group ----
         // word pairs of dimensions 32 j + 8 c + (0, 4), (1, 5), (2, 6), (3, 7) of row 8 nt + g
         uint32_t qf[NT == 1 ? J : 1][4];
@@ -347,12 +506,13 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) posc[nt][e] = sg.ctx - sg.nq + min(sg.nq - 1, (f0 + 8 * nt + 2 * c + e) / gq);
+            for (int e = 0; e < 2; ++e) posc[nt][e] = ctx - nq + min(nq - 1, (f0 + 8 * nt + 2 * c + e) / gq);
+        if (NT > 1) sync();  // the last item's readers
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && warp != nt % NW) continue;
+            if (NT > 1 && COOP && warp != nt % NW) continue;
             const int f = f0 + 8 * nt + g, i = f / gq;
-            const uint16_t* src = a.q + (long long)(sg.q0 + i) * a.q_stride + (long long)(h * gq + f - i * gq) * D + 8 * c;
+            const uint16_t* src = a.q + (long long)(q0 + i) * a.q_stride + (long long)(h * gq + f - i * gq) * D + 8 * c;
             float sum[NG];
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) sum[gr] = 0.f;
@@ -361,7 +521,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 v[j] = make_uint4(0, 0, 0, 0);
-                if (i < sg.nq) v[j] = *reinterpret_cast<const uint4*>(src + 32 * j);
+                if (i < nq) v[j] = *reinterpret_cast<const uint4*>(src + 32 * j);
                 big = __vmaxu2(__vmaxu2(big, v[j].x & 0x7FFF7FFFu), __vmaxu2(v[j].y & 0x7FFF7FFFu,
                                __vmaxu2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu)));
             }
@@ -406,34 +566,18 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                 }
             }
         }
-        if (NT > 1) __syncthreads();
+        if (NT > 1) sync();
 
-        float o[NT][D / 16][4], z[RAW ? NG : 1][4], r[NT][NG][2], M[NT][2], L[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-                r[nt][gr][0] = r[nt][gr][1] = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[RAW ? gr : 0][e] = 0.f;
-            }
-            M[nt][0] = M[nt][1] = -CUDART_INF_F;
-            L[nt][0] = L[nt][1] = 0.f;
-        }
-
+        clear();
         // scores are kept as s and m give them; col_scale (>= 0) takes those of a column to powers of two
         auto col_scale = [&](int nt, int e) { return NT == 1 ? qscale[e] : qsums[NG * ROWS + 8 * nt + 2 * c + e]; };
 
         for (int k = 0; k < nsteps; ++k) {
             cp_async_wait<DEPTH - 2>();
             __syncwarp();  // the step's copies of every lane are there, and step k - 1 is read
-            issue(sg, k + DEPTH - 1);
+            issue(k + DEPTH - 1);
             const uint8_t* stage = my_ring + (k % DEPTH) * NB * BB;
-            const int blk0 = bs + (k * NW + warp) * NB;
+            const int blk0 = bs + (k * STRIDE + at) * NB;
 
             // scores y of NB blocks: rows g and g + 8 (tokens), columns 2c and 2c + 1 of each n-tile
             float y[NB][NT][4];
@@ -498,8 +642,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                 }
             }
             // Some key of this step may be unseen by some row, or lie past the segment.
-            const bool edge = blk0 + NB > be || (blk0 + NB) * 16 - 1 > sg.pos_lo ||
-                              (a.window && blk0 * 16 <= sg.pos_hi - a.window);
+            const bool edge = blk0 + NB > be || (blk0 + NB) * 16 - 1 > pos_lo ||
+                              (a.window && blk0 * 16 <= pos_hi - a.window);
             uint32_t seen = 0xFFFFFFFFu;
             static_assert(NB * NT * 4 <= 32, "one bit per score");
             if (edge) {
@@ -635,26 +779,17 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         }
         cp_async_wait<0>();
 
-        // the next segment's first copies run while this one's warps are joined
-        const Segment done = sg;
-        more = next_segment(sg);
-        if (more)
-            for (int k = 0; k < DEPTH - 1; ++k) issue(sg, k);
-
-        // ---- join the warps, then write the item or this CTA's part of it ----
+        // ---- the rows' sums complete, then the item or the worker's part of it ----
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                if (M[nt][e] != -CUDART_INF_F) M[nt][e] *= col_scale(nt, e);
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) {
                     L[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, L[nt][e], w);
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) r[nt][gr][e] += __shfl_xor_sync(0xFFFFFFFFu, r[nt][gr][e], w);
-                }
-                if (g == 0) {
-                    sm_m[warp * ROWS + 8 * nt + 2 * c + e] = M[nt][e] * col_scale(nt, e);
-                    sm_l[warp * ROWS + 8 * nt + 2 * c + e] = L[nt][e];
                 }
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -668,137 +803,75 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                     }
                 }
             }
-        float* part = nullptr;
-        if (!done.whole) {
-            const bool begins = done.iu0 >= u0;  // the item's other parts are later CTAs'
-            part = static_cast<float*>(a.workspace) + 1024 + (2 * (long long)blockIdx.x + begins) * S::PART;
-            if (tid == 0) {
-                Pending& p = pend[begins];
-                p.q0 = done.q0, p.nq = done.nq, p.h = h, p.f0 = f0;
-                p.parts0 = (int)(((done.iu0 + 1) * C - 1) / W);
-                p.parts = (int)(((done.iu0 + done.units) * C - 1) / W) - p.parts0 + 1;
-            }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int hd = 0; hd < D / 64; ++hd) {
-                if (nt + hd > 0) __syncthreads();  // the buffer is read
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        buf[(warp * 8 + 2 * c + (e & 1)) * S::PAD + 16 * i + g + 8 * (e >> 1)] = o[nt][4 * hd + i][e];
-                __syncthreads();
-                for (int i = tid; i < 128; i += THREADS) {
-                    const int row = i / 16, d = i % 16 * 4, f = f0 + 8 * nt + row;
-                    if (f >= done.nq * gq) continue;
-                    float m = -CUDART_INF_F, l = 0.f;
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) m = fmaxf(m, sm_m[w * ROWS + 8 * nt + row]);
-                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) {
-                        const float mw = sm_m[w * ROWS + 8 * nt + row], x = mw == -CUDART_INF_F ? 0.f : exp2_fast(mw - m);
-                        const float4 v = *reinterpret_cast<const float4*>(buf + (w * 8 + row) * S::PAD + d);
-                        l = fmaf(x, sm_l[w * ROWS + 8 * nt + row], l);
-                        s.x = fmaf(x, v.x, s.x), s.y = fmaf(x, v.y, s.y), s.z = fmaf(x, v.z, s.z), s.w = fmaf(x, v.w, s.w);
-                    }
-                    if (done.whole) {
-                        store(done.q0, h, f, 64 * hd + d, s, m, l);
-                    } else {
-                        *reinterpret_cast<float4*>(part + (8 * nt + row) * D + 64 * hd + d) = s;
-                        if (hd == 0 && d == 0) {
-                            part[ROWS * D + 8 * nt + row] = m;
-                            part[ROWS * D + ROWS + 8 * nt + row] = l;
-                        }
-                    }
+        if (COOP) join_warps();
+        if (!COOP || warp == 0) {
+            if (u0 == 0 && u1 == rq.units) {
+                store(q0, nq, h, f0);
+            } else {
+                const int begins = u0 == 0;  // the item's other parts are later workers'
+                put_part(2 * me + begins);
+                if (lane == 0) {
+                    Pending& p = sh_pend[own][begins];
+                    p.q0 = q0, p.nq = nq, p.h = h, p.f0 = f0;
+                    p.first = owner_of(i0 + EXTRA);
+                    p.n = owner_of(i0 + len - 1) - p.first + 1;
                 }
             }
-        __syncthreads();  // the buffers are free for the next segment
+        }
+        if (COOP) __syncthreads();  // the rings are free
     }
     if (bad) atomicExch(&g_kv4_attn_range, 1);
 
-    // ---- parts: the CTA that arrives last at an item joins them ----
-    if (pend[0].parts + pend[1].parts == 0) return;
-    __threadfence();
-    __syncthreads();
-    if (tid < 2) {
-        sh_last[tid] = 0;
-        const int n = tid ? pend[1].parts : pend[0].parts, at = tid ? pend[1].parts0 : pend[0].parts0;
-        if (n) sh_last[tid] = atomicInc(static_cast<unsigned*>(a.workspace) + at, (unsigned)n - 1) == (unsigned)n - 1;  // wraps to 0 behind the last
+    // ---- parts: the worker that arrives last at an item joins them ----
+    sync();
+    if (sh_pend[own][0].n + sh_pend[own][1].n == 0) return;
+    if ((COOP ? tid : lane) == 0) {
+        __threadfence();  // the worker's parts before their counts
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const uint32_t n = sh_pend[own][w].n;
+            sh_last[own][w] = n && atomicInc(counters + sh_pend[own][w].first, n - 1) == n - 1;  // back to 0 behind the last
+        }
         __threadfence();
     }
-    __syncthreads();
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (!sh_last[which]) continue;
-        const Pending p = pend[which];
-        const int n = p.parts;
-        // CTA j's part: slot 2j, or 2j + 1 where the item begins within it, that is at parts0
-        const float* base = static_cast<const float*>(a.workspace) + 1024;
-        auto at = [&](int j) { return base + (2 * (long long)(p.parts0 + j) + (j == 0)) * S::PART; };
-        // factors 2^(m_j - m) and the joined m and l of each row, one warp a row
-        float* fac = reinterpret_cast<float*>(smem);
-        float* joined = fac + ROWS * n;
-        for (int row = warp; row < ROWS; row += NW) {
-            float m = -CUDART_INF_F, l = 0.f;
-            for (int j = lane; j < n; j += 32) {
-                const float mj = __ldcg(at(j) + ROWS * D + row);
-                fac[row * n + j] = mj;
-                m = fmaxf(m, mj);
-            }
-#pragma unroll
-            for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
-            for (int j = lane; j < n; j += 32) {
-                const float mj = fac[row * n + j], x = mj == -CUDART_INF_F ? 0.f : exp2_fast(mj - m);
-                fac[row * n + j] = x;
-                l = fmaf(x, __ldcg(at(j) + ROWS * D + ROWS + row), l);
-            }
-            l = warp_sum(l);
-            if (lane == 0) joined[2 * row] = m, joined[2 * row + 1] = l;
-        }
-        __syncthreads();
-        for (int i = tid; i < ROWS * D / 4; i += THREADS) {
-            const int row = i / (D / 4), d = i % (D / 4) * 4, f = p.f0 + row;
-            if (f >= p.nq * gq) continue;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int j = 0; j < n; ++j) {
-                const float x = fac[row * n + j];
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(at(j) + row * D + d));
-                s.x = fmaf(x, v.x, s.x), s.y = fmaf(x, v.y, s.y), s.z = fmaf(x, v.z, s.z), s.w = fmaf(x, v.w, s.w);
-            }
-            store(p.q0, p.h, f, d, s, joined[2 * row], joined[2 * row + 1]);
-        }
-        __syncthreads();
+    sync();
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+        if (!sh_last[own][w]) continue;
+        const Pending p = sh_pend[own][w];
+        clear();
+        // worker j's part lies in its slot 0, or 1 where the item begins with it; a CTA's warps take turns of them
+        for (uint32_t j = at; j < p.n; j += STRIDE) add_part(2 * (p.first + j) + (j == 0));
+        if (COOP) join_warps();
+        if (!COOP || warp == 0) store(p.q0, p.nq, p.h, p.f0);
+        if (COOP) __syncthreads();
     }
 }
-
-constexpr int kMaxCtas = 1024;  // counters in the workspace's first 4 KB
 
 struct Entry {
     const void* fn;
-    int threads, smem, occ, rows, part, most;
+    int threads, smem, occ, rows, part, workers, step;
 };
 
-template <int D, int G, int NT, int NW, int NB, int DEPTH, int OCC>
+template <int D, int G, int NT, int NW, int NB, int DEPTH, int OCC, bool COOP>
 Entry entry() {
-    using S = Shape<D, G, NT, NW, NB, DEPTH>;
+    using S = Shape<D, G, NT, NW, NB, DEPTH, COOP>;
     static_assert(S::SMEM * OCC <= 225 * 1024, "shared memory of the CTAs of an SM");
-    return {(const void*)kv4_attention_kernel<D, G, NT, NW, NB, DEPTH, OCC>, NW * 32, S::SMEM, OCC, S::ROWS, S::PART, S::MOST};
+    return {(const void*)kv4_attention_kernel<D, G, NT, NW, NB, DEPTH, OCC, COOP>, NW * 32, S::SMEM, OCC, S::ROWS, S::PART,
+            S::WORKERS, S::STEP};
 }
 
-// rows: query rows per KV head of an average request; few: fewer items than SMs, so each is cut over several.
+// rows: query rows per KV head of an average request; few: few items, each cut over several SMs.
 template <int D, int G>
 Entry pick(int rows, bool few) {
-    // columns: as few n-tiles as hold the rows of an average request, at most what the registers hold
+    // columns: one n-tile of 8 rows, or two where requests have more and the registers hold them
     if constexpr (D == 256) {
-        return rows <= 8 || G == 32 ? entry<D, G, 1, 4, 1, 4, 2>() : entry<D, G, G == 32 ? 1 : 2, 4, 1, 4, 2>();
+        if constexpr (G == 64)
+            if (rows > 8) return few ? entry<D, G, 2, 8, 1, 4, 1, true>() : entry<D, G, 2, 4, 1, 4, 2, false>();
+        return few ? entry<D, G, 1, 8, 1, 4, 1, true>() : entry<D, G, 1, 4, 1, 4, 2, false>();
     } else {
-        if (rows <= 8) return few ? entry<D, G, 1, 16, 2, D == 64 ? 4 : 2, 1>() : entry<D, G, 1, 4, 2, D == 64 ? 4 : 3, D == 64 ? 4 : 3>();
-        if (rows <= 16 || (D == 128 && G == 32)) return entry<D, G, 2, 4, 1, 4, D == 64 ? 3 : 2>();
-        return entry<D, G, D == 128 && G == 32 ? 2 : 4, 4, 1, 4, 2>();
+        if (rows <= 8) return few ? entry<D, G, 1, 16, 2, D == 64 ? 4 : 2, 1, true>() : entry<D, G, 1, 4, 2, D == 64 ? 4 : 3, D == 64 ? 4 : 3, false>();
+        return few ? entry<D, G, 2, 8, 1, 4, 1, true>() : entry<D, G, 2, 4, 1, 4, D == 64 ? 3 : 2, false>();
     }
 }
 
@@ -808,20 +881,21 @@ Entry pick_for(int head_dim, int group, int rows, bool few) {
     return head_dim == 64 ? pick<64, 64>(rows, few) : head_dim == 128 ? pick<128, 64>(rows, few) : pick<256, 64>(rows, few);
 }
 
-// One wave, at most as many CTAs as counters and as the buffer of a joining CTA holds factors for.
+// One wave, and a counter for each worker.
 int grid_of(const Entry& e, int sms) {
-    int n = sms * e.occ;
-    if (n > kMaxCtas) n = kMaxCtas;
-    return n < e.most ? n : e.most;
+    const int n = sms * e.occ;
+    return n * e.workers < kCounters ? n : kCounters / e.workers;
 }
-size_t workspace_of(const Entry& e, int grid) { return 4096 + (size_t)grid * 2 * e.part * sizeof(float); }
+size_t workspace_of(const Entry& e, int grid) {
+    return kCounters * sizeof(uint32_t) + (size_t)grid * e.workers * 2 * e.part * sizeof(float);
+}
 
 }  // namespace
 
 size_t kv4_attention_workspace(int head_dim) {
     size_t most = 0;
     for (int group : {32, 64})
-        for (int rows : {8, 16, 32})
+        for (int rows : {8, 16})
             for (bool few : {false, true}) {
                 const Entry e = pick_for(head_dim, group, rows, few);
                 const size_t n = workspace_of(e, grid_of(e, device_sm_count()));
@@ -832,12 +906,22 @@ size_t kv4_attention_workspace(int head_dim) {
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     const int sms = device_sm_count();
-    const int64_t rows = ((int64_t)a.T * (a.q_heads / a.kv_heads) + a.B - 1) / a.B;
-    const Entry e = pick_for(a.head_dim, a.group, (int)(rows < 64 ? rows : 64), (int64_t)a.B * a.kv_heads <= sms);
+    const int64_t gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
+    const int64_t tile = rows <= 8 ? 8 : 16, items = a.kv_heads * (((int64_t)a.T * gq + tile - 1) / tile);
+    const Entry e = pick_for(a.head_dim, a.group, (int)(rows < 64 ? rows : 64), items < sms);
     cudaError_t err = cudaFuncSetAttribute(e.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, e.smem);
     if (err != cudaSuccess) return err;
-    const int grid = grid_of(e, sms);
+    int grid = grid_of(e, sms);
     int split = a.ws_bytes >= workspace_of(e, grid) ? 1 : 0;
+    // Units so large that the line of all items has places of 32 bits.
+    const int64_t tiles = a.kv_heads * (((int64_t)a.T * gq + e.rows - 1) / e.rows + a.B);
+    int shift = 0;
+    while (tiles * (((int64_t)a.table_width * a.page_size / 16 + ((int64_t)e.step << shift)) / ((int64_t)e.step << shift) + 3) > 0x7FFFFFFFll &&
+           shift < 20)
+        ++shift;
+    // No more CTAs than there can be work for.
+    const int64_t most = tiles * (((int64_t)a.table_width * a.page_size / 16 + e.step - 1) / e.step + 3);
+    if (most < grid) grid = (int)(most > 0 ? most : 1);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3((unsigned)e.threads, 1, 1);
@@ -850,7 +934,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     cfg.numAttrs = 1;
     count_launch();
     Kv4AttnArgs args = a;
-    void* params[2] = {&args, &split};
+    void* params[3] = {&args, &split, &shift};
     return cudaLaunchKernelExC(&cfg, e.fn, params);
 }
 
