@@ -26,7 +26,8 @@ def __getattr__(name):
     if name in _EXPORTS:
         from . import _binding
 
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)  # the next access finds it here
+        return value
     if name == "rope_table":
         from .rope import rope_table
 

@@ -472,6 +472,57 @@ def dequant_int4_awq_g128(Wq, scales, zeros):
     return out
 
 
+# The calls below are made many times per token, so their checks read each tensor once and compare devices by number; what
+# is wrong is told by the slower checks above.
+_dtypes = None
+
+
+def _types():
+    global _dtypes
+    if _dtypes is None:
+        torch = _torch()
+        _dtypes = (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8, torch.empty)
+    return _dtypes
+
+
+def _device_index():
+    global _device_index
+    _device_index = _torch()._C._cuda_getDevice
+    return _device_index()
+
+
+def _raw_stream(index):
+    global _raw_stream
+    _raw_stream = _torch()._C._cuda_getCurrentRawStream
+    return _raw_stream(index)
+
+
+def _check_devices(*ts):
+    """All tensors (None skipped) on the current CUDA device, whose number it returns."""
+    cur = _device_index()
+    for t in ts:
+        if t is not None and t.get_device() != cur:
+            _on_current_device(*ts)  # says which
+    return cur
+
+
+def _plain(t, name, dtype, ndim):
+    """_need's checks; returns the shape."""
+    try:
+        shape = t.shape
+        if t.dtype is dtype and t.is_cuda and len(shape) == ndim and t.is_contiguous():
+            return shape
+    except AttributeError:
+        pass
+    _need(t, name, dtype, ndim)
+    return t.shape
+
+
+def _vector(t, name, dtype, n):
+    if _plain(t, name, dtype, 1)[0] != n:
+        _need_shape(t, name, (n,))
+
+
 class Kv4Cache:
     """4-bit paged key/value cache over `pages`, a contiguous uint8 tensor (num_pages,
     kv4_page_bytes(page_size, kv_heads, head_dim, group)) that the caller owns."""
@@ -479,13 +530,12 @@ class Kv4Cache:
     __slots__ = ("pages", "kv_heads", "head_dim", "page_size", "group", "_c")
 
     def __init__(self, pages, kv_heads, head_dim, page_size=16, group=64):
-        torch = _torch()
-        _need(pages, "pages", torch.uint8, 2)
         size = kv4_page_bytes(page_size, kv_heads, head_dim, group)
-        if pages.shape[1] != size:
-            raise ValueError(f"pages must have {size} bytes per page, got {pages.shape[1]}")
+        num, got = _plain(pages, "pages", _types()[4], 2)
+        if got != size:
+            raise ValueError(f"pages must have {size} bytes per page, got {got}")
         self.pages, self.kv_heads, self.head_dim, self.page_size, self.group = pages, kv_heads, head_dim, page_size, group
-        self._c = MbwKv4Cache(pages.data_ptr(), pages.shape[0], page_size, kv_heads, head_dim, group)
+        self._c = MbwKv4Cache(pages.data_ptr(), num, page_size, kv_heads, head_dim, group)
 
 
 def kv4_page_bytes(page_size, kv_heads, head_dim, group=64):
@@ -498,7 +548,15 @@ def kv4_page_bytes(page_size, kv_heads, head_dim, group=64):
 
 
 def _need_rows(t, name, heads, dim):
-    """bf16 (T, heads, dim), possibly rows of a wider matrix; returns the row stride in elements."""
+    """bf16 (T, heads, dim), possibly rows of a wider matrix; returns (T, heads, the row stride in elements)."""
+    try:
+        shape, st = t.shape, t.stride()
+        if t.dtype is _types()[0] and t.is_cuda and len(shape) == 3:
+            n, h, w = shape
+            if w == dim and (heads is None or h == heads) and st[2] == 1 and (st[1] == dim or h == 1):
+                return n, h, st[0] if n > 1 else h * dim
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -508,10 +566,7 @@ def _need_rows(t, name, heads, dim):
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
         raise ValueError(f"{name} must have shape (T, {'heads' if heads is None else heads}, {dim}), got {tuple(t.shape)}")
-    st = t.stride()
-    if st[2] != 1 or (t.shape[1] > 1 and st[1] != dim):
-        raise ValueError(f"{name} must have contiguous rows of heads")
-    return st[0] if t.shape[0] > 1 else t.shape[1] * dim
+    raise ValueError(f"{name} must have contiguous rows of heads")
 
 
 def kv4_append(cache, k, v, slots, q=None, positions=None, cos_sin=None, interleaved=False, q_out=None):
@@ -520,26 +575,25 @@ def kv4_append(cache, k, v, slots, q=None, positions=None, cos_sin=None, interle
     wider QKV output; slots int64 (T,), page * page_size + place in the page, negative: not stored.
     positions int32 (T,) and cos_sin fp32 (max_pos, rotary_dim) (see rope_table) together, or neither:
     no rotation. Returns the rotated queries (`q_out`, which may be q, or a new tensor), None without q."""
-    torch = _torch()
+    bf16, f32, i32, i64, _, empty = _types()
     hk, d = cache.kv_heads, cache.head_dim
-    ks, vs = _need_rows(k, "k", hk, d), _need_rows(v, "v", hk, d)
-    T = k.shape[0]
-    if v.shape[0] != T:
+    T, _, ks = _need_rows(k, "k", hk, d)
+    Tv, _, vs = _need_rows(v, "v", hk, d)
+    if Tv != T:
         raise ValueError("k and v must have the same number of tokens")
-    _need(slots, "slots", torch.int64, 1)
-    _need_shape(slots, "slots", (T,))
+    _vector(slots, "slots", i64, T)
     qp = op = None
     qs = os_ = hq = 0
     if q is not None:
-        qs, hq = _need_rows(q, "q", None, d), q.shape[1]
-        if q.shape[0] != T:
+        Tq, hq, qs = _need_rows(q, "q", None, d)
+        if Tq != T:
             raise ValueError("q and k must have the same number of tokens")
         if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+            q_out = empty((T, hq, d), dtype=bf16, device=q.device)
             os_ = hq * d
         else:
-            os_ = _need_rows(q_out, "q_out", hq, d)
-            if q_out.shape[0] != T:
+            To, _, os_ = _need_rows(q_out, "q_out", hq, d)
+            if To != T:
                 raise ValueError("q_out and q must have the same number of tokens")
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -548,29 +602,28 @@ def kv4_append(cache, k, v, slots, q=None, positions=None, cos_sin=None, interle
     if (positions is None) != (cos_sin is None):
         raise ValueError("positions and cos_sin go together")
     if positions is not None:
-        _need(positions, "positions", torch.int32, 1)
-        _need_shape(positions, "positions", (T,))
-        _need(cos_sin, "cos_sin", torch.float32, 2)
-        rope = ctypes.byref(MbwRope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
-                                    positions.data_ptr()))
-    _on_current_device(cache.pages, k, v, slots, q, q_out, positions, cos_sin)
-    check("mbw_kv4_append", lib().mbw_kv4_append(ctypes.byref(cache._c), k.data_ptr(), ks, v.data_ptr(), vs,
-                                                 slots.data_ptr(), qp, qs, op, os_, hq, rope, T,
-                                                 _stream_ptr(k.device)))
+        _vector(positions, "positions", i32, T)
+        most, dim = _plain(cos_sin, "cos_sin", f32, 2)
+        rope = ctypes.byref(MbwRope(cos_sin.data_ptr(), most, dim, 1 if interleaved else 0, positions.data_ptr()))
+    dev = _check_devices(cache.pages, k, v, slots, q, q_out, positions, cos_sin)
+    st = lib().mbw_kv4_append(ctypes.byref(cache._c), k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), qp, qs, op,
+                              os_, hq, rope, T, _raw_stream(dev))
+    if st:
+        check("mbw_kv4_append", st)
     return q_out
 
 
 def kv4_gather(cache, slots):
     """The keys and values the cache holds at `slots` int64 (T,), each bf16 (T, kv_heads, head_dim); zeros for a
     negative slot."""
-    torch = _torch()
-    _need(slots, "slots", torch.int64, 1)
-    _on_current_device(cache.pages, slots)
-    shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
-    v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
-    check("mbw_kv4_gather", lib().mbw_kv4_gather(ctypes.byref(cache._c), slots.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                                 shape[0], _stream_ptr(slots.device)))
+    bf16, _, _, i64, _, empty = _types()
+    T, = _plain(slots, "slots", i64, 1)
+    dev = _check_devices(cache.pages, slots)
+    shape, device = (T, cache.kv_heads, cache.head_dim), slots.device
+    k, v = empty(shape, dtype=bf16, device=device), empty(shape, dtype=bf16, device=device)
+    st = lib().mbw_kv4_gather(ctypes.byref(cache._c), slots.data_ptr(), k.data_ptr(), v.data_ptr(), T, _raw_stream(dev))
+    if st:
+        check("mbw_kv4_gather", st)
     return k, v
 
 
@@ -588,30 +641,36 @@ def kv4_attention(cache, q, block_table, ctx_lens, q_starts=None, scale=None, wi
     A query sees the keys up to its own position, with `window` > 0 only that many. scale: head_dim ** -0.5
     by default. Returns out (T, q_heads, head_dim), with return_lse also fp32 (T, q_heads). workspace: from
     kv4_attention_workspace; without one, long contexts are not split and take longer."""
-    torch = _torch()
+    bf16, f32, i32, _, _, empty = _types()
     d = cache.head_dim
-    qs, (T, hq) = _need_rows(q, "q", None, d), q.shape[:2]
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(ctx_lens, "ctx_lens", torch.int32, 1)
-    B, width = block_table.shape
-    _need_shape(ctx_lens, "ctx_lens", (B,))
+    T, hq, qs = _need_rows(q, "q", None, d)
+    B, width = _plain(block_table, "block_table", i32, 2)
+    _vector(ctx_lens, "ctx_lens", i32, B)
+    sp = None
     if q_starts is not None:
-        _need(q_starts, "q_starts", torch.int32, 1)
-        _need_shape(q_starts, "q_starts", (B + 1,))
-    if out is None or _out_dtype() != torch.bfloat16:
-        out = _alloc_out((T, hq, d), q, out)
-        os_ = hq * d
-    else:
-        os_ = _need_rows(out, "out", hq, d)
-        if out.shape[0] != T:
+        _vector(q_starts, "q_starts", i32, B + 1)
+        sp = q_starts.data_ptr()
+    os_ = hq * d
+    wide = getattr(_tls, "fp32", False)  # output_fp32
+    if out is None:
+        out = empty((T, hq, d), dtype=f32 if wide else bf16, device=q.device)
+    elif not wide:
+        To, _, os_ = _need_rows(out, "out", hq, d)
+        if To != T:
             raise ValueError("out and q must have the same number of tokens")
-    lse = torch.empty((T, hq), dtype=torch.float32, device=q.device) if return_lse else None
-    _on_current_device(cache.pages, q, block_table, ctx_lens, q_starts, out, workspace)
+    else:
+        out = _alloc_out((T, hq, d), q, out)
+    lse = lp = None
+    if return_lse:
+        lse = empty((T, hq), dtype=f32, device=q.device)
+        lp = lse.data_ptr()
+    dev = _check_devices(cache.pages, q, block_table, ctx_lens, q_starts, out, workspace)
     wp, wn = _ws(workspace)
-    check("mbw_kv4_attention", lib().mbw_kv4_attention(
-        ctypes.byref(cache._c), q.data_ptr(), qs, out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
-        block_table.data_ptr(), width, width, ctx_lens.data_ptr(), None if q_starts is None else q_starts.data_ptr(), B, T,
-        hq, d ** -0.5 if scale is None else scale, window, wp, wn, _stream_ptr(q.device)))
+    st = lib().mbw_kv4_attention(
+        ctypes.byref(cache._c), q.data_ptr(), qs, out.data_ptr(), os_, lp, block_table.data_ptr(), width, width,
+        ctx_lens.data_ptr(), sp, B, T, hq, d ** -0.5 if scale is None else scale, window, wp, wn, _raw_stream(dev))
+    if st:
+        check("mbw_kv4_attention", st)
     return (out, lse) if return_lse else out
 
 
@@ -629,35 +688,35 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, workspace=None):
     probability fp32 (M,) and rank int32 (M,) of targets int32 (M,) (None without), the entropy fp32 (M,) in
     nats, the top_k (<= 32) most likely ids int32 (M, top_k) and their log probabilities fp32 (M, top_k).
     workspace: from token_logprobs_workspace; without one, few rows take longer."""
-    torch = _torch()
-    if not isinstance(logits, torch.Tensor):
-        raise TypeError("logits must be a torch.Tensor")
+    bf16, f32, i32, _, _, empty = _types()
+    try:
+        shape, dtype, device = logits.shape, logits.dtype, logits.device
+    except AttributeError:
+        raise TypeError("logits must be a torch.Tensor") from None
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"logits must be {torch.bfloat16} or {torch.float32}, got {logits.dtype}")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    wide = dtype is f32
+    if not wide and dtype is not bf16:
+        raise TypeError(f"logits must be {bf16} or {f32}, got {dtype}")
+    if len(shape) != 2 or (logits.stride(1) != 1 and shape[1] > 1):
         raise ValueError("logits must have 2 dimensions and contiguous rows")
-    M, V = logits.shape
-    dev = logits.device
-    lp = rank = None
+    M, V = shape
+    tp = lp = rank = lpp = rp = None
     if targets is not None:
-        _need(targets, "targets", torch.int32, 1)
-        _need_shape(targets, "targets", (M,))
-        lp = torch.empty(M, dtype=torch.float32, device=dev)
-        rank = torch.empty(M, dtype=torch.int32, device=dev)
-    ent = torch.empty(M, dtype=torch.float32, device=dev)
+        _vector(targets, "targets", i32, M)
     if not 0 <= top_k <= 32:
         raise ValueError("top_k must be 0 to 32")
-    ids = torch.empty((M, top_k), dtype=torch.int32, device=dev)
-    tlp = torch.empty((M, top_k), dtype=torch.float32, device=dev)
-    _on_current_device(logits, targets, workspace)
+    dev = _check_devices(logits, targets, workspace)
+    if targets is not None:
+        lp, rank = empty(M, dtype=f32, device=device), empty(M, dtype=i32, device=device)
+        tp, lpp, rp = targets.data_ptr(), lp.data_ptr(), rank.data_ptr()
+    ent = empty(M, dtype=f32, device=device)
+    ids, tlp = empty((M, top_k), dtype=i32, device=device), empty((M, top_k), dtype=f32, device=device)
     wp, wn = _ws(workspace)
-    check("mbw_token_logprobs", lib().mbw_token_logprobs(
-        logits.data_ptr(), int(logits.dtype == torch.float32), logits.stride(0) if M > 1 else V,
-        None if targets is None else targets.data_ptr(), M, V, scale, top_k, None if lp is None else lp.data_ptr(),
-        None if rank is None else rank.data_ptr(), ent.data_ptr(), ids.data_ptr(), tlp.data_ptr(), wp, wn,
-        _stream_ptr(dev)))
+    st = lib().mbw_token_logprobs(logits.data_ptr(), 1 if wide else 0, logits.stride(0) if M > 1 else V, tp, M, V, scale,
+                                  top_k, lpp, rp, ent.data_ptr(), ids.data_ptr(), tlp.data_ptr(), wp, wn, _raw_stream(dev))
+    if st:
+        check("mbw_token_logprobs", st)
     return TokenLogprobs(lp, rank, ent, ids, tlp)
 
 

@@ -4,6 +4,7 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <atomic>
 #include <cstring>
 #include <string>
 
@@ -21,9 +22,13 @@ void set_last_error(const std::string& msg) { g_last_error = msg; }
 void count_launch() { ++g_launches; }
 
 int device_sm_count() {
+    static std::atomic<int> known[16];  // per device, once asked for
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    const bool keep = dev >= 0 && dev < 16;
+    if (keep && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    if (keep) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -50,6 +50,7 @@
 
 #include <math_constants.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -890,6 +891,32 @@ size_t workspace_of(const Entry& e, int grid) {
     return kCounters * sizeof(uint32_t) + (size_t)grid * e.workers * 2 * e.part * sizeof(float);
 }
 
+// The kernel's shared memory, allowed once per kernel and device.
+cudaError_t allow_smem(const Entry& e) {
+    struct Done {
+        std::atomic<const void*> fn;
+        std::atomic<unsigned> devices;
+    };
+    static Done done[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    Done* slot = nullptr;
+    for (Done& d : done) {
+        const void* fn = d.fn.load(std::memory_order_acquire);
+        if (!fn && d.fn.compare_exchange_strong(fn, e.fn)) fn = e.fn;
+        if (fn == e.fn) {
+            slot = &d;
+            break;
+        }
+    }
+    const unsigned bit = dev < 32 ? 1u << dev : 0u;
+    if (slot && (slot->devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    err = cudaFuncSetAttribute(e.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, e.smem);
+    if (err == cudaSuccess && slot) slot->devices.fetch_or(bit, std::memory_order_release);
+    return err;
+}
+
 }  // namespace
 
 size_t kv4_attention_workspace(int head_dim) {
@@ -909,8 +936,10 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     const int64_t gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
     const int64_t tile = rows <= 8 ? 8 : 16, items = a.kv_heads * (((int64_t)a.T * gq + tile - 1) / tile);
     const Entry e = pick_for(a.head_dim, a.group, (int)(rows < 64 ? rows : 64), items < sms);
-    cudaError_t err = cudaFuncSetAttribute(e.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, e.smem);
-    if (err != cudaSuccess) return err;
+    if (e.smem > 48 * 1024) {
+        const cudaError_t err = allow_smem(e);
+        if (err != cudaSuccess) return err;
+    }
     int grid = grid_of(e, sms);
     int split = a.ws_bytes >= workspace_of(e, grid) ? 1 : 0;
     // Units so large that the line of all items has places of 32 bits.

@@ -150,8 +150,8 @@ def calls(monkeypatch):
             return lambda *a: made.append((name, len(a))) or 0
 
     monkeypatch.setattr(B, "lib", lambda: Lib())
-    monkeypatch.setattr(B, "_stream_ptr", lambda device: 0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(B, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(B, "_device_index", lambda: -1)  # a host tensor's
     return made
 
 
