@@ -135,7 +135,7 @@ struct Shape {
     static constexpr int QSUM = NT > 1 ? WORKERS * (NG + 1) * ROWS * 4 : 0;
     static constexpr int JOIN = COOP ? NW * 8 * PAD * 4 : 0;  // over the ring, which is drained then
     static constexpr int BUF = RING > JOIN ? RING : JOIN;
-    static constexpr int SMEM = BUF + QS + QSUM + (COOP ? 2 * (NW + 1) * ROWS * 4 : 0) + (NW * 32 + 1) * 4;
+    static constexpr int SMEM = BUF + QS + QSUM + (COOP ? 2 * (NW + 1) * ROWS * 4 : 0) + (NW * 32 + 1) * 16;
     static constexpr int PART = ROWS * (D + 2);  // floats of a part: its sums, then m and l of each row
 };
 
@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     float* qsums = reinterpret_cast<float*>(smem + S::BUF + S::QS) + own * (NG + 1) * ROWS;
     float* sm_m = reinterpret_cast<float*>(smem + S::BUF + S::QS + S::QSUM);  // [NW + 1][ROWS], the last joined
     float* sm_l = sm_m + (NW + 1) * ROWS;
-    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + S::SMEM) - (THREADS + 1);  // of the line, per thread's requests
+    // the line before each thread's requests, and q0, nq and ctx of the one where a thread has no more
+    uint4* prefix = reinterpret_cast<uint4*>(smem + S::SMEM) - (THREADS + 1);
     struct Pending {  // an item of which the worker wrote a part
         int q0, nq, h, f0;
         uint32_t first, n;
@@ -186,8 +187,16 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     // ---- the line: per item, EXTRA and its units of STEP << shift blocks ----
     const int unit = S::STEP << shift;
     const int cap = a.table_width * a.page_size;  // at most MBW_MAX_DIM
-    auto request = [&](int b) {
+    auto sized = [&](int q0, int nq, int ctx) {
         Request r;
+        r.q0 = q0, r.nq = nq, r.ctx = ctx;
+        r.fb = a.window ? max(0, ctx - nq - a.window + 1) / 16 : 0;
+        r.units = max(1u, ((uint32_t)((ctx + 15) / 16 - r.fb) + unit - 1) / unit);
+        r.qt = ((uint32_t)nq * gq + ROWS - 1) / ROWS;  // at most MBW_MAX_DIM query rows
+        r.tiles = (uint32_t)r.qt * a.kv_heads;
+        return r;
+    };
+    auto request = [&](int b) {
         int q0, q1;
         if (a.q_starts) {
             const int s0 = a.q_starts[b], s1 = a.q_starts[b + 1];
@@ -200,22 +209,19 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         }
         int ctx = max(a.ctx_lens[b], 0);
         if (ctx > cap) bad = true, ctx = cap;
-        r.q0 = q0, r.nq = q1 - q0, r.ctx = ctx;
-        r.fb = a.window ? max(0, ctx - r.nq - a.window + 1) / 16 : 0;
-        r.units = max(1u, ((uint32_t)((ctx + 15) / 16 - r.fb) + unit - 1) / unit);
-        r.qt = ((uint32_t)r.nq * gq + ROWS - 1) / ROWS;  // at most MBW_MAX_DIM query rows
-        r.tiles = (uint32_t)r.qt * a.kv_heads;
-        return r;
+        return sized(q0, q1 - q0, ctx);
     };
     const int stride = (a.B + THREADS - 1) / THREADS;  // requests per thread
     uint32_t W, items = 0;
     {
         uint32_t x = 0, n = 0;
+        uint4 mine = make_uint4(0, 0, 0, 0);
         for (int i = 0; i < stride; ++i) {
             const int b = tid * stride + i;
             if (b < a.B) {
                 const Request r = request(b);
                 x += r.tiles * (r.units + EXTRA), n += r.tiles;
+                mine.y = r.q0, mine.z = r.nq, mine.w = r.ctx;
             }
         }
         n = __reduce_add_sync(0xFFFFFFFFu, n);
@@ -235,8 +241,9 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             if (w < warp) before += y;
             W += y, items += sh_items[w];
         }
-        prefix[tid] = before + sum - x;
-        if (tid == 0) prefix[THREADS] = W;
+        mine.x = before + sum - x;
+        prefix[tid] = mine;
+        if (tid == 0) prefix[THREADS].x = W;
         __syncthreads();
     }
     // as many workers as items at least; worker i of C has the places [i each + min(i, rest), ...)
@@ -342,25 +349,44 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             }
         }
     };
-    // Adds the part of a slot to o, M and L.
-    auto add_part = [&](uint32_t slot) {
-        const float* part = parts + (long long)slot * S::PART;
+    // Adds the parts of an item to o, M and L, in their order from `j` on, each `by`-th; some at a time are on their way.
+    // Piece j's part lies in its slot 0, or 1 where the item begins with it.
+    auto add_parts = [&](uint32_t first, uint32_t n, uint32_t j, uint32_t by) {
+        constexpr int BATCH = NT * D <= 64 ? 4 : NT * D <= 128 ? 2 : 1;
+        for (; j < n; j += BATCH * by) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float2 m = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + 8 * nt + 2 * c));
-            const float2 l = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + ROWS + 8 * nt + 2 * c));
-            float4 v[D / 16];
+            for (int nt = 0; nt < NT; ++nt) {
+                float2 m[BATCH], l[BATCH];
+                float4 v[BATCH][D / 16];
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part) + (nt * (D / 16) + i) * 32 + lane);
-            const float m0 = fmaxf(M[nt][0], m.x), m1 = fmaxf(M[nt][1], m.y);
-            const float f0 = M[nt][0] == -CUDART_INF_F ? 0.f : exp2_fast(M[nt][0] - m0), f1 = M[nt][1] == -CUDART_INF_F ? 0.f : exp2_fast(M[nt][1] - m1);
-            const float x0 = m.x == -CUDART_INF_F ? 0.f : exp2_fast(m.x - m0), x1 = m.y == -CUDART_INF_F ? 0.f : exp2_fast(m.y - m1);
-            M[nt][0] = m0, M[nt][1] = m1;
-            L[nt][0] = fmaf(L[nt][0], f0, l.x * x0), L[nt][1] = fmaf(L[nt][1], f1, l.y * x1);
+                for (int k = 0; k < BATCH; ++k) {
+                    const uint32_t q = j + k * by;
+                    m[k] = make_float2(-CUDART_INF_F, -CUDART_INF_F), l[k] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                o[nt][i][0] = fmaf(o[nt][i][0], f0, v[i].x * x0), o[nt][i][1] = fmaf(o[nt][i][1], f1, v[i].y * x1);
-                o[nt][i][2] = fmaf(o[nt][i][2], f0, v[i].z * x0), o[nt][i][3] = fmaf(o[nt][i][3], f1, v[i].w * x1);
+                    for (int i = 0; i < D / 16; ++i) v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (q < n) {
+                        const float* part = parts + (long long)(2 * (first + q) + (q == 0)) * S::PART;
+                        m[k] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + 8 * nt + 2 * c));
+                        l[k] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + ROWS + 8 * nt + 2 * c));
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) v[k][i] = __ldcg(reinterpret_cast<const float4*>(part) + (nt * (D / 16) + i) * 32 + lane);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const float m0 = fmaxf(M[nt][0], m[k].x), m1 = fmaxf(M[nt][1], m[k].y);
+                    const float f0 = M[nt][0] == -CUDART_INF_F ? 0.f : exp2_fast(M[nt][0] - m0);
+                    const float f1 = M[nt][1] == -CUDART_INF_F ? 0.f : exp2_fast(M[nt][1] - m1);
+                    const float x0 = m[k].x == -CUDART_INF_F ? 0.f : exp2_fast(m[k].x - m0);
+                    const float x1 = m[k].y == -CUDART_INF_F ? 0.f : exp2_fast(m[k].y - m1);
+                    M[nt][0] = m0, M[nt][1] = m1;
+                    L[nt][0] = fmaf(L[nt][0], f0, l[k].x * x0), L[nt][1] = fmaf(L[nt][1], f1, l[k].y * x1);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        o[nt][i][0] = fmaf(o[nt][i][0], f0, v[k][i].x * x0), o[nt][i][1] = fmaf(o[nt][i][1], f1, v[k][i].y * x1);
+                        o[nt][i][2] = fmaf(o[nt][i][2], f0, v[k][i].z * x0), o[nt][i][3] = fmaf(o[nt][i][3], f1, v[k][i].w * x1);
+                    }
+                }
             }
         }
     };
@@ -446,12 +472,15 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         // ---- the item at pos, and what of it is this worker's ----
         int b;
         uint32_t base;
+        Request rq;
         {   // the thread whose requests hold it, by two ballots over the prefixes
-            const uint32_t hi = __ballot_sync(0xFFFFFFFFu, prefix[lane * NW] <= pos);
+            const uint32_t hi = __ballot_sync(0xFFFFFFFFu, prefix[lane * NW].x <= pos);
             const int t0 = (31 - __clz(hi)) * NW;
-            const uint32_t lo = __ballot_sync(0xFFFFFFFFu, lane < NW && prefix[t0 + (lane < NW ? lane : 0)] <= pos);
+            const uint32_t lo = __ballot_sync(0xFFFFFFFFu, lane < NW && prefix[t0 + (lane < NW ? lane : 0)].x <= pos);
             const int t = t0 + 31 - __clz(lo);
-            base = prefix[t], b = t * stride;
+            const uint4 at_t = prefix[t];
+            base = at_t.x, b = t * stride;
+            if (stride == 1) rq = sized((int)at_t.y, (int)at_t.z, (int)at_t.w);
             if (stride > 1) {  // 32 of its requests at a time
                 for (;; b += 32) {
                     uint32_t n = 0;
@@ -473,9 +502,9 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                     }
                     base += __shfl_sync(0xFFFFFFFFu, sum, 31);
                 }
+                rq = request(b);
             }
         }
-        const Request rq = request(b);
         const uint32_t len = rq.units + EXTRA, item = (pos - base) / len, i0 = base + item * len, in = pos - i0;
         const uint32_t u0 = in > EXTRA ? in - EXTRA : 0;
         uint32_t u1 = rq.units;
@@ -496,6 +525,13 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             be = max(bs, be);
             nsteps = be > bs + at * NB ? (be - bs - at * NB + S::STEP - 1) / S::STEP : 0;
             table = a.table + (long long)b * a.table_stride;
+        }
+        uint4 q_raw[NT == 1 ? J : 1];  // on their way while the block table is read
+        if (NT == 1) {
+            const int f = f0 + g, i = f / gq;
+            const uint16_t* src = a.q + (long long)(q0 + i) * a.q_stride + (long long)(h * gq + f - i * gq) * D + 8 * c;
+#pragma unroll
+            for (int j = 0; j < J; ++j) q_raw[j] = i < nq ? *reinterpret_cast<const uint4*>(src + 32 * j) : make_uint4(0, 0, 0, 0);
         }
         for (int k = 0; k < DEPTH - 1; ++k) issue(k);
 
@@ -521,8 +557,10 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             uint32_t big = 0;  // the largest |q| of the row, as bf16 bits
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (i < nq) v[j] = *reinterpret_cast<const uint4*>(src + 32 * j);
+                if (NT == 1)
+                    v[j] = q_raw[j];
+                else
+                    v[j] = i < nq ? *reinterpret_cast<const uint4*>(src + 32 * j) : make_uint4(0, 0, 0, 0);
                 big = __vmaxu2(__vmaxu2(big, v[j].x & 0x7FFF7FFFu), __vmaxu2(v[j].y & 0x7FFF7FFFu,
                                __vmaxu2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu)));
             }
@@ -841,8 +879,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         if (!sh_last[own][w]) continue;
         const Pending p = sh_pend[own][w];
         clear();
-        // worker j's part lies in its slot 0, or 1 where the item begins with it; a CTA's warps take turns of them
-        for (uint32_t j = at; j < p.n; j += STRIDE) add_part(2 * (p.first + j) + (j == 0));
+        add_parts(p.first, p.n, at, STRIDE);
         if (COOP) join_warps();
         if (!COOP || warp == 0) store(p.q0, p.nq, p.h, p.f0);
         if (COOP) __syncthreads();
