@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     constexpr bool RAW = NT == 1;
     // What an item costs besides its blocks, and the least share of a worker, in units: below it the parts' way through
     // the workspace takes longer than the blocks.
-    constexpr uint32_t EXTRA = COOP ? 1 : 2, LEAST = COOP ? 4 : 6;
+    constexpr uint32_t EXTRA = COOP ? 1 : 4, LEAST = COOP ? 2 : 4;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int own = COOP ? 0 : warp;  // the worker in the CTA
@@ -349,18 +349,18 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             }
         }
     };
-    // Adds the parts of an item to o, M and L, in their order from `j` on, each `by`-th; some at a time are on their way.
+    // Adds the parts of an item to o, M and L, in their order; some at a time are on their way.
     // Piece j's part lies in its slot 0, or 1 where the item begins with it.
-    auto add_parts = [&](uint32_t first, uint32_t n, uint32_t j, uint32_t by) {
+    auto add_parts = [&](uint32_t first, uint32_t n) {
         constexpr int BATCH = NT * D <= 64 ? 4 : NT * D <= 128 ? 2 : 1;
-        for (; j < n; j += BATCH * by) {
+        for (uint32_t j = 0; j < n; j += BATCH) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float2 m[BATCH], l[BATCH];
                 float4 v[BATCH][D / 16];
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
-                    const uint32_t q = j + k * by;
+                    const uint32_t q = j + k;
                     m[k] = make_float2(-CUDART_INF_F, -CUDART_INF_F), l[k] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -405,6 +405,70 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             }
             M[nt][0] = M[nt][1] = -CUDART_INF_F;
             L[nt][0] = L[nt][1] = 0.f;
+        }
+    };
+    // COOP: the parts of an item joined by all the CTA's threads, each four values of a lane's o, in groups of threads
+    // that take every GROUPS-th part; the groups meet in shared memory.
+    auto join_parts = [&](const Pending& p) {
+        constexpr int VALUES = NT * (D / 16) * 32, GROUPS = THREADS / VALUES > 1 ? THREADS / VALUES : 1, BATCH = 4;
+        struct Sum {
+            float4 s;
+            float2 m, l;
+        };
+        Sum* meet = reinterpret_cast<Sum*>(smem);
+        auto join = [&](Sum& x, float4 v, float2 m, float2 l) {
+            const float m0 = fmaxf(x.m.x, m.x), m1 = fmaxf(x.m.y, m.y);
+            const float f0 = x.m.x == -CUDART_INF_F ? 0.f : exp2_fast(x.m.x - m0), f1 = x.m.y == -CUDART_INF_F ? 0.f : exp2_fast(x.m.y - m1);
+            const float g0 = m.x == -CUDART_INF_F ? 0.f : exp2_fast(m.x - m0), g1 = m.y == -CUDART_INF_F ? 0.f : exp2_fast(m.y - m1);
+            x.m = make_float2(m0, m1);
+            x.l = make_float2(fmaf(x.l.x, f0, l.x * g0), fmaf(x.l.y, f1, l.y * g1));
+            x.s = make_float4(fmaf(x.s.x, f0, v.x * g0), fmaf(x.s.y, f1, v.y * g1), fmaf(x.s.z, f0, v.z * g0), fmaf(x.s.w, f1, v.w * g1));
+        };
+        for (int i0 = 0; i0 < VALUES; i0 += THREADS / GROUPS) {
+            const int i = i0 + tid % (THREADS / GROUPS), group = tid / (THREADS / GROUPS), ln = i & 31, tile = i / 32;
+            const int col = 8 * (tile / (D / 16)) + 2 * (ln & 3);
+            Sum x = {make_float4(0.f, 0.f, 0.f, 0.f), make_float2(-CUDART_INF_F, -CUDART_INF_F), make_float2(0.f, 0.f)};
+            for (uint32_t j = group; j < p.n; j += GROUPS * BATCH) {
+                float4 v[BATCH];
+                float2 m[BATCH], l[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const uint32_t q = j + k * GROUPS;
+                    v[k] = make_float4(0.f, 0.f, 0.f, 0.f), m[k] = make_float2(-CUDART_INF_F, -CUDART_INF_F), l[k] = make_float2(0.f, 0.f);
+                    if (q < p.n) {
+                        const float* part = parts + (long long)(2 * (p.first + q) + (q == 0)) * S::PART;
+                        v[k] = __ldcg(reinterpret_cast<const float4*>(part) + i);
+                        m[k] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + col));
+                        l[k] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + ROWS + col));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) join(x, v[k], m[k], l[k]);
+            }
+            if (GROUPS > 1) {
+                if (group > 0) meet[tid] = x;
+                __syncthreads();
+                if (group == 0)
+                    for (int w = 1; w < GROUPS; ++w) {
+                        const Sum y = meet[tid + w * (THREADS / GROUPS)];
+                        join(x, y.s, y.m, y.l);
+                    }
+                __syncthreads();
+            }
+            if (group > 0) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int f = p.f0 + col + e, qi = f / gq;
+                if (f >= p.nq * gq) continue;
+                const float m = e ? x.m.y : x.m.x, l = e ? x.l.y : x.l.x, inv = l == 0.f ? 0.f : 1.f / l;
+                const long long row = p.q0 + qi;
+                const int head = p.h * gq + f - qi * gq, d = 16 * (tile % (D / 16)) + (ln >> 2);
+                const long long to = row * a.out_stride + (long long)head * D + d;
+                store_out(a.out, to, (e ? x.s.y : x.s.x) * inv, a.out_f32);
+                store_out(a.out, to + 8, (e ? x.s.w : x.s.z) * inv, a.out_f32);
+                if (a.lse && d == 0)
+                    a.lse[row * a.q_heads + head] = l == 0.f ? -CUDART_INF_F : (m + log2f(l) - 2.f) * 0.69314718055994530942f;
+            }
         }
     };
     // COOP: the sums of the CTA's warps joined into warp 0's, through shared memory (over the rings).
@@ -878,11 +942,13 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     for (int w = 0; w < 2; ++w) {
         if (!sh_last[own][w]) continue;
         const Pending p = sh_pend[own][w];
-        clear();
-        add_parts(p.first, p.n, at, STRIDE);
-        if (COOP) join_warps();
-        if (!COOP || warp == 0) store(p.q0, p.nq, p.h, p.f0);
-        if (COOP) __syncthreads();
+        if (COOP) {
+            join_parts(p);
+        } else {
+            clear();
+            add_parts(p.first, p.n);
+            store(p.q0, p.nq, p.h, p.f0);
+        }
     }
 }
 
@@ -899,16 +965,20 @@ Entry entry() {
             S::WORKERS, S::STEP};
 }
 
+// Query rows per KV head of an average request from which on tiles hold 16 of them, not 8: K and V are unpacked half as
+// often, but more rows of the last tile are empty and fewer warps fit an SM. (3 requests of 90 to 200 queries of 4 heads:
+// 102 us against 107 with 8; 12 requests of 2 to 5 queries of 7 heads: 32.5 against 27.5.)
+constexpr int kWideRows = 96;
+
 // rows: query rows per KV head of an average request; few: few items, each cut over several SMs.
 template <int D, int G>
 Entry pick(int rows, bool few) {
-    // columns: one n-tile of 8 rows, or two where requests have more and the registers hold them
     if constexpr (D == 256) {
         if constexpr (G == 64)
-            if (rows > 8) return few ? entry<D, G, 2, 8, 1, 4, 1, true>() : entry<D, G, 2, 4, 1, 4, 2, false>();
+            if (rows >= kWideRows) return few ? entry<D, G, 2, 8, 1, 4, 1, true>() : entry<D, G, 2, 4, 1, 4, 2, false>();
         return few ? entry<D, G, 1, 8, 1, 4, 1, true>() : entry<D, G, 1, 4, 1, 4, 2, false>();
     } else {
-        if (rows <= 8) return few ? entry<D, G, 1, 16, 2, D == 64 ? 4 : 2, 1, true>() : entry<D, G, 1, 4, 2, D == 64 ? 4 : 3, D == 64 ? 4 : 3, false>();
+        if (rows < kWideRows) return few ? entry<D, G, 1, 16, 2, D == 64 ? 4 : 2, 1, true>() : entry<D, G, 1, 4, 2, D == 64 ? 4 : 3, D == 64 ? 4 : 3, false>();
         return few ? entry<D, G, 2, 8, 1, 4, 1, true>() : entry<D, G, 2, 4, 1, 4, D == 64 ? 3 : 2, false>();
     }
 }
@@ -959,7 +1029,7 @@ cudaError_t allow_smem(const Entry& e) {
 size_t kv4_attention_workspace(int head_dim) {
     size_t most = 0;
     for (int group : {32, 64})
-        for (int rows : {8, 16})
+        for (int rows : {8, kWideRows})
             for (bool few : {false, true}) {
                 const Entry e = pick_for(head_dim, group, rows, few);
                 const size_t n = workspace_of(e, grid_of(e, device_sm_count()));
@@ -971,8 +1041,8 @@ size_t kv4_attention_workspace(int head_dim) {
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     const int sms = device_sm_count();
     const int64_t gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
-    const int64_t tile = rows <= 8 ? 8 : 16, items = a.kv_heads * (((int64_t)a.T * gq + tile - 1) / tile);
-    const Entry e = pick_for(a.head_dim, a.group, (int)(rows < 64 ? rows : 64), items < sms);
+    const int64_t tile = rows < kWideRows ? 8 : 16, items = a.kv_heads * (((int64_t)a.T * gq + tile - 1) / tile);
+    const Entry e = pick_for(a.head_dim, a.group, (int)(rows < kWideRows ? rows : kWideRows), items < sms);
     if (e.smem > 48 * 1024) {
         const cudaError_t err = allow_smem(e);
         if (err != cudaSuccess) return err;
