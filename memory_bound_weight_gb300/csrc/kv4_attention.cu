@@ -148,9 +148,9 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     constexpr int NG = S::NG, J = S::J, BB = S::BB, ROWS = S::ROWS, THREADS = NW * 32, NV = D / 64;
     // V's codes as they are and 8 sum w from a constant tile; or, where several n-tiles share their unpacking, n - 8
     constexpr bool RAW = NT == 1;
-    // What an item costs besides its blocks, and the least share of a worker, in units: below it the parts' way through
-    // the workspace takes longer than the blocks.
-    constexpr uint32_t EXTRA = COOP ? 1 : 4, LEAST = COOP ? 2 : 4;
+    // Units that an item costs besides its own (a warp's line), and the units from which on it is worth their parts' way
+    // through the workspace to share them: of a worker at least, of an item that CTAs cut.
+    constexpr uint32_t EXTRA = 4, LEAST = 4;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int own = COOP ? 0 : warp;  // the worker in the CTA
@@ -212,6 +212,29 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         return sized(q0, q1 - q0, ctx);
     };
     const int stride = (a.B + THREADS - 1) / THREADS;  // requests per thread
+    // COOP: places are pieces of one item each, as many as the item's units are of all among the CTAs, so that no CTA
+    // has to end one item and begin another (a CTA whose share spanned two took 8 us longer).
+    float per_unit = 0.f;  // pieces
+    if (COOP) {
+        float n = 0.f;  // the same in every CTA
+        for (int i = 0; i < stride; ++i) {
+            const int b = tid * stride + i;
+            if (b < a.B) {
+                const Request r = request(b);
+                n += (float)r.tiles * (float)r.units;
+            }
+        }
+        n = warp_sum(n);
+        if (lane == 0) sh_scan[warp] = __float_as_uint(n);
+        __syncthreads();
+        n = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) n += __uint_as_float(sh_scan[w]);
+        per_unit = split ? fminf((float)gridDim.x / n, 1.f) : 0.f;
+        __syncthreads();
+    }
+    auto pieces_of = [&](const Request& r) { return r.units < LEAST ? 1u : max(1u, (uint32_t)((float)r.units * per_unit)); };
+    auto places_of = [&](const Request& r) { return COOP ? pieces_of(r) : r.units + EXTRA; };  // of an item
     uint32_t W, items = 0;
     {
         uint32_t x = 0, n = 0;
@@ -220,7 +243,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             const int b = tid * stride + i;
             if (b < a.B) {
                 const Request r = request(b);
-                x += r.tiles * (r.units + EXTRA), n += r.tiles;
+                x += r.tiles * places_of(r), n += r.tiles;
                 mine.y = r.q0, mine.z = r.nq, mine.w = r.ctx;
             }
         }
@@ -246,16 +269,18 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         if (tid == 0) prefix[THREADS].x = W;
         __syncthreads();
     }
-    // as many workers as items at least; worker i of C has the places [i each + min(i, rest), ...)
-    const uint32_t all = gridDim.x * S::WORKERS, C = max(1u, min(all, max(items, W / LEAST))), each = W / C, rest = W - each * C;
+    // Warps: as many as items at least; worker i of C has the places [i each + min(i, rest), ...). CTAs: one place, and
+    // where there are more pieces than CTAs the others behind it.
+    const uint32_t all = gridDim.x * S::WORKERS, C = COOP ? all : max(1u, min(all, max(items, W / LEAST)));
+    const uint32_t each = W / C, rest = W - each * C;
     const uint32_t me = COOP ? blockIdx.x : warp * gridDim.x + blockIdx.x;  // neighbours on different SMs
     auto start_of = [&](uint32_t i) { return i * each + min(i, rest); };
     auto owner_of = [&](uint32_t p) {
         const uint32_t big = rest * (each + 1);
         return p < big ? p / (each + 1) : rest + (p - big) / each;
     };
-    uint32_t pos = me < C ? start_of(me) : W;
-    const uint32_t end = me < C ? start_of(me + 1) : W;
+    uint32_t pos = COOP ? me : me < C ? start_of(me) : W;
+    const uint32_t end = COOP ? W : me < C ? start_of(me + 1) : W;
 
     // ---- copies: the lane's block offset among the 32 of the steps win * 32 / NB ..., -1 past the end ----
     constexpr int SPW = 32 / NB, STRIDE = COOP ? NW : 1;
@@ -436,7 +461,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                     const uint32_t q = j + k * GROUPS;
                     v[k] = make_float4(0.f, 0.f, 0.f, 0.f), m[k] = make_float2(-CUDART_INF_F, -CUDART_INF_F), l[k] = make_float2(0.f, 0.f);
                     if (q < p.n) {
-                        const float* part = parts + (long long)(2 * (p.first + q) + (q == 0)) * S::PART;
+                        const float* part = parts + (long long)(p.first + q) * S::PART;
                         v[k] = __ldcg(reinterpret_cast<const float4*>(part) + i);
                         m[k] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + col));
                         l[k] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + ROWS + col));
@@ -532,7 +557,9 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         }
     };
 
-    while (pos < end) {
+    for (;;) {
+    const bool there = pos < end;
+    if (there) {
         // ---- the item at pos, and what of it is this worker's ----
         int b;
         uint32_t base;
@@ -550,7 +577,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                     uint32_t n = 0;
                     if (b + lane < a.B && b + lane < (t + 1) * stride) {
                         const Request q = request(b + lane);
-                        n = q.tiles * (q.units + EXTRA);
+                        n = q.tiles * places_of(q);
                     }
                     uint32_t sum = n;
 #pragma unroll
@@ -569,15 +596,21 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                 rq = request(b);
             }
         }
-        const uint32_t len = rq.units + EXTRA, item = (pos - base) / len, i0 = base + item * len, in = pos - i0;
-        const uint32_t u0 = in > EXTRA ? in - EXTRA : 0;
-        uint32_t u1 = rq.units;
-        if (split)
-            u1 = min(u1, max(end - i0, EXTRA) - EXTRA);
-        else if (in > EXTRA)  // its first unit is another worker's, and so is the item
-            u1 = 0;
-        pos = i0 + len;
-        if (u1 <= u0) continue;
+        const uint32_t len = places_of(rq), item = (pos - base) / len, i0 = base + item * len, in = pos - i0;
+        uint32_t u0, u1 = rq.units;
+        if (COOP) {
+            const uint32_t n = rq.units / len, more = rq.units - n * len;  // the first `more` pieces hold one unit more
+            u0 = in * n + min(in, more), u1 = u0 + n + (in < more);
+            pos += gridDim.x;
+        } else {
+            u0 = in > EXTRA ? in - EXTRA : 0;
+            if (split)
+                u1 = min(u1, max(end - i0, EXTRA) - EXTRA);
+            else if (in > EXTRA)  // its first unit is another worker's, and so is the item
+                u1 = 0;
+            pos = i0 + len;
+            if (u1 <= u0) continue;
+        }
         const int q0 = rq.q0, nq = rq.nq, ctx = rq.ctx;
         h = (int)(item / (uint32_t)rq.qt);
         const int f0 = (int)(item - (uint32_t)h * rq.qt) * ROWS;
@@ -911,45 +944,53 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             if (u0 == 0 && u1 == rq.units) {
                 store(q0, nq, h, f0);
             } else {
-                const int begins = u0 == 0;  // the item's other parts are later workers'
-                put_part(2 * me + begins);
+                // A warp's two parts at most: of an item that began before its share, and of one whose other parts are
+                // later workers'. A CTA's: one per piece.
+                const int begins = !COOP && u0 == 0;
+                put_part(COOP ? i0 + in : 2 * me + begins);
                 if (lane == 0) {
                     Pending& p = sh_pend[own][begins];
                     p.q0 = q0, p.nq = nq, p.h = h, p.f0 = f0;
-                    p.first = owner_of(i0 + EXTRA);
-                    p.n = owner_of(i0 + len - 1) - p.first + 1;
+                    p.first = COOP ? i0 : owner_of(i0 + EXTRA);
+                    p.n = COOP ? len : owner_of(i0 + len - 1) - p.first + 1;
                 }
             }
         }
-        if (COOP) __syncthreads();  // the rings are free
+    }
+    if (!COOP && there) continue;
+
+    // ---- parts: the worker that arrives last at an item joins them. A CTA looks behind each piece, a warp at the end ----
+    sync();
+    if (sh_pend[own][0].n + sh_pend[own][1].n > 0) {
+        if ((COOP ? tid : lane) == 0) {
+            __threadfence();  // the worker's parts before their counts
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const uint32_t n = sh_pend[own][w].n;
+                sh_last[own][w] = n && atomicInc(counters + sh_pend[own][w].first, n - 1) == n - 1;  // back to 0 behind the last
+            }
+            __threadfence();
+        }
+        sync();
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+            if (!sh_last[own][w]) continue;
+            const Pending p = sh_pend[own][w];
+            if (COOP) {
+                join_parts(p);
+            } else {
+                clear();
+                add_parts(p.first, p.n);
+                store(p.q0, p.nq, p.h, p.f0);
+            }
+        }
+        sync();
+        if ((COOP ? tid : lane) < 2) sh_pend[own][COOP ? tid : lane].n = 0;
+        sync();
+    }
+    if (!there) break;
     }
     if (bad) atomicExch(&g_kv4_attn_range, 1);
-
-    // ---- parts: the worker that arrives last at an item joins them ----
-    sync();
-    if (sh_pend[own][0].n + sh_pend[own][1].n == 0) return;
-    if ((COOP ? tid : lane) == 0) {
-        __threadfence();  // the worker's parts before their counts
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const uint32_t n = sh_pend[own][w].n;
-            sh_last[own][w] = n && atomicInc(counters + sh_pend[own][w].first, n - 1) == n - 1;  // back to 0 behind the last
-        }
-        __threadfence();
-    }
-    sync();
-#pragma unroll 1
-    for (int w = 0; w < 2; ++w) {
-        if (!sh_last[own][w]) continue;
-        const Pending p = sh_pend[own][w];
-        if (COOP) {
-            join_parts(p);
-        } else {
-            clear();
-            add_parts(p.first, p.n);
-            store(p.q0, p.nq, p.h, p.f0);
-        }
-    }
 }
 
 struct Entry {
@@ -989,13 +1030,15 @@ Entry pick_for(int head_dim, int group, int rows, bool few) {
     return head_dim == 64 ? pick<64, 64>(rows, few) : head_dim == 128 ? pick<128, 64>(rows, few) : pick<256, 64>(rows, few);
 }
 
-// One wave, and a counter for each worker.
+// One wave; for each warp two parts and a counter, for each CTA and each of at most 4 items per CTA a part and a counter.
+constexpr int kItemsPerCta = 4;
 int grid_of(const Entry& e, int sms) {
-    const int n = sms * e.occ;
-    return n * e.workers < kCounters ? n : kCounters / e.workers;
+    const int n = sms * e.occ, most = e.workers > 1 ? kCounters / e.workers : kCounters / (kItemsPerCta + 1);
+    return n < most ? n : most;
 }
 size_t workspace_of(const Entry& e, int grid) {
-    return kCounters * sizeof(uint32_t) + (size_t)grid * e.workers * 2 * e.part * sizeof(float);
+    const size_t slots = (size_t)grid * (e.workers > 1 ? 2 * e.workers : kItemsPerCta + 1);
+    return kCounters * sizeof(uint32_t) + slots * e.part * sizeof(float);
 }
 
 // The kernel's shared memory, allowed once per kernel and device.
@@ -1041,8 +1084,14 @@ size_t kv4_attention_workspace(int head_dim) {
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     const int sms = device_sm_count();
     const int64_t gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
-    const int64_t tile = rows < kWideRows ? 8 : 16, items = a.kv_heads * (((int64_t)a.T * gq + tile - 1) / tile);
-    const Entry e = pick_for(a.head_dim, a.group, (int)(rows < kWideRows ? rows : kWideRows), items < sms);
+    const int64_t tile = rows < kWideRows || (a.head_dim == 256 && a.group == 32) ? 8 : 16;
+    // items of requests of average size, and the most that requests of any sizes have
+    const int64_t with = a.B < a.T ? a.B : a.T, items = a.kv_heads * with * ((rows + tile - 1) / tile);
+    const int64_t most_items = a.kv_heads * (with + ((int64_t)a.T * gq + tile - 1) / tile);
+    // CTAs as workers cut whole items among them, so there have to be more CTAs than items by enough (12 requests of 8
+    // KV heads and 32768 tokens, 96 items: 119 us against 91 with warps; 64 items: 67 against 69; 8: 19 against 87).
+    const bool few = 2 * items <= sms && most_items <= kItemsPerCta * sms;
+    const Entry e = pick_for(a.head_dim, a.group, (int)(rows < kWideRows ? rows : kWideRows), few);
     if (e.smem > 48 * 1024) {
         const cudaError_t err = allow_smem(e);
         if (err != cudaSuccess) return err;
