@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
             const uint32_t ex = max(max(big >> 16, big & 0xFFFFu) >> 7, 20u);  // its biased exponent
             // to 2^14, and back with the codes' 2^24 (in two factors: either is a normal number)
-            const float up = copysignf(__uint_as_float((268u - ex) << 23), a.scale), down = __uint_as_float((ex - 14u) << 23) * (sl2 * 16777216.f);
+            const float up = copysignf(__uint_as_float((268u - ex) << 23), a.scale), down =
+                fmaxf(__uint_as_float((ex - 14u) << 23) * (sl2 * 16777216.f), 1.17549435e-38f);  // 0 times the minus infinity of an unseen key is not 0
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
