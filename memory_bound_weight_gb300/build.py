@@ -26,7 +26,8 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-
 
 # translation units of libmbw.so (the product) and of the input generator
 LIB_SOURCES = ["abi.cu", "plan.cu", "gemv_simt.cu", "gemv_mma.cu", "gemv_tma.cu", "gemv_lat.cu", "gemm_tc.cu",
-               "gemv_awq_batch.cu", "quantize.cu", "kv4_cache.cu", "kv4_attention.cu", "logprobs.cu"]
+               "gemv_awq_batch.cu", "quantize.cu", "kv4_cache.cu", "kv4_attention.cu",
+               "kv4_attention_tc.cu", "logprobs.cu"]
 GEN_SOURCES = ["gen_inputs.cu"]
 
 

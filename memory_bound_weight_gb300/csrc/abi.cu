@@ -598,13 +598,14 @@ mbw_status mbw_check_device_error(void) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     const int f = tma_take_fault();
-    const int f2 = tc_take_fault();
+    const int f2 = tc_take_fault(), f3 = kv4_attn_tc_take(true);
     const int r = kv4_cache_take_range(), r2 = kv4_attn_take_range(), r3 = logprobs_take_range();
-    if (f < 0 || f2 < 0 || r < 0 || r2 < 0 || r3 < 0)
+    const int r4 = kv4_attn_tc_take(false);
+    if (f < 0 || f2 < 0 || f3 < 0 || r < 0 || r2 < 0 || r3 < 0 || r4 < 0)
         return cuda_fail(cudaGetLastError(), "reading the device fault flag");
-    if (f || f2) return fail(MBW_ERR_DEVICE_TIMEOUT, "a bounded wait inside a kernel expired");
+    if (f || f2 || f3) return fail(MBW_ERR_DEVICE_TIMEOUT, "a bounded wait inside a kernel expired");
     if (r) return fail(MBW_ERR_DEVICE_RANGE, "a cache slot or position was out of range");
-    if (r2) return fail(MBW_ERR_DEVICE_RANGE, "a page id, context length or query offset was out of range");
+    if (r2 || r4) return fail(MBW_ERR_DEVICE_RANGE, "a page id, context length or query offset was out of range");
     if (r3) return fail(MBW_ERR_DEVICE_RANGE, "a target token id was out of range");
     return MBW_OK;
 }

@@ -290,6 +290,10 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s);
 size_t kv4_attention_workspace(int head_dim);
+cudaError_t launch_kv4_attention_tc(const Kv4AttnArgs& a, cudaStream_t s);  // head dimensions 64 and 128
+size_t kv4_attention_tc_workspace(int head_dim);
+cudaError_t kv4_allow_smem(const void* kernel, int bytes);  // its dynamic shared memory, once per kernel and device
+int kv4_attn_tc_take(bool fault);  // its range flag, or its flag of an expired wait; cleared
 int kv4_cache_take_range();  // 1 if a slot or position was out of range since the last call (and clear it)
 int kv4_attn_take_range();
 

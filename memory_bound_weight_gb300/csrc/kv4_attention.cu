@@ -1007,10 +1007,14 @@ Entry entry() {
             S::WORKERS, S::STEP};
 }
 
-// Query rows per KV head of an average request from which on tiles hold 16 of them, not 8: K and V are unpacked half as
-// often, but more rows of the last tile are empty and fewer warps fit an SM. (3 requests of 90 to 200 queries of 4 heads:
-// 102 us against 107 with 8; 12 requests of 2 to 5 queries of 7 heads: 32.5 against 27.5.)
-constexpr int kWideRows = 96;
+// Query rows per KV head of an average request from which on they are many: tiles of 128 rows on tcgen05 where there are
+// enough such tiles (kv4_attention_tc.cu) and the head has at most 128 dimensions, else tiles of 16 here, which unpack K
+// and V half as often as tiles of 8, with more empty rows and fewer warps to an SM. Measured, tiles of 16 or 8 against 128
+// rows: 16 requests of 32 queries x 4 heads and 4000 tokens 191 us, 49 us; 16 of 16 x 7 heads and 4000 tokens 92, 39; 4
+// tiles of 112 rows, 16 of them of 128, 32 of 128: a geometric mean over contexts of 300 to 16000 tokens of 0.64, 1.35 and
+// 1.60 of the time here, the join of what many CTAs share included. Below 96 rows the two are closer than 1.2 but where
+// there are as many items as SMs. (12 requests of 2 to 5 queries x 7 heads: tiles of 16 take 32.5 us, of 8 27.5.)
+constexpr int kWideRows = 96, kTensorItems = 16;
 
 // rows: query rows per KV head of an average request; few: few items, each cut over several SMs.
 template <int D, int G>
@@ -1042,8 +1046,9 @@ size_t workspace_of(const Entry& e, int grid) {
     return kCounters * sizeof(uint32_t) + slots * e.part * sizeof(float);
 }
 
-// The kernel's shared memory, allowed once per kernel and device.
-cudaError_t allow_smem(const Entry& e) {
+}  // namespace
+
+cudaError_t kv4_allow_smem(const void* kernel, int bytes) {
     struct Done {
         std::atomic<const void*> fn;
         std::atomic<unsigned> devices;
@@ -1055,20 +1060,18 @@ cudaError_t allow_smem(const Entry& e) {
     Done* slot = nullptr;
     for (Done& d : done) {
         const void* fn = d.fn.load(std::memory_order_acquire);
-        if (!fn && d.fn.compare_exchange_strong(fn, e.fn)) fn = e.fn;
-        if (fn == e.fn) {
+        if (!fn && d.fn.compare_exchange_strong(fn, kernel)) fn = kernel;
+        if (fn == kernel) {
             slot = &d;
             break;
         }
     }
     const unsigned bit = dev < 32 ? 1u << dev : 0u;
     if (slot && (slot->devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    err = cudaFuncSetAttribute(e.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, e.smem);
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err == cudaSuccess && slot) slot->devices.fetch_or(bit, std::memory_order_release);
     return err;
 }
-
-}  // namespace
 
 size_t kv4_attention_workspace(int head_dim) {
     size_t most = 0;
@@ -1079,22 +1082,25 @@ size_t kv4_attention_workspace(int head_dim) {
                 const size_t n = workspace_of(e, grid_of(e, device_sm_count()));
                 most = n > most ? n : most;
             }
-    return most;
+    const size_t n = kv4_attention_tc_workspace(head_dim);
+    return n > most ? n : most;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     const int sms = device_sm_count();
     const int64_t gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
+    const int64_t with = a.B < a.T ? a.B : a.T;  // requests that have queries, at most
+    if (a.head_dim <= 128 && rows >= kWideRows && a.kv_heads * with * ((rows + 127) / 128) >= kTensorItems) return launch_kv4_attention_tc(a, s);
     const int64_t tile = rows < kWideRows || (a.head_dim == 256 && a.group == 32) ? 8 : 16;
     // items of requests of average size, and the most that requests of any sizes have
-    const int64_t with = a.B < a.T ? a.B : a.T, items = a.kv_heads * with * ((rows + tile - 1) / tile);
+    const int64_t items = a.kv_heads * with * ((rows + tile - 1) / tile);
     const int64_t most_items = a.kv_heads * (with + ((int64_t)a.T * gq + tile - 1) / tile);
     // CTAs as workers cut whole items among them, so there have to be more CTAs than items by enough (12 requests of 8
     // KV heads and 32768 tokens, 96 items: 119 us against 91 with warps; 64 items: 67 against 69; 8: 19 against 87).
     const bool few = 2 * items <= sms && most_items <= kItemsPerCta * sms;
     const Entry e = pick_for(a.head_dim, a.group, (int)(rows < kWideRows ? rows : kWideRows), few);
     if (e.smem > 48 * 1024) {
-        const cudaError_t err = allow_smem(e);
+        const cudaError_t err = kv4_allow_smem(e.fn, e.smem);
         if (err != cudaSuccess) return err;
     }
     int grid = grid_of(e, sms);
