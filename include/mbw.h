@@ -374,8 +374,12 @@ mbw_status mbw_kv4_gather(const mbw_kv4_cache *cache, const int64_t *slots, void
  * to its own. A query that sees no key gets zeros (lse: minus infinity). Keys
  * and values at places a query does not see, or past a request's length, do
  * not enter, whatever they hold.
+ * Products and sums are fp32; a softmax weight is rounded to fp16, and for
+ * chunks of a prompt (96 query rows per KV head and more) also s (code - 8), to
+ * 2^-8 of a step s. Results do not depend on the order in which CTAs run.
  * workspace: mbw_kv4_attention_workspace_bytes() bytes, zero before its first
- * use and left so by every call (one workspace per stream). Smaller or NULL:
+ * use; every call leaves it ready for the next (one workspace per stream).
+ * Smaller or NULL:
  * contexts are not split over CTAs, and long ones take longer.
  * A page id or length out of range is reported by mbw_check_device_error
  * (MBW_ERR_DEVICE_RANGE); that request's output is then unspecified.

@@ -1,5 +1,6 @@
 // kv4_attention.cu -- attention of one or several query tokens per request
-// over the 4-bit paged cache (layout in kv4.cuh).
+// over the 4-bit paged cache (layout in kv4.cuh). Chunks of a prompt, many query
+// rows per KV head, are kv4_attention_tc.cu's; the choice is at the launch below.
 //
 //   o_h = sum_t p_t v_t,  p = softmax over the keys t a query sees of
 //   scale * q_h . k_t,  k_t = s n + m from codes n, likewise v_t
@@ -43,9 +44,16 @@
 // that the result does not depend on who that is.
 //   Many items: each warp is a worker, and no warp waits for another. (With the
 // four warps of a CTA as one worker, joining them at every item, 64 requests of
-// 300 to 16000 tokens took 82 us.)
+// 300 to 16000 tokens took 82 us, and with blocks handed out by a counter 95 to 103.)
 //   Few items, each cut many times: a CTA of 16 warps is one, and its warps are
-// joined in shared memory, so that fewer parts go through the workspace.
+// joined in shared memory, so that fewer parts go through the workspace (1 request
+// of 65536 tokens: 21 us, of 4 heads and a part per SM; 87 with warps as workers).
+//
+// What bounds it: 64 requests of 300 to 16000 tokens, 308 MB, take 66 us, 4.7 TB/s;
+// the time of a further token is that of 6.0 TB/s, 88% of what a copy reaches, and 14
+// us are the start (lengths, block table and first block one behind the other), ends
+// that are not even, and the join of parts. One request of 1024 tokens takes 10.6 us,
+// all of it such latencies.
 #include <cuda_runtime.h>
 
 #include <math_constants.h>

@@ -14,6 +14,11 @@
 // below, a code is a function of the inputs alone, not of the order of
 // operations. A NaN or a value beyond fp16 makes its whole group NaN when it
 // is read, so it is not lost.
+//
+// What bounds it: for one token or some dozens the launch and its three dependent
+// loads (2.5 us each of append and gather, in a graph); for many the instructions,
+// some 2800 for a token of 28 + 8 rows: 8192 of them, 147 MB, take 30 us, 4.9 TB/s,
+// and 10 us to read back.
 #include <cuda_runtime.h>
 
 #include "internal.h"
