@@ -15,14 +15,17 @@
 // are few rows. A warp keeps one reference for all its lanes, so that its common
 // path is the sums and, for four 16-byte loads at a time, one comparison with the
 // gate: 74 instructions per 16-byte load of 8 logits. That bounds 2000 rows of 152064
-// 16-bit logits, 608 MB: 130 us, 4.7 TB/s, and 6.1 TB/s for a further row; the rest
-// is the tail of the last wave. 1 row with the 20 best: 12.7 us, 50 of 4-byte logits
-// with the 8 best 20.6, where the pieces' lists and their joins count. The
-// rare path, taken when a logit passes the warp's gate, moves the maximum and
-// inserts into the warp's list of top tokens, one entry per lane. The gate is
-// the k-th best so far, of the CTA, so it is passed some k ln(n) times. Lists
-// are joined by counting, for each entry, the better ones. Pieces of a row meet
-// in the workspace; the CTA that arrives last joins them in their order.
+// 16-bit logits, 608 MB: 124 us, 4.9 TB/s, and 6.1 TB/s for a further row.
+//   The rare path, taken when a logit passes the gate, moves the reference and takes
+// in candidates for the top tokens: into a buffer of the CTA, or in long pieces into
+// the warp's list, one entry per lane, in order. The first gate is the K-th largest
+// of the warps' best lanes' largest logits, which is little below the K-th best of
+// the first loads; the lists' K-th entries raise it. At the end the better ones of
+// each candidate are counted. Pieces of a row meet in the workspace; the CTA that
+// arrives last joins them in their order, and of their lists only what can still be
+// among the K best. (The 20 best of 1 row: 10.7 us, 6.9 without any; of 50 rows of
+// 4-byte logits 20.8 and 11.3; 32 with a list per warp and a gate that was the least
+// of the warps'.)
 #include <cuda_runtime.h>
 
 #include <math_constants.h>
@@ -38,6 +41,7 @@ __device__ int g_logprobs_range;  // a target was not below V
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;        // a warp's list is one entry per lane
+constexpr int kBuffer = kMaxTop * kMaxTop - kWarps * kMaxTop;  // candidates of a CTA, besides its warps' lists
 constexpr int kPieces = 8192;      // pieces that the workspace holds
 constexpr int kMaxSplit = 256;     // pieces of a row, one per thread of the CTA that joins them
 constexpr int kNoTau = (int)0x807FFFFF;  // minus infinity as an ordered whole number
@@ -228,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     __shared__ Cand sm_top[kMaxTop];
     __shared__ int sm_tau;  // k-th best logit of some warp of the CTA, as an ordered whole number
     __shared__ Cand sm_bound;    // the K-th best head of a row's pieces
-    __shared__ int sm_ref, sm_seed, sm_n, sm_lists, sm_last, sm_list[kMaxTop];
+    __shared__ int sm_seeds[kWarps * (kMaxTop / kWarps + 3)];
+    __shared__ int sm_ref, sm_n, sm_lists, sm_last, sm_list[kMaxTop];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = a.top_k;
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     uint4 ring[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) ring[u] = load(first + u * kThreads + tid);
-    if (tid == 0) sm_tau = sm_ref = kNoTau, sm_seed = INT_MAX, sm_n = 0;
+    if (tid == 0) sm_tau = sm_ref = kNoTau, sm_n = 0;
     __syncthreads();
 
     int target = a.targets ? a.targets[row] : -1;
@@ -299,6 +304,10 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     bool plain = true;
     Cand mine = {-CUDART_INF_F, INT_MAX};  // the warp's list, in order: entry `lane`
     float gate = -CUDART_INF_F;  // no logit up to this one moves the maximum or enters the list
+    // Where the first loads, which make the gate, are a fair share of the piece, few pass it: they go into a buffer of the
+    // CTA, ranked at the end. In long pieces the lists let the gate rise. (50 rows in 9 pieces each, the 32 best: 44 us with
+    // lists; 2000 rows of one piece with a buffer would rank some 30 times the tokens asked for.)
+    const bool append = v1 - v0 <= 6 * kThreads * AHEAD;
 
     // Logits as ordered whole numbers (a NaN below all), and back.
     auto tau_of = [](float v) {  // an ordered whole number, and back
@@ -307,6 +316,11 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     };
 
     auto value_of = [](int t) { return __int_as_float(t < 0 ? t ^ 0x7FFFFFFF : t); };
+
+    auto before_of = [](float v) {  // the number below
+        const int b = __float_as_int(v);
+        return v == -CUDART_INF_F ? v : v == 0.f ? -1.4012985e-45f : __int_as_float(b > 0 ? b - 1 : b + 1);
+    };
 
     auto settle = [&]() {  // the sums as if y had been exact
         const float f = exp2_fast(lag);
@@ -389,7 +403,26 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
                     for (int j = 0; j < E; ++j) has |= (uint32_t)(e[j] > kth && e[j] >= floor) << (u * E + j);
                 }
             }
-            uint32_t lanes = __ballot_sync(0xFFFFFFFFu, has != 0);
+            if (append && __any_sync(0xFFFFFFFFu, has != 0)) {
+                int n = __popc(has), at = n;  // the lanes' places in the CTA's buffer
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xFFFFFFFFu, at, o);
+                    if (lane >= o) at += y;
+                }
+                int start = 0;
+                if (lane == 31) start = atomicAdd(&sm_n, at);
+                at += __shfl_sync(0xFFFFFFFFu, start, 31) - n;
+                for (; __any_sync(0xFFFFFFFFu, has != 0 && at < kBuffer); ++at) {
+                    const int b = __ffs(has) - 1;
+                    const float v = pick(b);
+                    if (has && at < kBuffer) {
+                        sm_cand[at] = {v, (base + b / E * kThreads) * E - skew + b % E};
+                        has &= has - 1;
+                    }
+                }
+            }
+            uint32_t lanes = __ballot_sync(0xFFFFFFFFu, has != 0);  // with no place there: into the warp's list
             float now = kth;
             if (lanes) {
                 do {
@@ -408,9 +441,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
                 if (lane == 0 && now > floor) atomicMax(&sm_tau, tau_of(now));
             }
             // a logit equal to another warp's K-th may still be ahead of it, one equal to this warp's not
-            const int fb = __float_as_int(floor);
-            const float below = floor == -CUDART_INF_F ? floor : floor == 0.f ? -1.4012985e-45f : __int_as_float(fb > 0 ? fb - 1 : fb + 1);
-            gate = fminf(fmaxf(now, below), st.ref);
+            gate = fminf(fmaxf(now, before_of(floor)), st.ref);
         }
     };
 
@@ -429,31 +460,37 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
                 for (int u = 0; u < AHEAD; ++u) ring[u] = load(base + u * kThreads);
             }
             // The CTA's largest logit so far is what its other warps refer to at first: each with its own largest, they
-            // would have to move it some three times more. And a first gate for the lists: each warp holds
-            // ceil(K / 8) lanes whose largest logit is at least t, so the least t of the warps is not above the K-th
-            // best logit of the CTA.
+            // would have to move it some three times more. And a first gate for the lists: of the largest logits of
+            // each warp's best `seeds` lanes the K-th largest, which is not above the K-th best logit of the CTA.
             uint32_t most = L::largest2(ring[0]);
 #pragma unroll
             for (int u = 1; u < AHEAD; ++u) most = L::larger(most, L::largest2(ring[u]));
             const float big = L::value(most);
             int o = tau_of(big), t = __reduce_max_sync(0xFFFFFFFFu, o);
-            const int top = t;
-            for (int r = 1; r < (K + kWarps - 1) / kWarps; ++r) {
+            const int top = t, seeds = min(K, (K + kWarps - 1) / kWarps + 3);
+            for (int r = 0; r < seeds; ++r) {
                 const uint32_t who = __ballot_sync(0xFFFFFFFFu, o == t);
-                if (lane == __ffs(who) - 1) o = kNoTau;
+                if (lane == __ffs(who) - 1) sm_seeds[warp * seeds + r] = t, o = kNoTau;
                 t = __reduce_max_sync(0xFFFFFFFFu, o);
             }
-            if (lane == 0) {
-                atomicMax(&sm_ref, top);
-                if (K > 0) atomicMin(&sm_seed, t);
-            }
+            if (lane == 0) atomicMax(&sm_ref, top);
             __syncthreads();
             const int ref = sm_ref;
-            if (tid == 0 && K > 0) atomicMax(&sm_tau, sm_seed);
+            if (tid < kWarps * seeds) {
+                const int own = sm_seeds[tid];
+                int ahead = 0;
+                for (int j = 0; j < kWarps * seeds; ++j) {
+                    const int v = sm_seeds[j];
+                    ahead += v > own || (v == own && j < tid);
+                }
+                if (ahead == K - 1) atomicMax(&sm_tau, own);
+            }
             if (top != ref && st.ref == -CUDART_INF_F) {
                 refer(value_of(ref));
                 if (K == 0) gate = st.ref;
             }
+            if (K > 0) __syncthreads();
+            if (K > 0 && st.ref != -CUDART_INF_F) gate = fminf(before_of(value_of(sm_tau)), st.ref);
             __syncthreads();
         }
         const int step = phase == 1 ? tid : 0;
@@ -531,6 +568,8 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         __syncthreads();
     };
     if (K > 0) {
+        if (tid == 0) sm_n = min(sm_n, kBuffer);
+        __syncthreads();
         const int tau = sm_tau;  // entries below it are not among the K best; the order of the others does not matter
         if (lane < K && mine.i != INT_MAX && tau_of(mine.x) >= tau) sm_cand[atomicAdd(&sm_n, 1)] = mine;
         __syncthreads();
@@ -554,9 +593,12 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         __syncthreads();
         if (!sm_last) return;
         const Piece* of = pieces + (int64_t)row * split;
+        // Where there are fewer pieces than K, each holds `deep` entries that are not behind the worst of the deep-th ones:
+        // K in all, so that what is behind that is not among the K best.
+        const int deep = split < K ? (K + split - 1) / split : 1;
         Cand head = {-CUDART_INF_F, INT_MAX};
         if (K > 0) {
-            if (tid < split) head = {__ldcg(&of[tid].top[0].x), __ldcg(&of[tid].top[0].i)};
+            if (tid < split) head = {__ldcg(&of[tid].top[deep - 1].x), __ldcg(&of[tid].top[deep - 1].i)};
             sm_cand[tid] = head;  // those past split are no candidates
         }
         if (warp == 0) {  // the pieces in their order, 32 at a time to the warp's lanes, then those
@@ -571,12 +613,13 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         }
         __syncthreads();
         if (K > 0) {
-            // Only the pieces with the K best heads can hold one of the row's K best, in entries not behind the K-th.
+            // Else only the pieces with the K best heads can hold one of the row's K best, in entries not behind the K-th.
             if (head.i != INT_MAX) {
                 const int r = place(sm_cand, split, head);
-                if (r < K) sm_list[atomicAdd(&sm_lists, 1)] = tid;
-                if (r == K - 1) sm_bound = head;
+                if (split >= K && r < K) sm_list[atomicAdd(&sm_lists, 1)] = tid;
+                if (r == min(split, K) - 1) sm_bound = head;
             }
+            if (split < K && tid < split) sm_list[atomicAdd(&sm_lists, 1)] = tid;
             __syncthreads();
             const int entries = sm_lists * K;
             const Cand bound = sm_bound;
