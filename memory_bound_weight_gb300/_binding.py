@@ -475,6 +475,28 @@ def dequant_int4_awq_g128(Wq, scales, zeros):
 # The calls below are made many times per token, so their checks read each tensor once and compare devices by number; what
 # is wrong is told by the slower checks above.
 _dtypes = None
+_fast = None  # the compiled marshalling of these calls (csrc/fast_calls.cpp); False where it was not built
+
+
+def _load_fast():
+    global _fast
+    L = lib()
+    if not isinstance(L, ctypes.CDLL):  # a stand-in for the library sees the calls as the Python functions make them
+        return
+    path = os.path.join(os.path.dirname(LIB_PATH), "_fast.so")
+    if not os.path.exists(path):
+        _fast = False
+        return
+    import importlib.machinery
+    import importlib.util
+
+    _torch()  # the libraries it is linked to
+    loader = importlib.machinery.ExtensionFileLoader("_fast", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast", loader))
+    loader.exec_module(mod)
+    mod.init(*(ctypes.cast(f, ctypes.c_void_p).value
+               for f in (L.mbw_kv4_append, L.mbw_kv4_gather, L.mbw_kv4_attention, L.mbw_token_logprobs)))
+    _fast = mod
 
 
 def _types():
@@ -527,7 +549,7 @@ class Kv4Cache:
     """4-bit paged key/value cache over `pages`, a contiguous uint8 tensor (num_pages,
     kv4_page_bytes(page_size, kv_heads, head_dim, group)) that the caller owns."""
 
-    __slots__ = ("pages", "kv_heads", "head_dim", "page_size", "group", "_c")
+    __slots__ = ("pages", "kv_heads", "head_dim", "page_size", "group", "_c", "_addr")
 
     def __init__(self, pages, kv_heads, head_dim, page_size=16, group=64):
         size = kv4_page_bytes(page_size, kv_heads, head_dim, group)
@@ -536,6 +558,7 @@ class Kv4Cache:
             raise ValueError(f"pages must have {size} bytes per page, got {got}")
         self.pages, self.kv_heads, self.head_dim, self.page_size, self.group = pages, kv_heads, head_dim, page_size, group
         self._c = MbwKv4Cache(pages.data_ptr(), num, page_size, kv_heads, head_dim, group)
+        self._addr = ctypes.addressof(self._c)
 
 
 def kv4_page_bytes(page_size, kv_heads, head_dim, group=64):
@@ -575,6 +598,12 @@ def kv4_append(cache, k, v, slots, q=None, positions=None, cos_sin=None, interle
     wider QKV output; slots int64 (T,), page * page_size + place in the page, negative: not stored.
     positions int32 (T,) and cos_sin fp32 (max_pos, rotary_dim) (see rope_table) together, or neither:
     no rotation. Returns the rotated queries (`q_out`, which may be q, or a new tensor), None without q."""
+    if _fast is None:
+        _load_fast()
+    if _fast:
+        r = _fast.kv4_append(cache._addr, cache.pages, k, v, slots, q, positions, cos_sin, interleaved, q_out)
+        if r is not None:
+            return r[0] if r.__class__ is tuple else check("mbw_kv4_append", r)
     bf16, f32, i32, i64, _, empty = _types()
     hk, d = cache.kv_heads, cache.head_dim
     T, _, ks = _need_rows(k, "k", hk, d)
@@ -616,6 +645,12 @@ def kv4_append(cache, k, v, slots, q=None, positions=None, cos_sin=None, interle
 def kv4_gather(cache, slots):
     """The keys and values the cache holds at `slots` int64 (T,), each bf16 (T, kv_heads, head_dim); zeros for a
     negative slot."""
+    if _fast is None:
+        _load_fast()
+    if _fast:
+        r = _fast.kv4_gather(cache._addr, cache.pages, slots)
+        if r is not None:
+            return r if r.__class__ is tuple else check("mbw_kv4_gather", r)
     bf16, _, _, i64, _, empty = _types()
     T, = _plain(slots, "slots", i64, 1)
     dev = _check_devices(cache.pages, slots)
@@ -641,6 +676,13 @@ def kv4_attention(cache, q, block_table, ctx_lens, q_starts=None, scale=None, wi
     A query sees the keys up to its own position, with `window` > 0 only that many. scale: head_dim ** -0.5
     by default. Returns out (T, q_heads, head_dim), with return_lse also fp32 (T, q_heads). workspace: from
     kv4_attention_workspace; without one, long contexts are not split and take longer."""
+    if _fast is None:
+        _load_fast()
+    if _fast and out is None and not getattr(_tls, "fp32", False):
+        r = _fast.kv4_attention(cache._addr, cache.pages, q, block_table, ctx_lens, q_starts,
+                                cache.head_dim ** -0.5 if scale is None else scale, window, return_lse, workspace)
+        if r is not None:
+            return check("mbw_kv4_attention", r) if r.__class__ is int else r
     bf16, f32, i32, _, _, empty = _types()
     d = cache.head_dim
     T, hq, qs = _need_rows(q, "q", None, d)
@@ -688,6 +730,12 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, workspace=None):
     probability fp32 (M,) and rank int32 (M,) of targets int32 (M,) (None without), the entropy fp32 (M,) in
     nats, the top_k (<= 32) most likely ids int32 (M, top_k) and their log probabilities fp32 (M, top_k).
     workspace: from token_logprobs_workspace; without one, few rows take longer."""
+    if _fast is None:
+        _load_fast()
+    if _fast:
+        r = _fast.token_logprobs(logits, targets, top_k, scale, workspace)
+        if r is not None:
+            return TokenLogprobs._make(r) if r.__class__ is tuple else check("mbw_token_logprobs", r)
     bf16, f32, i32, _, _, empty = _types()
     try:
         shape, dtype, device = logits.shape, logits.dtype, logits.device

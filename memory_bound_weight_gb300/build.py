@@ -1,4 +1,5 @@
-"""Compile the CUDA sources of this package into libmbw.so (sm_103a only).
+"""Compile the CUDA sources of this package into libmbw.so (sm_103a only), and
+the binding's hot calls into _fast.so (g++, against the headers of PyTorch).
 
 One nvcc process per translation unit, run in parallel, then one link step.
 The library is built in-tree (memory_bound_weight_gb300/libmbw.so) and loaded
@@ -19,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmbw.so")
 GEN_LIB = os.path.join(PKG, "libmbw_inputs.so")
+FAST = os.path.join(PKG, "_fast.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -75,12 +77,37 @@ def _link(objs: list[str], out: str) -> None:
     os.replace(tmp, out)
 
 
+def _fast() -> None:
+    """_fast.so; where it cannot be compiled (no headers of Python or PyTorch) the binding marshals every call in Python."""
+    src = os.path.join(CSRC, "fast_calls.cpp")
+    if not _stale(FAST, [src, os.path.join(INCLUDE, "mbw.h")]):
+        return
+    import sysconfig
+
+    import torch
+
+    at, inc = os.path.dirname(torch.__file__), sysconfig.get_path("include")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(at, "include"), "-I", inc, "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+           "-I", INCLUDE, src, "-o", FAST + ".tmp", "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(f"_fast.so is not built, calls are marshalled in Python:\n{r.stderr[-2000:]}\n")
+        if os.path.exists(FAST):
+            os.remove(FAST)
+        return
+    os.replace(FAST + ".tmp", FAST)
+
+
 def build(ptxas_v: bool = False) -> str:
-    """Build libmbw.so and libmbw_inputs.so; returns the path of libmbw.so."""
+    """Build libmbw.so, libmbw_inputs.so and _fast.so; returns the path of libmbw.so."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = [os.path.join(CSRC, f) for f in LIB_SOURCES + GEN_SOURCES]
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        fast = ex.submit(_fast)
         objs = list(ex.map(lambda s: _compile(s, ptxas_v), srcs))
+        fast.result()
     _link(objs[: len(LIB_SOURCES)], LIB)
     _link(objs[len(LIB_SOURCES):], GEN_LIB)
     return LIB
