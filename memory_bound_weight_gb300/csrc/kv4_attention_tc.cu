@@ -53,6 +53,7 @@
 
 #include <math_constants.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -243,8 +244,10 @@ __device__ __forceinline__ bool no_number(uint32_t m) { return (m & 0x7C00u) == 
 constexpr int kRows = 128, kKeys = 128, kStages = 2;
 // Warps: softmax, 8 that unpack even tiles, 8 odd ones, one that issues the products, and 3 that only fill its warpgroup.
 constexpr int kSoftmax = 8, kUnpack = 8, kIssuer = kSoftmax + 2 * kUnpack, kWarps = kIssuer + 4, kThreads = kWarps * 32;
-// Registers: 72 a thread at launch, 64512 in all; then by warpgroup 2 x 104 + 4 x 64 + 40 = 504, times 128 the same.
-constexpr int kRegsSoftmax = 104, kRegsUnpack = 64, kRegsIssuer = 40;
+// Registers: 72 a thread at launch, 64512 in all; then by warpgroup 2 x 104 + 4 x 64 + 40 = 504, times 128 the same. A
+// build with fewer at launch could not hand them out, and is not launched.
+constexpr int kRegsSoftmax = 104, kRegsUnpack = 64, kRegsIssuer = 40, kRegsLaunch = 72;
+static_assert(kSoftmax * kRegsSoftmax + 2 * kUnpack * kRegsUnpack + 4 * kRegsIssuer <= kWarps * kRegsLaunch, "");
 constexpr int kCounters = 4096;  // of items cut between CTAs, as the other kernel's: both leave them at zero
 constexpr int kUp = 7;           // weights are 2^kUp p
 constexpr int kPieces = 8;       // of an item: the CTA that joins them reads 64 KB a piece, some 0.5 us
@@ -969,6 +972,14 @@ cudaError_t launch(const Kv4AttnArgs& a, int slots, int grid, cudaStream_t s) {
     static_assert(smem <= 227 * 1024, "");
     const cudaError_t err = kv4_allow_smem((const void*)kv4_attention_tc_kernel<D, G>, smem);
     if (err != cudaSuccess) return err;
+    static std::atomic<int> regs{0};
+    if (!regs.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes attr;
+        const cudaError_t e = cudaFuncGetAttributes(&attr, kv4_attention_tc_kernel<D, G>);
+        if (e != cudaSuccess) return e;
+        regs.store(attr.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return cudaErrorLaunchOutOfResources;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3((unsigned)kThreads, 1, 1);
