@@ -75,3 +75,19 @@ def test_append_of_more_tokens_than_a_wave_with_padding(hq, hk, d, group, rotary
         want = n * s + m
         want[::17] = 0
         assert ((ref.f64(got) - want).abs() <= ulp_bf16(want) * (1 + 2.0 ** -10)).all()
+
+
+@pytest.mark.parametrize("hk,d", [(5, 128), (8, 64), (3, 256), (1, 256)])
+def test_gather_of_many_tokens_is_that_of_few(hk, d):
+    """Many tokens take several heads a thread; the values are the same bits."""
+    T, page = 12000, 32
+    g = gen(75)
+    cache = new_cache(T // page + 3, page, hk, d, 32)
+    slots = torch.randperm((T // page + 3) * page, generator=g, device="cuda")[:T].long()
+    mbw.kv4_append(cache, normal(g, T, hk, d), normal(g, T, hk, d), slots)
+    slots[5::31] = -1
+    k, v = mbw.kv4_gather(cache, slots)
+    assert not torch.isnan(k).any() and (k[5::31] == 0).all() and (v[5::31] == 0).all()
+    for i in range(0, T, 700):
+        kk, vv = mbw.kv4_gather(cache, slots[i:i + 700].contiguous())
+        assert torch.equal(k[i:i + 700], kk) and torch.equal(v[i:i + 700], vv)
