@@ -42,9 +42,10 @@
 // in the order of which a fence waits for the loads behind it; 39 with copies and
 // offsets one a lane; 38 with the constants of the unpacking kept in registers; 35
 // with shared memory addressed as such, not through generic pointers; 31 with the
-// maximum taken in the pass of the weights, the first item found by one warp, and
-// halves of Q read by halves of the softmax: 490 TFLOP/s. 16 requests of 32 queries
-// of 32 heads and 4000 tokens take 49 us, 660 TFLOP/s.
+// maximum taken in the pass of the weights, the first item found by one warp, halves
+// of Q read by halves of the softmax, and joins at the roles' ends (33 with a join
+// behind each piece, whose registers the loops paid for): 500 TFLOP/s. 16 requests of
+// 32 queries of 32 heads and 4000 tokens take 49 us, 660 TFLOP/s.
 //
 // Tokens that some rows do not see may hold no numbers, and 0 times NaN is not 0:
 // V's groups that are no numbers become zeros, and where there was one in an
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     // the places before each thread's requests, and q0, nq and ctx of the one where a thread has no more
     uint4* prefix = reinterpret_cast<uint4*>(smem + L::OFF_PREFIX);
     __shared__ float sh_units[kWarps];
-    __shared__ uint32_t sh_sum[kWarps], sh_items[kWarps], sh_last;
+    __shared__ uint32_t sh_sum[kWarps], sh_items[kWarps];
     __shared__ float sh_max[2][kRows], sh_sums[2][kRows];
     __shared__ uint32_t sh_bad;  // the last key tile in which a group of V was no number, from 1
 
@@ -459,10 +460,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     // The first item is found by one warp: all of them at it take as long as the unpacking of a tile.
     __shared__ Item sh_first;
     __shared__ uint32_t sh_places;
+    __shared__ Item sh_items_cut[2];  // of which the CTA has a part: there are fewer places than two per CTA where items are cut
+    __shared__ int sh_cut, sh_last[2];
     __shared__ float sh_per_unit;
     if (warp == kIssuer) {
         const Item it = item_at(blockIdx.x);
-        if (lane == 0) sh_first = it, sh_places = W, sh_per_unit = per_unit;
+        if (lane == 0) sh_first = it, sh_places = W, sh_per_unit = per_unit, sh_cut = 0;
     }
     __syncthreads();
     W = sh_places, per_unit = sh_per_unit;
@@ -475,17 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         return it;
     };
     float* parts = reinterpret_cast<float*>(static_cast<uint32_t*>(a.workspace) + kCounters);
-    // The item's parts joined, by all threads, in order.
+    // An item's parts joined, in order, by the warps of softmax and unpacking.
     auto join = [&](const Item& it) {
-        bar_joiners();
-        if (tid == 0) {
-            __threadfence();
-            sh_last = atomicInc(static_cast<uint32_t*>(a.workspace) + it.first, it.pieces - 1) == it.pieces - 1;
-            __threadfence();
-        }
-        bar_joiners();
-        if (!sh_last) return;
-        if (warp == kIssuer) return;
         const float* part = parts + (size_t)it.first * L::PART;
         constexpr int LPR = D / 4, BATCH = 4;  // lanes of a row, four columns each; parts on their way at a time
         for (int r = warp * (32 / LPR) + lane / LPR; r < kRows; r += kIssuer * (32 / LPR)) {
@@ -521,6 +515,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 a.lse[(long long)(it.q0 + qi) * a.q_heads + it.h * gq + f - qi * gq] =
                     l == 0.f ? -CUDART_INF_F : (m + log2f(l) - kUp) * 0.69314718055994530942f;
         }
+    };
+
+    // At the end of a role: the CTA's parts are counted, and the items whose last part was among them joined. (At the end
+    // of each piece the roles' registers would be spilled around it.)
+    auto finish = [&](bool joins) {
+        if (per_unit == 0.f) return;
+        bar_joiners();
+        if (tid == 0) {
+            __threadfence();
+            for (int i = 0; i < sh_cut; ++i)
+                sh_last[i] = atomicInc(static_cast<uint32_t*>(a.workspace) + sh_items_cut[i].first, sh_items_cut[i].pieces - 1) == sh_items_cut[i].pieces - 1;
+            __threadfence();
+        }
+        bar_joiners();
+        if (!joins) return;
+#pragma unroll 1
+        for (int i = 0; i < sh_cut; ++i)
+            if (sh_last[i]) join(sh_items_cut[i]);
     };
 
     uint32_t tile = 0, count = 0;  // key tiles, and items with any, before this one: the phases of every barrier
@@ -745,8 +757,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             else if (there && a.lse)
                 a.lse[row * a.q_heads + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - kUp) * 0.69314718055994530942f;
             fence_before();
-            if (it.pieces > 1) join(it);
+            if (it.pieces > 1 && tid == 0) sh_items_cut[sh_cut++] = it;
         }
+        finish(true);
     } else if (warp < kIssuer) {
         // ------------------ unpack: a warp takes K, or V, of a block of 16 keys of each tile ----
         registers<kRegsUnpack>(false);
@@ -903,8 +916,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 copy(o_next, 1);
             }
             tile += it.n;
-            if (it.pieces > 1) join(it);
         }
+        finish(true);
     } else if (warp >= kIssuer) {
         registers<kRegsIssuer>(false);
         if (warp == kIssuer) {
@@ -950,8 +963,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 if (k > 0) outputs(tile - 1, k == 1);
             }
             if (it.n > 0) outputs(tile - 1, it.n == 1);
-            if (it.pieces > 1) join(it);
         }
+        finish(false);
         // every product issued has completed before TMEM is released
         if (leader) commit(done);
         __syncwarp();
