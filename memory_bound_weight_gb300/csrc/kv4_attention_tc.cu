@@ -679,7 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                     bar_any(2 + (warp & 3), false);  // sh_max is read
                 }
                 st16(s_at, w), st16(s_at + 16, w + 16);  // over columns that are read
-                if (k == it.n - 1) bar_wait(&vfull[tile % kStages], (tile / kStages) & 1, ok);  // for sh_bad, below
                 wait_st();
                 fence_before();
                 __syncwarp();
@@ -688,19 +687,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             // ---- outputs, or the item's part ----
             float l = 0.f, off[NG];
             uint32_t poison = 0;  // groups in which a key that the row sees is no number
-            if (it.n > 0 && *reinterpret_cast<volatile uint32_t*>(&sh_bad) > tile0) {
-                const int end = min(pos + 1, (it.bs + 8 * it.n) * 16);
-                for (int t = max(it.bs * 16, a.window ? pos - a.window + 1 : 0); t < end; ++t) {
-                    const int p = t / a.page_size, page = a.table[(long long)it.b * a.table_stride + p];
-                    const long long blk = ((long long)(page < 0 || page >= a.num_pages ? 0 : page) * a.kv_heads + it.h) * bpp + (t - p * a.page_size) / 16;
-                    const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.pages + blk * kv4_block_bytes(D, G) + kv4_meta(D, G, t & 15, 0, 1));
-#pragma unroll
-                    for (int gr = 0; gr < NG; ++gr) poison |= (uint32_t)no_number(meta[gr]) << gr;
-                }
-            }
             if (it.n > 0) {
+                // The last product is issued behind V's arrival in every tile, of the even set's warps and of the odd set's:
+                // behind this wait sh_bad is all that they found in the item.
                 bar_wait(&odone[(tile - 1) & 1], ((tile - 1) >> 1) & 1, ok);
                 fence_after();
+                if (*reinterpret_cast<volatile uint32_t*>(&sh_bad) > tile0) {
+                    const int end = min(pos + 1, (it.bs + 8 * it.n) * 16);
+                    for (int t = max(it.bs * 16, a.window ? pos - a.window + 1 : 0); t < end; ++t) {
+                        const int p = t / a.page_size, page = a.table[(long long)it.b * a.table_stride + p];
+                        const long long blk = ((long long)(page < 0 || page >= a.num_pages ? 0 : page) * a.kv_heads + it.h) * bpp + (t - p * a.page_size) / 16;
+                        const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.pages + blk * kv4_block_bytes(D, G) + kv4_meta(D, G, t & 15, 0, 1));
+#pragma unroll
+                        for (int gr = 0; gr < NG; ++gr) poison |= (uint32_t)no_number(meta[gr]) << gr;
+                    }
+                    __syncwarp();
+                }
                 uint32_t v[16];
                 ld16(v, my + L::O_COL + D);
                 wait_ld16(v);
