@@ -45,6 +45,7 @@ constexpr int kBuffer = kMaxTop * kMaxTop - kWarps * kMaxTop;  // candidates of 
 constexpr int kPieces = 8192;      // pieces that the workspace holds
 constexpr int kMaxSplit = 256;     // pieces of a row, one per thread of the CTA that joins them
 constexpr int kNoTau = (int)0x807FFFFF;  // minus infinity as an ordered whole number
+constexpr float kFar = 1e8f;       // |shift| from which on terms are taken plainly; below it |lag| <= 4
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct Cand {  // a logit and its index; better: larger, then the lower index
@@ -297,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
     float counted = 0.f;
     // y = (x - best) * c2 as x c2 + shift in one operation. shift is off by -lag, for all logits alike, which is put
     // right when best moves and at the end. Logits are first raised to `low`, where y is below -150 and finite: their
-    // e is 0, and 0 times it. Where best is beyond 1e37 (a row that is masked throughout with the type's lowest
-    // value), plainly.
+    // e is 0, and 0 times it. Where best is kFar away or more (a mask of finite numbers over a whole row), plainly: lag
+    // would not stay small beside fp32's range, nor 160 / c2 beside best's own last place.
     float shift = 0.f, lag = 0.f;
     uint32_t low = 0;
     bool plain = true;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         st.ref = x;
         shift = -x * c2, lag = fmaf(-x, c2, -shift);
         const float cut = x - 160.f / c2;
-        plain = !(fabsf(shift) < 1e37f) || !(cut > -1e37f) || !(x < 1e37f);
+        plain = !(fabsf(shift) < kFar) || !(cut > -1e37f) || !(x < 1e37f);
         low = L::below(cut);
     };
     // Where the largest of the loads in hand is, among equals the first: its number in them, and its index.
