@@ -25,7 +25,7 @@
 //   sum p (s n + m) = [sum w n - 8 sum w] / 4 + sum p (m + 8 s)
 // with the same rounded w in both sums, so that its rounding (2^-11) acts on
 // the centred code n - 8 only; 8 sum w comes from a constant tile. p <= 1
-// against the running maximum and s <= 8737 in fp16, so w cannot overflow; the
+// against the running maximum and s <= 8704 (values within fp16), so w cannot overflow; the
 // factor 4 moves w's subnormal range to p s < 1.5e-5. Scores, maxima, sums and
 // outputs are fp32.
 //

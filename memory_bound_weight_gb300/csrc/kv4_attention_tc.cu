@@ -47,9 +47,10 @@
 // behind each piece, whose registers the loops paid for): 500 TFLOP/s. 16 requests of
 // 32 queries of 32 heads and 4000 tokens take 49 us, 660 TFLOP/s.
 //
-// Tokens that some rows do not see may hold no numbers, and 0 times NaN is not 0:
-// V's groups that are no numbers become zeros, and where there was one in an
-// item, its rows look at the tokens that they see once more at the end.
+// Tokens that some rows do not see may hold no numbers, or bytes that no append
+// wrote, whose products pass fp16; and 0 times NaN is not 0: V's groups of either
+// kind become zeros, and where there was one in an item, its rows look at the tokens
+// that they see once more at the end.
 #include <cuda_runtime.h>
 
 #include <math_constants.h>
@@ -240,7 +241,13 @@ __device__ __forceinline__ uint32_t offset_of(uint32_t m) {
     const uint32_t hi = pack(c, 0.f);
     return pack(__half2float(__ushort_as_half((unsigned short)hi)), c - __half2float(__ushort_as_half((unsigned short)hi)));
 }
-__device__ __forceinline__ bool no_number(uint32_t m) { return (m & 0x7C00u) == 0x7C00u || (m & 0x7C000000u) == 0x7C000000u; }
+// Whether a pair, whose offset is given, makes operands that are no numbers: one that is none itself, or that an append
+// does not write (of finite values its scale is at most 8704, whose 7.5 steps are 65280, or minus zero, and its centre lies
+// between them), as a place that was never written may hold.
+__device__ __forceinline__ bool no_number(uint32_t m, uint32_t offset) {
+    const uint32_t s = m & 0xFFFFu;
+    return (s > 0x7040u && s != 0x8000u) || (offset & 0x7C00u) == 0x7C00u;
+}
 
 constexpr int kRows = 128, kKeys = 128, kStages = 2;
 // Warps: softmax, 8 that unpack even tiles, 8 odd ones, one that issues the products, and 3 that only fill its warpgroup.
@@ -699,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                         const long long blk = ((long long)(page < 0 || page >= a.num_pages ? 0 : page) * a.kv_heads + it.h) * bpp + (t - p * a.page_size) / 16;
                         const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.pages + blk * kv4_block_bytes(D, G) + kv4_meta(D, G, t & 15, 0, 1));
 #pragma unroll
-                        for (int gr = 0; gr < NG; ++gr) poison |= (uint32_t)no_number(meta[gr]) << gr;
+                        for (int gr = 0; gr < NG; ++gr) poison |= (uint32_t)no_number(meta[gr], offset_of(meta[gr])) << gr;
                     }
                     __syncwarp();
                 }
@@ -869,13 +876,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 for (int i = 0; i < PER; ++i) {
                     const int j = lane + 32 * i;
                     if (16 * NG % 32 && lane >= 16 * NG) break;
-                    uint32_t y = vmeta[j];
+                    const uint32_t y = vmeta[j];
                     const bool unseen = (it.bs + 8 * k + u) * 16 + j / NG > it.pos_hi;
-                    if (unseen || no_number(y)) {
-                        if (!unseen) atomicMax(&sh_bad, tile + k + 1);
-                        vmeta[j] = y = 0;
-                    }
                     off[i] = offset_of(y);
+                    if (unseen || no_number(y, off[i])) {
+                        if (!unseen) atomicMax(&sh_bad, tile + k + 1);
+                        vmeta[j] = off[i] = 0;
+                    }
                 }
                 __syncwarp();
                 if (turn) bar_wait(&vempty[set], (turn - 1) & 1, ok);

@@ -12,14 +12,19 @@
 // code = clamp(rint((x - m) / s), 0, 15), 0 where s = 0; each step one IEEE
 // fp32 operation. With the rotation summed to about twice fp32's precision
 // below, a code is a function of the inputs alone, not of the order of
-// operations. A NaN or a value beyond fp16 makes its whole group NaN when it
-// is read, so it is not lost.
+// operations. A NaN or a value beyond fp16 (one that would round to its infinity)
+// makes its whole group NaN when it is read, so it is not lost: a minimum beyond it
+// by itself, a maximum through a scale that is none. Finite scales are then at most
+// 8704, (65280 + 65280) / 15 with the largest bf16 values within fp16, which the
+// attention kernels' operands rely on.
 //
 // What bounds it: for one token or some dozens the launch and its three dependent
 // loads (2.5 us each of append and gather, in a graph); for many the instructions,
 // some 2800 for a token of 28 + 8 rows: 8192 of them, 147 MB, take 30 us, 4.9 TB/s,
 // and 10 us to read back.
 #include <cuda_runtime.h>
+
+#include <math_constants.h>
 
 #include "internal.h"
 #include "kv4.cuh"
@@ -112,7 +117,7 @@ __device__ __forceinline__ uint32_t quantize8(const float* x, uint32_t& meta) {
     }
     const __half mh = __float2half_rn(lo);
     const float m = __half2float(mh);
-    const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, m), 15.0f));
+    const __half sh = __float2half_rn(hi < 65520.f ? __fdiv_rn(__fsub_rn(hi, m), 15.0f) : CUDART_NAN_F);
     const float s = __half2float(sh);
     meta = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(mh) << 16);
     // (x - m) / s, correctly rounded, as Markstein (IBM J. Res. Dev. 1990) gets it from the correctly rounded
