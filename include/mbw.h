@@ -381,8 +381,10 @@ mbw_status mbw_kv4_gather(const mbw_kv4_cache *cache, const int64_t *slots, void
  * use; every call leaves it ready for the next (one workspace per stream).
  * Smaller or NULL:
  * contexts are not split over CTAs, and long ones take longer.
- * A page id or length out of range is reported by mbw_check_device_error
- * (MBW_ERR_DEVICE_RANGE); that request's output is then unspecified.
+ * A page id, length or query offset out of range is reported by
+ * mbw_check_device_error (MBW_ERR_DEVICE_RANGE); that request's output is then
+ * unspecified, and where q_starts falls the whole call's. Nothing else is
+ * written, and the workspace is left ready all the same.
  */
 mbw_status mbw_kv4_attention(const mbw_kv4_cache *cache, const void *q, int64_t q_stride, void *out,
                              int64_t out_stride, float *lse, const int32_t *block_table, int64_t table_stride,

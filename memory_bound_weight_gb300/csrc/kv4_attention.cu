@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     const float sl2 = fabsf(a.scale) * 1.44269504088896340736f;
     uint32_t* counters = static_cast<uint32_t*>(a.workspace);
     float* parts = reinterpret_cast<float*>(counters + kCounters);
-    bool bad = false;
+    bool bad = false, falls = false;
     if ((COOP ? tid : lane) < 2) sh_pend[own][COOP ? tid : lane].n = 0;
 
     pdl_launch_dependents();
@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             q0 = min(max(s0, 0), a.T);
             q1 = min(max(s1, q0), a.T);
             if (q0 != s0 || q1 != s1) bad = true;
+            if (s1 < s0) falls = true;
         } else {
             const int n = a.T / a.B;
             q0 = b * n, q1 = q0 + n;
@@ -275,7 +276,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         mine.x = before + sum - x;
         prefix[tid] = mine;
         if (tid == 0) prefix[THREADS].x = W;
-        __syncthreads();
+        // Offsets that fall make ranges that overlap, and more items than the launch left room for: then there is no work.
+        if (__syncthreads_or(falls)) W = 0;
     }
     // Warps: as many as items at least; worker i of C has the places [i each + min(i, rest), ...). CTAs: one place, and
     // where there are more pieces than CTAs the others behind it.

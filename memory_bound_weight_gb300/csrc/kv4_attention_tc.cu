@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = a.q_heads / a.kv_heads, bpp = a.page_size / 16;
-    bool bad = false, ok = true;
+    bool bad = false, falls = false, ok = true;
 
     if (tid == 0) {
         sh_bad = 0;
@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             q0 = min(max(s0, 0), a.T);
             q1 = min(max(s1, q0), a.T);
             if (q0 != s0 || q1 != s1) bad = true;
+            if (s1 < s0) falls = true;
         } else {
             const int n = a.T / a.B;
             q0 = b * n, q1 = q0 + n;
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         for (int w = 0; w < kWarps; ++w) before += w < warp ? sh_sum[w] : 0, W += sh_sum[w];
         mine.x = before + sum - n;
         prefix[tid] = mine;
-        __syncthreads();
+        if (__syncthreads_or(falls)) W = 0;  // ranges that overlap: no work, as in kv4_attention.cu
     }
     const uint32_t tmem = *tmem_slot;
 
@@ -423,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             set_per_unit(warp_sum((float)mine.tiles * (float)mine.units), __reduce_add_sync(0xFFFFFFFFu, (uint32_t)mine.tiles) * a.kv_heads);
             const uint32_t n = (uint32_t)mine.tiles * a.kv_heads * pieces_of(mine), sum = scan(n);
             W = __shfl_sync(0xFFFFFFFFu, sum, 31);
+            if (__any_sync(0xFFFFFFFFu, falls)) W = 0;
             it.n = -1;
             if (place >= W) return it;
             it.b = __ffs(__ballot_sync(0xFFFFFFFFu, sum > place)) - 1;
