@@ -47,6 +47,9 @@ __host__ __device__ __forceinline__ int kv4_meta(int D, int G, int t, int i, int
     return 16 * D + v * 64 * (D / G) + (t * (D / G) + i) * 4;
 }
 
+// The first position that a query at pos sees under a window; pos may lie far before 0, and the window be any.
+__device__ __forceinline__ int kv4_first_seen(int pos, int window) { return window && pos + 1 > window ? pos + 1 - window : 0; }
+
 __device__ __forceinline__ float2 kv4_pair(uint32_t m) {
     return __half22float2(*reinterpret_cast<const __half2*>(&m));
 }

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     auto sized = [&](int q0, int nq, int ctx) {
         Request r;
         r.q0 = q0, r.nq = nq, r.ctx = ctx;
-        r.fb = a.window ? max(0, ctx - nq - a.window + 1) / 16 : 0;
+        r.fb = kv4_first_seen(ctx - nq, a.window) / 16;
         r.units = max(1u, ((uint32_t)((ctx + 15) / 16 - r.fb) + unit - 1) / unit);
         r.qt = ((uint32_t)nq * gq + ROWS - 1) / ROWS;  // at most MBW_MAX_DIM query rows
         r.tiles = (uint32_t)r.qt * a.kv_heads;
@@ -626,8 +626,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         const int f0 = (int)(item - (uint32_t)h * rq.qt) * ROWS;
         const int pos_lo = ctx - nq + f0 / gq, pos_hi = ctx - nq + min(nq - 1, (f0 + ROWS - 1) / gq);
         {
-            const int k_lo = a.window ? max(0, pos_lo - a.window + 1) : 0;
-            bs = max(rq.fb + (int)u0 * unit, k_lo / 16);
+            bs = max(rq.fb + (int)u0 * unit, kv4_first_seen(pos_lo, a.window) / 16);
             be = (int)min((long long)rq.fb + (long long)u1 * unit, (long long)max(pos_hi + 16, 0) / 16);
             be = max(bs, be);
             nsteps = be > bs + at * NB ? (be - bs - at * NB + S::STEP - 1) / S::STEP : 0;

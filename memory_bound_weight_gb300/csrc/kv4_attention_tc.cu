@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         it.q0 = r.q0, it.nq = r.nq, it.ctx = r.ctx;
         it.pos_lo = r.ctx - r.nq + it.f0 / gq;
         it.pos_hi = r.ctx - r.nq + min(r.nq - 1, (it.f0 + kRows - 1) / gq);
-        const int b0 = a.window ? max(0, it.pos_lo - a.window + 1) / 16 : 0, b1 = max(it.pos_hi + 16, 0) / 16;
+        const int b0 = kv4_first_seen(it.pos_lo, a.window) / 16, b1 = max(it.pos_hi + 16, 0) / 16;
         const int total = max(0, b1 - b0 + 7) / 8;
         const int each = total / (int)it.pieces, rest = total - each * (int)it.pieces, p = (int)it.piece;
         it.bs = b0 + (p * each + min(p, rest)) * 8;
