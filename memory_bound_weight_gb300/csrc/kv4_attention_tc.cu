@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = a.q_heads / a.kv_heads, bpp = a.page_size / 16;
-    bool bad = false, falls = false, ok = true;
+    bool bad = false, ok = true;
 
     if (tid == 0) {
         sh_bad = 0;
@@ -345,7 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             q0 = min(max(s0, 0), a.T);
             q1 = min(max(s1, q0), a.T);
             if (q0 != s0 || q1 != s1) bad = true;
-            if (s1 < s0) falls = true;
         } else {
             const int n = a.T / a.B;
             q0 = b * n, q1 = q0 + n;
@@ -354,6 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         if (ctx > cap) bad = true, ctx = cap;
         return sized(q0, q1 - q0, ctx);
     };
+    // Offsets that fall make ranges that overlap: then there is no work, as in kv4_attention.cu. Looked for once, at the start.
+    auto offsets_fall = [&](int b) { return a.q_starts && a.q_starts[b + 1] < a.q_starts[b]; };
     // Up to 32 requests are a lane's each, and every warp finds its items by itself; more are shared out over the threads.
     const bool lanes = a.B <= 32;
     const int stride = (a.B + kThreads - 1) / kThreads;  // requests per thread
@@ -374,11 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     if (!lanes) {
         float units = 0.f;
         uint32_t items = 0, n = 0;
+        bool falls = false;
         uint4 mine = make_uint4(0, 0, 0, 0);
         for (int i = 0; i < stride; ++i) {
             const int b = tid * stride + i;
             if (b < a.B) {
                 const Request r = request(b);
+                falls |= offsets_fall(b);
                 mine.y = r.q0, mine.z = r.nq, mine.w = r.ctx;
                 units += (float)r.tiles * (float)r.units, items += r.tiles;
             }
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         for (int w = 0; w < kWarps; ++w) before += w < warp ? sh_sum[w] : 0, W += sh_sum[w];
         mine.x = before + sum - n;
         prefix[tid] = mine;
-        if (__syncthreads_or(falls)) W = 0;  // ranges that overlap: no work, as in kv4_attention.cu
+        if (__syncthreads_or(falls)) W = 0;
     }
     const uint32_t tmem = *tmem_slot;
 
@@ -424,7 +427,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             set_per_unit(warp_sum((float)mine.tiles * (float)mine.units), __reduce_add_sync(0xFFFFFFFFu, (uint32_t)mine.tiles) * a.kv_heads);
             const uint32_t n = (uint32_t)mine.tiles * a.kv_heads * pieces_of(mine), sum = scan(n);
             W = __shfl_sync(0xFFFFFFFFu, sum, 31);
-            if (__any_sync(0xFFFFFFFFu, falls)) W = 0;
             it.n = -1;
             if (place >= W) return it;
             it.b = __ffs(__ballot_sync(0xFFFFFFFFu, sum > place)) - 1;
@@ -473,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     __shared__ int sh_cut, sh_last[2];
     __shared__ float sh_per_unit;
     if (warp == kIssuer) {
-        const Item it = item_at(blockIdx.x);
+        Item it = item_at(blockIdx.x);
+        if (lanes && __any_sync(0xFFFFFFFFu, lane < a.B && offsets_fall(lane))) it.n = -1, W = 0;
         if (lane == 0) sh_first = it, sh_places = W, sh_per_unit = per_unit, sh_cut = 0;
     }
     __syncthreads();
