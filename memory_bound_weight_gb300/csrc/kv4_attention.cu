@@ -70,6 +70,11 @@ namespace {
 
 __device__ int g_kv4_attn_range;  // a page id, length or query offset was out of range
 
+// A weight's exponent is formed in one operation, the score times its factor less the maximum's, which is rounded; from
+// maxima of this size on (in powers of two) that rounding, 2^-10 of a power here and as many as a float holds further out,
+// would show, and the difference of the scores is taken first.
+constexpr float kFar = 16384.f;
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -718,6 +723,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         // scores are kept as s and m give them; col_scale (>= 0) takes those of a column to powers of two
         auto col_scale = [&](int nt, int e) { return NT == 1 ? qscale[e] : qsums[NG * ROWS + 8 * nt + 2 * c + e]; };
 
+        bool far = false;  // some row's maximum is kFar or more from 0
         for (int k = 0; k < nsteps; ++k) {
             cp_async_wait<DEPTH - 2>();
             __syncwarp();  // the step's copies of every lane are there, and step k - 1 is read
@@ -834,20 +840,34 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) o[nt][i][e] *= f, o[nt][i][2 + e] *= f;
                     }
+                bool out = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) out |= M[nt][e] != -CUDART_INF_F && !(fabsf(M[nt][e] * col_scale(nt, e)) < kFar);
+                far = __any_sync(0xFFFFFFFFu, out);
             }
             // weights 4 p
+            auto weights = [&](auto far_step) {
+                constexpr bool FAR = decltype(far_step)::value;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = col_scale(nt, e), m = M[nt][e] == -CUDART_INF_F ? 0.f : fmaf(-M[nt][e], f, 2.f);
+                    for (int e = 0; e < 2; ++e) {
+                        const bool none = M[nt][e] == -CUDART_INF_F;
+                        const float f = col_scale(nt, e), base = none ? 0.f : M[nt][e], m = none ? 0.f : FAR ? 2.f : fmaf(-M[nt][e], f, 2.f);
 #pragma unroll
-                    for (int sub = 0; sub < NB; ++sub) {
-                        y[sub][nt][e] = exp2_fast(fmaf(y[sub][nt][e], f, m));
-                        y[sub][nt][2 + e] = exp2_fast(fmaf(y[sub][nt][2 + e], f, m));
-                        L[nt][e] += y[sub][nt][e] + y[sub][nt][2 + e];
+                        for (int sub = 0; sub < NB; ++sub) {
+                            y[sub][nt][e] = exp2_fast(fmaf(FAR ? y[sub][nt][e] - base : y[sub][nt][e], f, m));
+                            y[sub][nt][2 + e] = exp2_fast(fmaf(FAR ? y[sub][nt][2 + e] - base : y[sub][nt][2 + e], f, m));
+                            L[nt][e] += y[sub][nt][e] + y[sub][nt][2 + e];
+                        }
                     }
-                }
+            };
+            if (far)
+                weights(std::true_type());
+            else
+                weights(std::false_type());
             auto values = [&](auto edge_step) {
                 constexpr bool EDGE = decltype(edge_step)::value;
 #pragma unroll

@@ -201,6 +201,12 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t
 __device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 __device__ __forceinline__ uint32_t pack(float a, float b) { return h2(__floats2half2_rn(a, b)); }
+// The same, the largest finite number in the place of what is beyond it (a NaN stays one).
+__device__ __forceinline__ uint32_t pack_finite(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
 
 // Nibbles 0 and 4, 1 and 5, 2 and 6, 3 and 7 of a word, less 8 each, times s and plus d: the codes ORed into the bits of
 // 1024 and of 64, an exact subtraction, one rounding. The constants are held in registers, opaque to the compiler, which
@@ -623,6 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 if (lane == 0) bar_arrive(qfull);
             }
             float M = -CUDART_INF_F;
+            // What a score's power of two is off its weight's. Rounded up, so that the maximum's weight is at least 2^kUp however
+            // large the scores are; beyond 2^24, where the rounding passes a power of two, a weight may pass fp16, and its
+            // largest number takes its place: the keys that have it are as near to each other as scores of 32 bits are.
+            auto offset_to = [&](float m) { return m == -CUDART_INF_F ? 0.f : __fmaf_ru(-m, scale_row, (float)kUp); };
             const uint32_t tile0 = tile;
             for (int k = 0; k < it.n; ++k, ++tile) {
                 const uint32_t sb = tile & 1, s_at = my + L::S_COL + sb * 128 + 64 * half;
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 // One pass for the weights against the maximum so far and for the tile's own; another where that has
                 // grown too far, which is rare behind the first tile.
                 uint32_t w[32];
-                float m, off = M == -CUDART_INF_F ? 0.f : fmaf(-M, scale_row, (float)kUp);
+                float m, off = offset_to(M);
                 auto pass = [&](auto edge_tile, auto maximum_alone) {
                     constexpr bool EDGE = decltype(edge_tile)::value, ALONE = decltype(maximum_alone)::value;
                     float m2[2] = {-CUDART_INF_F, -CUDART_INF_F};
@@ -654,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                             m2[i & 1] = max3(m2[i & 1], see_x ? x : -CUDART_INF_F, see_y ? y : -CUDART_INF_F);
                             if (ALONE) continue;
                             const float2 e = fma2(make_float2(x, y), make_float2(scale_row, scale_row), make_float2(off, off));
-                            w[16 * c + i] = pack(see_x ? exp2_fast(e.x) : 0.f, see_y ? exp2_fast(e.y) : 0.f);
+                            w[16 * c + i] = pack_finite(see_x ? exp2_fast(e.x) : 0.f, see_y ? exp2_fast(e.y) : 0.f);
                         }
                     }
                     m = fmaxf(m2[0], m2[1]);
@@ -672,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                     m = fmaxf(m, sh_max[half ^ 1][r]);
                     raise = m > M && (M == -CUDART_INF_F || (m - M) * scale_row > kGrow);
                     if (k > 0) {
-                        const float e = raise && M != -CUDART_INF_F ? exp2_fast((M - m) * scale_row) : 1.f;
+                        const float e = raise && M != -CUDART_INF_F ? exp2_fast(offset_to(m) - off) : 1.f;
                         bar_wait(&odone[(tile - 1) & 1], ((tile - 1) >> 1) & 1, ok);  // the products into the outputs so far
                         fence_after();
 #pragma unroll 1
@@ -686,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                         }
                     }
                     if (raise) M = m;
-                    off = M == -CUDART_INF_F ? 0.f : fmaf(-M, scale_row, (float)kUp);
+                    off = offset_to(M);
                     pass(std::true_type(), std::false_type());
                     bar_any(2 + (warp & 3), false);  // sh_max is read
                 }
@@ -723,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 for (int gr = 0; gr < NG; ++gr)
                     off[gr] = poison >> gr & 1 ? CUDART_NAN_F : __uint_as_float(v[2 * gr]) + __uint_as_float(v[2 * gr + 1]);
             }
-            const float m2 = M == -CUDART_INF_F ? M : M * scale_row;
+            const float m2 = M == -CUDART_INF_F ? M : kUp - offset_to(M);  // what the weights refer to
             const float inv = it.pieces > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
             float* part = parts + (size_t)place * L::PART;
             const long long to = row * a.out_stride + (long long)head * D;
