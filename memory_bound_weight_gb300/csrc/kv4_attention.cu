@@ -20,14 +20,18 @@
 // q is scaled by a power of two per row so that its largest entry lies in
 // [2^14, 2^15), and by another 2^-4 at the places of the 2^-20 codes: fp16 then
 // holds bf16 entries exactly down to 2^-24 of the largest, smaller ones to
-// within 2^-35 of it. The softmax weight p enters as w = fp16(4 p s), one per
+// within 2^-35 of it. The softmax weight p enters as w = fp16(2^u p s), one per
 // group:
-//   sum p (s n + m) = [sum w n - 8 sum w] / 4 + sum p (m + 8 s)
+//   sum p (s n + m) = [sum w n - 8 sum w] / 2^u + sum p (m + 8 s)
 // with the same rounded w in both sums, so that its rounding (2^-11) acts on
 // the centred code n - 8 only; 8 sum w comes from a constant tile. p <= 1
-// against the running maximum and s <= 8704 (values within fp16), so w cannot overflow; the
-// factor 4 moves w's subnormal range to p s < 1.5e-5. Scores, maxima, sums and
-// outputs are fp32.
+// against the running maximum, and u follows the largest scale so far: 2^u s is
+// below 2^15, and was between 2^13 and 2^14 when that scale came, so that a weight
+// keeps its 11 bits down to p = 2^-26 and is lost only below 2^-37, whatever the
+// size of the values. (With 4 p s the weights of many small p beside a large one
+// were lost where values are small: at 1e-4 the sum of 2000 of them, half the
+// result.) Each lane looks at the scales of its share of a step's tokens, which takes
+// 2.5% of the time at 64 requests. Scores, maxima, sums and outputs are fp32.
 //
 // Unpacking is thus one AND per pair and a shift for every other pair. It runs
 // on the ALU pipe at half rate, which bounded the forms before: with a shift
@@ -724,12 +728,40 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         auto col_scale = [&](int nt, int e) { return NT == 1 ? qscale[e] : qsums[NG * ROWS + 8 * nt + 2 * c + e]; };
 
         bool far = false;  // some row's maximum is kFar or more from 0
+        // weights are 2^up p; in the lower half of limit the largest scale that this has room for, as fp16 bits
+        float up = 2.f;
+        uint32_t limit = 0x7FFF8000u;
         for (int k = 0; k < nsteps; ++k) {
             cp_async_wait<DEPTH - 2>();
             __syncwarp();  // the step's copies of every lane are there, and step k - 1 is read
             issue(k + DEPTH - 1);
             const uint8_t* stage = my_ring + (k % DEPTH) * NB * BB;
             const int blk0 = bs + (k * STRIDE + at) * NB;
+
+            // Some key of this step may be unseen by some row, or lie past the segment.
+            const bool edge = blk0 + NB > be || (blk0 + NB) * 16 - 1 > pos_lo ||
+                              (a.window && blk0 * 16 <= pos_hi - a.window);
+            // limit, or a larger scale of V of the lane's share of the tokens
+            uint32_t most = limit, ms[NB * (NG > 2 ? NG / 2 : 1)];
+            constexpr int SHARE = NG > 2 ? NG / 2 : 1;
+#pragma unroll
+            for (int sub = 0; sub < NB; ++sub) {
+                const int first = NG > 1 ? lane * SHARE : lane & 15;
+                uint32_t m[SHARE];
+                load_meta<SHARE>(stage + sub * BB + kv4_meta(D, G, 0, 0, 1) + 4 * first, m);
+#pragma unroll
+                for (int i = 0; i < SHARE; ++i) {
+                    if (edge) {  // not that of a token that no row sees
+                        const int t = (blk0 + sub) * 16 + (first + i) / NG;
+                        if (blk0 + sub >= be || t > pos_hi || (a.window && t <= pos_lo - a.window)) m[i] = 0x8000u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < SHARE; ++i) ms[sub * SHARE + i] = m[i];
+            }
+#pragma unroll
+            for (int i = 0; i + 1 < NB * SHARE; i += 2) most = __vimax3_s16x2(ms[i], ms[i + 1], most);
+            if (NB * SHARE % 2) most = __vmaxs2(most, ms[NB * SHARE - 1]);
 
             // scores y of NB blocks: rows g and g + 8 (tokens), columns 2c and 2c + 1 of each n-tile
             float y[NB][NT][4];
@@ -793,9 +825,6 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                     }
                 }
             }
-            // Some key of this step may be unseen by some row, or lie past the segment.
-            const bool edge = blk0 + NB > be || (blk0 + NB) * 16 - 1 > pos_lo ||
-                              (a.window && blk0 * 16 <= pos_hi - a.window);
             uint32_t seen = 0xFFFFFFFFu;
             static_assert(NB * NT * 4 <= 32, "one bit per score");
             if (edge) {
@@ -812,7 +841,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                             }
                         }
             }
-            bool raise = false;
+            bool raise = most != limit;
 #pragma unroll
             for (int sub = 0; sub < NB; ++sub)
 #pragma unroll
@@ -820,6 +849,13 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
                     for (int e = 0; e < 4; ++e) raise |= y[sub][nt][e] > M[nt][e & 1];
             if (__any_sync(0xFFFFFFFFu, raise)) {
+                float less = 1.f;  // of 2^up
+                const int top = __reduce_max_sync(0xFFFFFFFFu, (int)(most << 16)) >> 16;
+                if (top > (int16_t)limit) {  // room for twice the scale
+                    const int E = min(max(top >> 10, 0) + 2, 31);
+                    less = __int_as_float((30 - E - (int)up + 127) << 23);
+                    up = (float)(30 - E), limit = 0x7FFF0000u | (uint32_t)(E < 31 ? (E << 10) - 1 : 0x7FFF);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -829,7 +865,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                         for (int sub = 0; sub < NB; ++sub) m = fmaxf(m, fmaxf(y[sub][nt][e], y[sub][nt][2 + e]));
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
-                        const float f = M[nt][e] == -CUDART_INF_F ? 0.f : exp2_fast((M[nt][e] - m) * col_scale(nt, e));
+                        const float f = M[nt][e] == -CUDART_INF_F ? 0.f : less * exp2_fast((M[nt][e] - m) * col_scale(nt, e));
                         M[nt][e] = m;
                         L[nt][e] *= f;
 #pragma unroll
@@ -847,7 +883,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                     for (int e = 0; e < 2; ++e) out |= M[nt][e] != -CUDART_INF_F && !(fabsf(M[nt][e] * col_scale(nt, e)) < kFar);
                 far = __any_sync(0xFFFFFFFFu, out);
             }
-            // weights 4 p
+            // weights 2^up p
             auto weights = [&](auto far_step) {
                 constexpr bool FAR = decltype(far_step)::value;
 #pragma unroll
@@ -855,7 +891,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const bool none = M[nt][e] == -CUDART_INF_F;
-                        const float f = col_scale(nt, e), base = none ? 0.f : M[nt][e], m = none ? 0.f : FAR ? 2.f : fmaf(-M[nt][e], f, 2.f);
+                        const float f = col_scale(nt, e), base = none ? 0.f : M[nt][e], m = none ? 0.f : FAR ? up : fmaf(-M[nt][e], f, up);
 #pragma unroll
                         for (int sub = 0; sub < NB; ++sub) {
                             y[sub][nt][e] = exp2_fast(fmaf(FAR ? y[sub][nt][e] - base : y[sub][nt][e], f, m));
@@ -945,7 +981,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         }
         cp_async_wait<0>();
 
-        // ---- the rows' sums complete, then the item or the worker's part of it ----
+        // ---- the rows' sums complete, of 4 p again, then the item or the worker's part of it ----
+        const float down = __int_as_float((2 - (int)up + 127) << 23);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -957,15 +994,18 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) r[nt][gr][e] += __shfl_xor_sync(0xFFFFFFFFu, r[nt][gr][e], w);
                 }
+                L[nt][e] *= down;
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) r[nt][gr][e] *= down;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const int gr = i * 16 / G;
                     if (RAW) {
-                        o[nt][i][e] = fmaf(o[nt][i][e] - z[gr][e], 0x1p24f, r[nt][gr][e]);
-                        o[nt][i][2 + e] = fmaf(o[nt][i][2 + e] - z[gr][2 + e], 0x1p20f, r[nt][gr][e]);
+                        o[nt][i][e] = fmaf(o[nt][i][e] - z[gr][e], 0x1p24f * down, r[nt][gr][e]);
+                        o[nt][i][2 + e] = fmaf(o[nt][i][2 + e] - z[gr][2 + e], 0x1p20f * down, r[nt][gr][e]);
                     } else {
-                        o[nt][i][e] += r[nt][gr][e];
-                        o[nt][i][2 + e] += r[nt][gr][e];
+                        o[nt][i][e] = fmaf(o[nt][i][e], down, r[nt][gr][e]);
+                        o[nt][i][2 + e] = fmaf(o[nt][i][2 + e], down, r[nt][gr][e]);
                     }
                 }
             }
