@@ -78,22 +78,27 @@ def _link(objs: list[str], out: str) -> None:
 
 
 def _fast() -> None:
-    """_fast.so; where it cannot be compiled (no headers of Python or PyTorch) the binding marshals every call in Python."""
+    """_fast.so; where it cannot be compiled (no PyTorch or no headers of it or of Python, no g++) the binding marshals every
+    call in Python."""
     src = os.path.join(CSRC, "fast_calls.cpp")
     if not _stale(FAST, [src, os.path.join(INCLUDE, "mbw.h")]):
         return
-    import sysconfig
+    try:
+        import sysconfig
 
-    import torch
+        import torch
 
-    at, inc = os.path.dirname(torch.__file__), sysconfig.get_path("include")
-    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", os.path.join(at, "include"), "-I", inc, "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
-           "-I", INCLUDE, src, "-o", FAST + ".tmp", "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
-           "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(f"_fast.so is not built, calls are marshalled in Python:\n{r.stderr[-2000:]}\n")
+        at, inc = os.path.dirname(torch.__file__), sysconfig.get_path("include")
+        cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-I", os.path.join(at, "include"), "-I", inc, "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+               "-I", INCLUDE, src, "-o", FAST + ".tmp", "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.stderr[-2000:] if r.returncode != 0 else None
+    except (ImportError, OSError) as e:
+        why = str(e)
+    if why is not None:
+        sys.stderr.write(f"_fast.so is not built, calls are marshalled in Python:\n{why}\n")
         if os.path.exists(FAST):
             os.remove(FAST)
         return
