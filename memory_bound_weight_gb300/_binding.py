@@ -475,7 +475,7 @@ def dequant_int4_awq_g128(Wq, scales, zeros):
 # The calls below are made many times per token, so their checks read each tensor once and compare devices by number; what
 # is wrong is told by the slower checks above.
 _dtypes = None
-_fast = None  # the compiled marshalling of these calls (csrc/fast_calls.cpp); False where it was not built
+_fast = None  # the compiled marshalling of these calls (csrc/fast_calls.cpp); False where it was not built or does not fit
 
 
 def _load_fast():
@@ -489,11 +489,21 @@ def _load_fast():
         return
     import importlib.machinery
     import importlib.util
+    import sys
+    import warnings
 
-    _torch()  # the libraries it is linked to
-    loader = importlib.machinery.ExtensionFileLoader("_fast", path)
-    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast", loader))
-    loader.exec_module(mod)
+    torch = _torch()  # the libraries it is linked to
+    _fast = False
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_fast", path)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast", loader))
+        loader.exec_module(mod)
+        here, its = f"{sys.implementation.cache_tag} torch {torch.__version__}", getattr(mod, "built_for", "another build")
+        if its != here:
+            raise ImportError(f"built for {its}, this is {here}")
+    except (ImportError, OSError) as e:
+        warnings.warn(f"{path} is not used, calls are marshalled in Python (build() makes it anew): {e}", RuntimeWarning)
+        return
     mod.init(*(ctypes.cast(f, ctypes.c_void_p).value
                for f in (L.mbw_kv4_append, L.mbw_kv4_gather, L.mbw_kv4_attention, L.mbw_token_logprobs)))
     _fast = mod

@@ -21,6 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmbw.so")
 GEN_LIB = os.path.join(PKG, "libmbw_inputs.so")
 FAST = os.path.join(PKG, "_fast.so")
+FAST_FOR = os.path.join(BUILD, "_fast.for")  # the Python and PyTorch that it was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -77,11 +78,28 @@ def _link(objs: list[str], out: str) -> None:
     os.replace(tmp, out)
 
 
+def _here() -> str:
+    """This Python and this installation of PyTorch, which need not be imported for it."""
+    import importlib.util
+
+    spec = importlib.util.find_spec("torch")
+    at = spec.origin if spec and spec.origin else None
+    return f"{sys.implementation.cache_tag} {at} {os.stat(at).st_mtime_ns if at else 0}"
+
+
+def _built_for() -> str:
+    try:
+        with open(FAST_FOR) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _fast() -> None:
     """_fast.so; where it cannot be compiled (no PyTorch or no headers of it or of Python, no g++) the binding marshals every
     call in Python."""
     src = os.path.join(CSRC, "fast_calls.cpp")
-    if not _stale(FAST, [src, os.path.join(INCLUDE, "mbw.h")]):
+    if not _stale(FAST, [src, os.path.join(INCLUDE, "mbw.h")]) and _built_for() == _here():
         return
     try:
         import sysconfig
@@ -90,6 +108,7 @@ def _fast() -> None:
 
         at, inc = os.path.dirname(torch.__file__), sysconfig.get_path("include")
         cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               f'-DMBW_BUILT_FOR="{sys.implementation.cache_tag} torch {torch.__version__}"',
                "-I", os.path.join(at, "include"), "-I", inc, "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
                "-I", INCLUDE, src, "-o", FAST + ".tmp", "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
                "-lc10_cuda"]
@@ -103,6 +122,8 @@ def _fast() -> None:
             os.remove(FAST)
         return
     os.replace(FAST + ".tmp", FAST)
+    with open(FAST_FOR, "w") as f:
+        f.write(_here())
 
 
 def build(ptxas_v: bool = False) -> str:
