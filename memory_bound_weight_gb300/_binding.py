@@ -557,7 +557,8 @@ def _vector(t, name, dtype, n):
 
 class Kv4Cache:
     """4-bit paged key/value cache over `pages`, a contiguous uint8 tensor (num_pages,
-    kv4_page_bytes(page_size, kv_heads, head_dim, group)) that the caller owns."""
+    kv4_page_bytes(page_size, kv_heads, head_dim, group)) that the caller owns. It stays as it was made, and so
+    must the tensor's memory; for other pages make another."""
 
     __slots__ = ("pages", "kv_heads", "head_dim", "page_size", "group", "_c", "_addr")
 
@@ -566,9 +567,21 @@ class Kv4Cache:
         num, got = _plain(pages, "pages", _types()[4], 2)
         if got != size:
             raise ValueError(f"pages must have {size} bytes per page, got {got}")
-        self.pages, self.kv_heads, self.head_dim, self.page_size, self.group = pages, kv_heads, head_dim, page_size, group
-        self._c = MbwKv4Cache(pages.data_ptr(), num, page_size, kv_heads, head_dim, group)
-        self._addr = ctypes.addressof(self._c)
+        c = MbwKv4Cache(pages.data_ptr(), num, page_size, kv_heads, head_dim, group)
+        for name, value in zip(self.__slots__, (pages, kv_heads, head_dim, page_size, group, c, ctypes.addressof(c))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a Kv4Cache stays as it was made; make another for other {name}")
+
+    def __delattr__(self, name):
+        raise AttributeError("a Kv4Cache stays as it was made")
+
+    def _check(self):
+        """The tensor still is what the cache was made over (its storage may have been changed or freed under it)."""
+        if self.pages.data_ptr() != (self._c.pages or 0) or self.pages.numel() != self._c.num_pages * kv4_page_bytes(
+                self.page_size, self.kv_heads, self.head_dim, self.group):
+            raise ValueError("the cache's pages were moved or resized after it was made; make another Kv4Cache")
 
 
 def kv4_page_bytes(page_size, kv_heads, head_dim, group=64):
@@ -614,6 +627,7 @@ def kv4_append(cache, k, v, slots, q=None, positions=None, cos_sin=None, interle
         r = _fast.kv4_append(cache._addr, cache.pages, k, v, slots, q, positions, cos_sin, interleaved, q_out)
         if r is not None:
             return r[0] if r.__class__ is tuple else check("mbw_kv4_append", r)
+    cache._check()
     bf16, f32, i32, i64, _, empty = _types()
     hk, d = cache.kv_heads, cache.head_dim
     T, _, ks = _need_rows(k, "k", hk, d)
@@ -661,6 +675,7 @@ def kv4_gather(cache, slots):
         r = _fast.kv4_gather(cache._addr, cache.pages, slots)
         if r is not None:
             return r if r.__class__ is tuple else check("mbw_kv4_gather", r)
+    cache._check()
     bf16, _, _, i64, _, empty = _types()
     T, = _plain(slots, "slots", i64, 1)
     dev = _check_devices(cache.pages, slots)
@@ -693,6 +708,7 @@ def kv4_attention(cache, q, block_table, ctx_lens, q_starts=None, scale=None, wi
                                 cache.head_dim ** -0.5 if scale is None else scale, window, return_lse, workspace)
         if r is not None:
             return check("mbw_kv4_attention", r) if r.__class__ is int else r
+    cache._check()
     bf16, f32, i32, _, _, empty = _types()
     d = cache.head_dim
     T, hq, qs = _need_rows(q, "q", None, d)

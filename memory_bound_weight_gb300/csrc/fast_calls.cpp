@@ -64,10 +64,11 @@ void* workspace(PyObject* o, int dev, size_t& bytes) {
     bytes = t.nbytes();
     return t.data_ptr();
 }
+// The cache's struct, if its tensor still lies where it lay when that was made.
 const mbw_kv4_cache* cache_of(PyObject* addr, PyObject* pages, int dev) {
-    tensor(pages, dev, at::kByte);
+    const at::Tensor* t = plain(pages, dev, at::kByte, 2);
     const mbw_kv4_cache* c = static_cast<const mbw_kv4_cache*>(PyLong_AsVoidPtr(addr));
-    if (!c) throw Unusual();
+    if (!c || t->data_ptr() != c->pages || t->size(0) != c->num_pages) throw Unusual();
     return c;
 }
 int64_t whole(PyObject* o) {
