@@ -79,6 +79,7 @@ class Decoder:
         self.cos_sin = mbw.rope_table(max_tokens, s.dim, s.rope_base)
         self.ctx = torch.zeros(requests, dtype=torch.int32, device=dev)  # tokens in the cache
         self.ids = torch.zeros(requests, dtype=torch.int64, device=dev)  # the next ones
+        self.longest = 0  # the largest of ctx, known on the host: a step past max_tokens would index past the tables
         self.attn_ws = mbw.kv4_attention_workspace(s.dim)
         self.prob_ws = mbw.token_logprobs_workspace()
 
@@ -113,6 +114,14 @@ class Decoder:
         """Fills the caches with the prompts (one list of ids per request) and returns their last logits' TokenLogprobs."""
         dev = self.ids.device
         n = [len(p) for p in prompts]
+        if len(n) != self.requests:
+            raise ValueError(f"{self.requests} prompts are needed, got {len(n)}")
+        if min(n) < 1:
+            raise ValueError("a prompt is empty")
+        if max(n) > self.max_tokens:
+            raise ValueError(f"a prompt of {max(n)} tokens is longer than max_tokens, {self.max_tokens}")
+        if any(not 0 <= t < self.shape.vocab for p in prompts for t in p):
+            raise ValueError(f"a prompt has an id outside 0 to {self.shape.vocab - 1}")
         starts = [0]
         for x in n:
             starts.append(starts[-1] + x)
@@ -120,12 +129,20 @@ class Decoder:
         request = torch.repeat_interleave(torch.arange(len(n), device=dev), torch.tensor(n, device=dev))
         positions = torch.cat([torch.arange(x, device=dev) for x in n])
         self.ctx.copy_(torch.tensor(n, dtype=torch.int32))
+        self.longest = max(n)
         logits = self.forward(ids, request, positions, torch.tensor(starts, dtype=torch.int32, device=dev),
                               torch.tensor(starts[1:], device=dev) - 1)
         return self.choose(logits)
 
+    def advance(self):
+        """Counts a token more on the host, or raises where the longest request has no place for it."""
+        if self.longest >= self.max_tokens:
+            raise ValueError(f"a request has max_tokens, {self.max_tokens}, already")
+        self.longest += 1
+
     def step(self, top_k=1):
         """One token of every request: self.ids go in at their places, and the most likely next ones take theirs."""
+        self.advance()
         positions = self.ctx.long()
         self.ctx += 1
         return self.choose(self.forward(self.ids, torch.arange(self.requests, device=positions.device), positions, None,
@@ -136,21 +153,32 @@ class Decoder:
         self.ids.copy_(r.top_ids[:, 0])
         return r
 
+    def counted(self, replay):
+        def counted_replay():
+            self.advance()
+            replay()
+
+        return counted_replay
+
     def graph(self, top_k=1):
-        """step() as a CUDA graph: (replay, its TokenLogprobs, overwritten by each replay)."""
-        keep = self.ctx.clone(), self.ids.clone()
+        """step() as a CUDA graph: (replay, its TokenLogprobs, overwritten by each replay). One place has to be left."""
+        keep, longest = (self.ctx.clone(), self.ids.clone()), self.longest
+        self.advance()  # refused before anything runs
+        self.longest = longest
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
             self.step(top_k)  # plans and allocations happen here
             side.synchronize()
+            self.longest = longest
             g = torch.cuda.CUDAGraph()
             with torch.cuda.graph(g, stream=side):
                 out = self.step(top_k)
         torch.cuda.current_stream().wait_stream(side)
         self.ctx.copy_(keep[0])
         self.ids.copy_(keep[1])
-        return g.replay, out
+        self.longest = longest
+        return self.counted(g.replay), out
 
 
 def main():
