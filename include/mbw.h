@@ -465,8 +465,9 @@ mbw_status mbw_plan_describe(int op, int64_t M, int64_t N, int64_t K, char *buf,
 
 /* Read and clear the device-side error flags set by bounded waits inside
  * kernels and by values out of range that the cache and token kernels met
- * (synchronizes the current device). MBW_OK, MBW_ERR_DEVICE_TIMEOUT or
- * MBW_ERR_DEVICE_RANGE. */
+ * (synchronizes the current device). MBW_OK, MBW_ERR_DEVICE_TIMEOUT (an
+ * expired wait, whatever else) or MBW_ERR_DEVICE_RANGE; mbw_last_error() names
+ * all that was flagged. */
 mbw_status mbw_check_device_error(void);
 
 /* Self-test of the failure path above. Launches two one-thread kernels on

@@ -603,11 +603,17 @@ mbw_status mbw_check_device_error(void) {
     const int r4 = kv4_attn_tc_take(false);
     if (f < 0 || f2 < 0 || f3 < 0 || r < 0 || r2 < 0 || r3 < 0 || r4 < 0)
         return cuda_fail(cudaGetLastError(), "reading the device fault flag");
-    if (f || f2 || f3) return fail(MBW_ERR_DEVICE_TIMEOUT, "a bounded wait inside a kernel expired");
-    if (r) return fail(MBW_ERR_DEVICE_RANGE, "a cache slot or position was out of range");
-    if (r2 || r4) return fail(MBW_ERR_DEVICE_RANGE, "a page id, context length or query offset was out of range");
-    if (r3) return fail(MBW_ERR_DEVICE_RANGE, "a target token id was out of range");
-    return MBW_OK;
+    // Every flag is cleared, so every one is named; the status is that of the gravest.
+    std::string what;
+    auto name = [&](bool set, const char* text) {
+        if (set) what += (what.empty() ? "" : "; ") + std::string(text);
+    };
+    name(f || f2 || f3, "a bounded wait inside a kernel expired");
+    name(r, "a cache slot or position was out of range");
+    name(r2 || r4, "a page id, context length or query offset was out of range");
+    name(r3, "a target token id was out of range");
+    if (what.empty()) return MBW_OK;
+    return fail(f || f2 || f3 ? MBW_ERR_DEVICE_TIMEOUT : MBW_ERR_DEVICE_RANGE, what);
 }
 
 mbw_status mbw_selftest_wait_expiry(int64_t tries, mbw_stream_t stream) {
