@@ -7,7 +7,7 @@ The compute path is libmbw.so (C ABI in include/mbw.h); this package is its
 binding. Submodules ``inputs`` and ``workloads`` (synthetic data and byte
 accounting) import without loading the CUDA library.
 """
-_EXPORTS = (
+_EXPORTS = frozenset((
     "gemv_bf16", "gemv_int4_g64", "gemv_int4_awq_g128", "gemm_skinny_bf16", "gemv_int8_pc", "quantize_int8_pc",
     "gemv_fused", "gemv_fused_awq_g128", "MbwFusion", "FUSE_NORM", "FUSE_GLU", "FUSE_RESIDUAL", "repack_int4", "REPACKED",
     "dequant_int4_g64", "dequant_int4_awq_g128", "autotune", "plan_describe", "plan_candidates", "plan_select", "plan_index", "workspace_bytes",
@@ -16,7 +16,7 @@ _EXPORTS = (
     "OP_GEMV_INT8_PC",
     "Kv4Cache", "kv4_page_bytes", "kv4_append", "kv4_gather", "kv4_attention", "kv4_attention_workspace",
     "token_logprobs", "token_logprobs_workspace", "TokenLogprobs",
-)
+))
 
 
 _PLAN_FILES = ("save_plans", "load_plans")
@@ -24,10 +24,11 @@ _PLAN_FILES = ("save_plans", "load_plans")
 
 def __getattr__(name):
     if name in _EXPORTS:
-        from . import _binding
+        binding = globals().get("_binding")
+        if binding is None:
+            from . import _binding as binding
 
-        value = globals()[name] = getattr(_binding, name)  # the next access finds it here
-        return value
+        return getattr(binding, name)  # each time: what is replaced there is seen here
     if name == "rope_table":
         from .rope import rope_table
 
