@@ -166,6 +166,7 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double scale = number(a[6]);
         const int64_t window = whole(a[7]);
         const int want_lse = PyObject_IsTrue(a[8]);
+        if (want_lse < 0) throw Unusual();
         size_t bytes;
         void* ws = workspace(a[9], dev, bytes);
         const at::Tensor out = empty({q.n, q.heads, c->head_dim}, *q.t, at::kBFloat16);
