@@ -323,11 +323,12 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
         return v == -CUDART_INF_F ? v : v == 0.f ? -1.4012985e-45f : __int_as_float(b > 0 ? b - 1 : b + 1);
     };
 
-    auto settle = [&]() {  // the sums as if y had been exact
-        const float f = exp2_fast(lag);
-        t2 = make_float2(f * fmaf(lag, s2.x, t2.x), f * fmaf(lag, s2.y, t2.y));
+    auto moved = [&](float by) {  // the sums as if every y had been so much larger
+        const float f = exp2_fast(by);
+        t2 = make_float2(f * fmaf(by, s2.x, t2.x), f * fmaf(by, s2.y, t2.y));
         s2 = make_float2(f * s2.x, f * s2.y);
     };
+    auto settle = [&]() { moved(lag); };  // as if y had been exact
     auto sum_fast = [&](const float* e) {
         const float2 sh = make_float2(shift, shift), cc = make_float2(c2, c2);
 #pragma unroll
@@ -387,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobArgs
             s2 = make_float2(f * s2.x, f * s2.y);
             st.own = first_at;
             refer(wm);
+            if (!plain) moved(-lag);  // as the terms to come are
             excluded = own;
         }
         gate = st.ref;

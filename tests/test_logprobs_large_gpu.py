@@ -49,3 +49,17 @@ def test_logits_near_a_large_number(V, big):
     for ws in (None, mbw.token_logprobs_workspace()):
         compare(x, t, 20, 1.0, ws)
         compare(x.bfloat16(), t, 20, 1.0, ws)
+
+
+@pytest.mark.parametrize("V", [3, 2000, 40000, 152064])
+@pytest.mark.parametrize("far", [1e2, 1e3, -1e4, 1e5, -1e6, 1e7, -5e7, 3e8])
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+def test_logits_spread_around_a_far_number(V, far, scale):
+    """The reference moves many times on the way: rising rows, and rows in no order."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V + 1)
+    x = torch.randn(24, V, generator=g, device="cuda") * 3 + far
+    x[:8] = x[:8].sort(-1).values
+    t = torch.randint(V, (24,), generator=g, device="cuda").int()
+    for ws in (None, mbw.token_logprobs_workspace()):
+        compare(x, t, 5, scale, ws)
