@@ -568,8 +568,9 @@ class Kv4Cache:
         if got != size:
             raise ValueError(f"pages must have {size} bytes per page, got {got}")
         c = MbwKv4Cache(pages.data_ptr(), num, page_size, kv_heads, head_dim, group)
-        for name, value in zip(self.__slots__, (pages, kv_heads, head_dim, page_size, group, c, ctypes.addressof(c))):
-            object.__setattr__(self, name, value)
+        put = _kv4_cache_put
+        put[0](self, pages), put[1](self, kv_heads), put[2](self, head_dim), put[3](self, page_size), put[4](self, group)
+        put[5](self, c), put[6](self, ctypes.addressof(c))
 
     def __setattr__(self, name, value):
         raise AttributeError(f"a Kv4Cache stays as it was made; make another for other {name}")
@@ -582,6 +583,9 @@ class Kv4Cache:
         if self.pages.data_ptr() != (self._c.pages or 0) or self.pages.numel() != self._c.num_pages * kv4_page_bytes(
                 self.page_size, self.kv_heads, self.head_dim, self.group):
             raise ValueError("the cache's pages were moved or resized after it was made; make another Kv4Cache")
+
+
+_kv4_cache_put = tuple(getattr(Kv4Cache, name).__set__ for name in Kv4Cache.__slots__)  # past its __setattr__
 
 
 def kv4_page_bytes(page_size, kv_heads, head_dim, group=64):
