@@ -24,11 +24,10 @@ _PLAN_FILES = ("save_plans", "load_plans")
 
 def __getattr__(name):
     if name in _EXPORTS:
-        binding = globals().get("_binding")
-        if binding is None:
-            from . import _binding as binding
+        from . import _binding
 
-        return getattr(binding, name)  # each time: what is replaced there is seen here
+        value = globals()[name] = getattr(_binding, name)  # found here from now on; the binding keeps it its own (_Module)
+        return value
     if name == "rope_table":
         from .rope import rope_table
 
