@@ -24,14 +24,15 @@
 // group:
 //   sum p (s n + m) = [sum w n - 8 sum w] / 2^u + sum p (m + 8 s)
 // with the same rounded w in both sums, so that its rounding (2^-11) acts on
-// the centred code n - 8 only; 8 sum w comes from a constant tile. p <= 1
-// against the running maximum, and u follows the largest scale so far: 2^u s is
-// below 2^15, and was between 2^13 and 2^14 when that scale came, so that a weight
-// keeps its 11 bits down to p = 2^-26 and is lost only below 2^-37, whatever the
-// size of the values. (With 4 p s the weights of many small p beside a large one
-// were lost where values are small: at 1e-4 the sum of 2000 of them, half the
-// result.) Each lane looks at the scales of its share of a step's tokens, which takes
-// 2.5% of the time at 64 requests. Scores, maxima, sums and outputs are fp32.
+// the centred code n - 8 only; 8 sum w comes from a constant tile. p refers to a
+// maximum that follows the true one only when it has grown by 2^3, so that what was
+// summed seldom has to be taken to another, and u follows the largest scale so far:
+// 2^u s is below 2^12, and was between 2^10 and 2^11 when that scale came. So w < 2^15,
+// and a weight keeps its 11 bits down to p = 2^-24 and is lost only below 2^-35,
+// whatever the size of the values. (With 4 p s the many small weights beside a large
+// one were lost where values are small: at 1e-4 the sum of 2000 of them, half the
+// result.) Each lane looks at the scales of its share of a step's tokens. Scores,
+// maxima, sums and outputs are fp32.
 //
 // Unpacking is thus one AND per pair and a shift for every other pair. It runs
 // on the ALU pipe at half rate, which bounded the forms before: with a shift
@@ -78,6 +79,8 @@ __device__ int g_kv4_attn_range;  // a page id, length or query offset was out o
 // maxima of this size on (in powers of two) that rounding, 2^-10 of a power here and as many as a float holds further out,
 // would show, and the difference of the scores is taken first.
 constexpr float kFar = 16384.f;
+// Growth of a maximum, in powers of two, that is let pass before what was summed is taken to it.
+constexpr int kSlack = 3;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
@@ -731,6 +734,10 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         // weights are 2^up p; in the lower half of limit the largest scale that this has room for, as fp16 bits
         float up = 2.f;
         uint32_t limit = 0x7FFF8000u;
+        // of each column, what a score's power of two is off its weight's, and the score from which on its reference moves
+        float shift[NT][2], above[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) shift[nt][0] = shift[nt][1] = 0.f, above[nt][0] = above[nt][1] = -CUDART_INF_F;
         for (int k = 0; k < nsteps; ++k) {
             cp_async_wait<DEPTH - 2>();
             __syncwarp();  // the step's copies of every lane are there, and step k - 1 is read
@@ -847,14 +854,14 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) raise |= y[sub][nt][e] > M[nt][e & 1];
+                    for (int e = 0; e < 4; ++e) raise |= y[sub][nt][e] > above[nt][e & 1];
             if (__any_sync(0xFFFFFFFFu, raise)) {
                 float less = 1.f;  // of 2^up
                 const int top = __reduce_max_sync(0xFFFFFFFFu, (int)(most << 16)) >> 16;
                 if (top > (int16_t)limit) {  // room for twice the scale
                     const int E = min(max(top >> 10, 0) + 2, 31);
-                    less = __int_as_float((30 - E - (int)up + 127) << 23);
-                    up = (float)(30 - E), limit = 0x7FFF0000u | (uint32_t)(E < 31 ? (E << 10) - 1 : 0x7FFF);
+                    less = __int_as_float((30 - kSlack - E - (int)up + 127) << 23);
+                    up = (float)(30 - kSlack - E), limit = 0x7FFF0000u | (uint32_t)(E < 31 ? (E << 10) - 1 : 0x7FFF);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -882,28 +889,39 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
                     for (int e = 0; e < 2; ++e) out |= M[nt][e] != -CUDART_INF_F && !(fabsf(M[nt][e] * col_scale(nt, e)) < kFar);
                 far = __any_sync(0xFFFFFFFFu, out);
-            }
-            // weights 2^up p
-            auto weights = [&](auto far_step) {
-                constexpr bool FAR = decltype(far_step)::value;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        const float f = col_scale(nt, e);
                         const bool none = M[nt][e] == -CUDART_INF_F;
-                        const float f = col_scale(nt, e), base = none ? 0.f : M[nt][e], m = none ? 0.f : FAR ? up : fmaf(-M[nt][e], f, up);
-#pragma unroll
-                        for (int sub = 0; sub < NB; ++sub) {
-                            y[sub][nt][e] = exp2_fast(fmaf(FAR ? y[sub][nt][e] - base : y[sub][nt][e], f, m));
-                            y[sub][nt][2 + e] = exp2_fast(fmaf(FAR ? y[sub][nt][2 + e] - base : y[sub][nt][2 + e], f, m));
-                            L[nt][e] += y[sub][nt][e] + y[sub][nt][2 + e];
-                        }
+                        shift[nt][e] = none ? 0.f : far ? up : fmaf(-M[nt][e], f, up);
+                        above[nt][e] = none ? -CUDART_INF_F : M[nt][e] + __fdividef((float)kSlack, f);
                     }
-            };
-            if (far)
-                weights(std::true_type());
-            else
-                weights(std::false_type());
+            }
+            if (far) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float base = M[nt][e] == -CUDART_INF_F ? 0.f : M[nt][e];
+#pragma unroll
+                        for (int sub = 0; sub < NB; ++sub) y[sub][nt][e] -= base, y[sub][nt][2 + e] -= base;
+                    }
+            }
+            // weights 2^up p
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float f = col_scale(nt, e);
+#pragma unroll
+                    for (int sub = 0; sub < NB; ++sub) {
+                        y[sub][nt][e] = exp2_fast(fmaf(y[sub][nt][e], f, shift[nt][e]));
+                        y[sub][nt][2 + e] = exp2_fast(fmaf(y[sub][nt][2 + e], f, shift[nt][e]));
+                        L[nt][e] += y[sub][nt][e] + y[sub][nt][2 + e];
+                    }
+                }
             auto values = [&](auto edge_step) {
                 constexpr bool EDGE = decltype(edge_step)::value;
 #pragma unroll
