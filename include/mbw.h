@@ -374,9 +374,13 @@ mbw_status mbw_kv4_gather(const mbw_kv4_cache *cache, const int64_t *slots, void
  * to its own. A query that sees no key gets zeros (lse: minus infinity). Keys
  * and values at places a query does not see, or past a request's length, do
  * not enter, whatever they hold.
- * Products and sums are fp32; a softmax weight is rounded to fp16, and for
- * chunks of a prompt (96 query rows per KV head and more) also s (code - 8), to
- * 2^-8 of a step s. Results do not depend on the order in which CTAs run.
+ * Products and sums are fp32; a softmax weight is rounded to fp16 (11 bits, of
+ * values of any size). Where head_dim is 64 or 128 and a request of the call has
+ * on average 96 query rows per KV head or more, in 16 tiles of 128 or more, the
+ * whole call runs on another kernel, which also rounds s (code - 8) to fp16, 2^-8
+ * of a step s, and sums lse over the rounded weights (within 5e-4 instead of
+ * 1e-5). The last bits of a request's result so depend on what else is in the
+ * call, but not on the order in which CTAs run.
  * workspace: mbw_kv4_attention_workspace_bytes() bytes, zero before its first
  * use; every call leaves it ready for the next (one workspace per stream).
  * Smaller or NULL:

@@ -52,12 +52,12 @@
 // 300 to 16000 tokens took 82 us, and with blocks handed out by a counter 95 to 103.)
 //   Few items, each cut many times: a CTA of 16 warps is one, and its warps are
 // joined in shared memory, so that fewer parts go through the workspace (1 request
-// of 65536 tokens: 21 us, of 4 heads and a part per SM; 87 with warps as workers).
+// of 65536 tokens: 21 us, of 4 heads and a part per SM; 145 with warps as workers).
 //
-// What bounds it: 64 requests of 300 to 16000 tokens, 308 MB, take 66 us, 4.7 TB/s;
-// the time of a further token is that of 6.0 TB/s, 88% of what a copy reaches, and 14
+// What bounds it: 64 requests of 300 to 16000 tokens, 308 MB, take 66 us, 4.6 TB/s;
+// the time of a further token is that of 6.0 TB/s, 88% of what a copy reaches, and 13
 // us are the start (lengths, block table and first block one behind the other), ends
-// that are not even, and the join of parts. One request of 1024 tokens takes 10.6 us,
+// that are not even, and the join of parts. One request of 1024 tokens takes 11.0 us,
 // all of it such latencies.
 #include <cuda_runtime.h>
 
@@ -1097,10 +1097,10 @@ Entry entry() {
 // Query rows per KV head of an average request from which on they are many: tiles of 128 rows on tcgen05 where there are
 // enough such tiles (kv4_attention_tc.cu) and the head has at most 128 dimensions, else tiles of 16 here, which unpack K
 // and V half as often as tiles of 8, with more empty rows and fewer warps to an SM. Measured, tiles of 16 or 8 against 128
-// rows: 16 requests of 32 queries x 4 heads and 4000 tokens 191 us, 49 us; 16 of 16 x 7 heads and 4000 tokens 92, 39; 4
+// rows: 16 requests of 32 queries x 4 heads and 4000 tokens 188 us, 50 us; 16 of 16 x 7 heads and 4000 tokens 92, 38; 4
 // tiles of 112 rows, 16 of them of 128, 32 of 128: a geometric mean over contexts of 300 to 16000 tokens of 0.64, 1.35 and
 // 1.60 of the time here, the join of what many CTAs share included. Below 96 rows the two are closer than 1.2 but where
-// there are as many items as SMs. (12 requests of 2 to 5 queries x 7 heads: tiles of 16 take 32.5 us, of 8 27.5.)
+// there are as many items as SMs. (12 requests of 2 to 5 queries x 7 heads: tiles of 16 take 37 us, of 8 27.)
 constexpr int kWideRows = 96, kTensorItems = 16;
 
 // rows: query rows per KV head of an average request; few: few items, each cut over several SMs.
@@ -1183,7 +1183,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     const int64_t items = a.kv_heads * with * ((rows + tile - 1) / tile);
     const int64_t most_items = a.kv_heads * (with + ((int64_t)a.T * gq + tile - 1) / tile);
     // CTAs as workers cut whole items among them, so there have to be more CTAs than items by enough (12 requests of 8
-    // KV heads and 32768 tokens, 96 items: 119 us against 91 with warps; 64 items: 67 against 69; 8: 19 against 87).
+    // KV heads and 32768 tokens, 96 items: 123 us against 92 with warps; 64 items: 68 against 69; 8: 19.5 against 84).
     const bool few = 2 * items <= sms && most_items <= kItemsPerCta * sms;
     const Entry e = pick_for(a.head_dim, a.group, (int)(rows < kWideRows ? rows : kWideRows), few);
     if (e.smem > 48 * 1024) {

@@ -45,7 +45,7 @@
 // maximum taken in the pass of the weights, the first item found by one warp, halves
 // of Q read by halves of the softmax, and joins at the roles' ends (33 with a join
 // behind each piece, whose registers the loops paid for): 500 TFLOP/s. 16 requests of
-// 32 queries of 32 heads and 4000 tokens take 49 us, 660 TFLOP/s.
+// 32 queries of 32 heads and 4000 tokens take 50 us, 665 TFLOP/s.
 //
 // Tokens that some rows do not see may hold no numbers, or bytes that no append
 // wrote, whose products pass fp16; and 0 times NaN is not 0: V's groups of either

@@ -19,9 +19,10 @@
 // attention kernels' operands rely on.
 //
 // What bounds it: for one token or some dozens the launch and its three dependent
-// loads (2.5 us each of append and gather, in a graph); for many the instructions,
-// some 2800 for a token of 28 + 8 rows: 8192 of them, 147 MB, take 30 us, 4.9 TB/s,
-// and 10 us to read back.
+// loads (2.4 and 1.8 us of append and gather, in a graph); for many, instructions at
+// an occupancy that does not hide all of their latency: some 2400 for a token of 28 +
+// 8 rows, issue slots 61% busy by 38% of the warps. 8192 tokens, 147 MB, take 32 us,
+// 4.6 TB/s, and 8 us to read back.
 #include <cuda_runtime.h>
 
 #include <math_constants.h>
@@ -344,7 +345,7 @@ cudaError_t launch_pdl(F* fn, dim3 grid, int threads, cudaStream_t s, const A& a
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
     // Few tokens: a CTA of 4 warps takes the rows it holds at a time, so that a token is done soonest. Many: one warp
     // takes a whole token, and what is done once per token and thread is done for all its rows (8192 tokens of 28 + 8
-    // rows: 1030 instructions a warp and 4 warps a token become some 2800).
+    // rows: 1030 instructions a warp and 4 warps a token become some 2400).
     const int total = a.q_heads + 2 * a.kv_heads;
     const int tokens = a.T >= (int64_t)device_sm_count() * 16 ? kAppendThreads / 32 : 1;
     const int slots = kAppendThreads / (a.head_dim / 8);

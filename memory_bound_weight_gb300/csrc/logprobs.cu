@@ -23,8 +23,8 @@
 // the first loads; the lists' K-th entries raise it. At the end the better ones of
 // each candidate are counted. Pieces of a row meet in the workspace; the CTA that
 // arrives last joins them in their order, and of their lists only what can still be
-// among the K best. (The 20 best of 1 row: 10.7 us, 6.9 without any; of 50 rows of
-// 4-byte logits 20.8 and 11.3; 32 with a list per warp and a gate that was the least
+// among the K best. (The 20 best of 1 row: 10.6 us, 6.6 without any; of 50 rows of
+// 4-byte logits 20.5 and 11.0; 32 with a list per warp and a gate that was the least
 // of the warps'.)
 #include <cuda_runtime.h>
 
