@@ -164,11 +164,15 @@ def _e4m3(x, scale):
     return torch.where(scale > 0, x / scale, torch.zeros_like(x)).to(torch.float8_e4m3fn)
 
 
+def _scale(high):  # by a tensor: torch multiplies by the reciprocal of a number
+    return high / torch.full_like(high, 448.0)
+
+
 def _by_rows(x):
     """Codes and scales of bf16 or fp32 rows, a scale per 128 columns."""
     m, k = x.shape
     y = x.float().view(m, k // 128, 128)
-    scale = y.abs().amax(-1) / 448.0
+    scale = _scale(y.abs().amax(-1))
     return _e4m3(y, scale[..., None]).view(m, k), scale
 
 
@@ -181,7 +185,7 @@ def _by_blocks(w):
         y = w[i:i + 1024].float()
         rows = y.shape[0]
         y = torch.nn.functional.pad(y, (0, 0, 0, -rows % 128)).view(-1, 128, k // 128, 128)
-        s = y.abs().amax((1, 3)) / 448.0
+        s = _scale(y.abs().amax((1, 3)))
         scales[i // 128:i // 128 + s.shape[0]] = s
         codes[i:i + 1024] = _e4m3(y, s[:, None, :, None]).view(-1, k)[:rows]
     return codes, scales
@@ -420,7 +424,7 @@ def _exact_quantize(c, s):
     high = torch.stack([p.float().abs().amax(1) for p in x.split(128, 1)], 1)
     if c["what"] == "weights":
         high = torch.stack([p.amax(0) for p in high.split(128, 0)])
-    scale = high / 448.0
+    scale = (high.double() / 448.0).float()  # 53 bits and then 24: the quotient of fp32 numbers, correctly rounded
     full = scale if c["what"] == "tokens" else scale.repeat_interleave(128, 0)[:c["m"]]
     out = torch.empty(c["m"], c["k"], dtype=torch.float64, device="cuda")
     for i in range(c["k"] // 128):
