@@ -220,6 +220,35 @@ mbw_status mbw_quantize_int8_pc(const void *W, int8_t *Wq, float *scales, int64_
                                 mbw_stream_t stream);
 
 /*
+ * 8-bit floating point with a scale for each block of 128: a value is an e4m3
+ * code (4 exponent bits, 3 mantissa bits, largest 448) times an fp32 scale, of
+ * activations one scale per row and 128 columns, of weights one per 128 x 128
+ * (the last rows of a matrix may be fewer). Per block, s = max|x| / 448 and
+ * code = e4m3(x / s), both divisions IEEE fp32, the code rounded to nearest,
+ * ties to even; a block of zeros has s = 0 and codes 0; a block that holds a
+ * NaN or an infinity reads as NaN. All K are positive multiples of 128.
+ *
+ * mbw_quantize_fp8_g128 -- activations, with norm_weight of the RMS-normed row
+ * bf16(x * r * norm_weight), r = fp32(1 / sqrt(mean(x^2) + norm_eps)): the sum
+ * is kept in two floats, so that the codes do not hang on its order.
+ *   X        : bf16 [M][K], rows x_stride elements apart (a multiple of 8)
+ *   Xq       : uint8 [M][K]     x_scales : fp32 [M][K/128]
+ *   norm_weight : bf16 [K] or NULL      X, Xq, norm_weight 16-byte aligned.
+ * mbw_quantize_fp8_b128 -- weights, the load-time step.
+ *   W : bf16 [N][K]     Wq : uint8 [N][K]     w_scales : fp32 [ceil(N/128)][K/128]
+ *   W and Wq 16-byte aligned.
+ * mbw_dequant_fp8_g128 / _b128 -- out[i][k] = scale * code, fp32.
+ */
+mbw_status mbw_quantize_fp8_g128(const void *X, int64_t x_stride, uint8_t *Xq, float *x_scales, int64_t M, int64_t K,
+                                 const void *norm_weight, double norm_eps, mbw_stream_t stream);
+mbw_status mbw_quantize_fp8_b128(const void *W, uint8_t *Wq, float *w_scales, int64_t N, int64_t K,
+                                 mbw_stream_t stream);
+mbw_status mbw_dequant_fp8_g128(const uint8_t *Xq, const float *x_scales, float *out, int64_t M, int64_t K,
+                                mbw_stream_t stream);
+mbw_status mbw_dequant_fp8_b128(const uint8_t *Wq, const float *w_scales, float *out, int64_t N, int64_t K,
+                                mbw_stream_t stream);
+
+/*
  * Optional fusions around one GEMV (all fields zero / NULL = none).
  *   norm_weight : bf16 [K] or NULL. RMSNorm prologue (llm-rs vs vLLM, "Decode:
  *                 from ~35% to ~70% of the ceiling": norms folded into the
@@ -285,6 +314,27 @@ mbw_status gemv_fused(int op, const void *W, const void *scales, const void *X, 
 mbw_status gemv_fused_awq_g128(const uint8_t *Wq, const void *scales, const uint8_t *zeros, const void *X, void *Y,
                                int64_t M, int64_t N, int64_t K, int repacked, const mbw_fusion *fusion,
                                void *workspace, size_t ws_bytes, mbw_stream_t stream);
+
+/*
+ * gemm_fp8_b128 -- Y = X . W^T of operands in 8-bit floating point with a scale
+ * for each block of 128 (above), any number of rows, one token or a prompt:
+ *   y[m][n] = sum_b x_scales[m][b] w_scales[n/128][b] sum_{k in b} Xq[m][k] Wq[n][k]
+ * Sums and factors are fp32 (a product of two scales below 2^-126 loses digits).
+ *   Xq : uint8 [M][K]     x_scales : fp32 [M][K/128]
+ *   Wq : uint8 [N][K]     w_scales : fp32 [ceil(N/128)][K/128]
+ *   Y  : bf16 [M][N] (fp32 under the fp32 hook)
+ * fusion (NULL: none): residual (may be Y), and with up_weights and up_scales,
+ * a second matrix of the same layout, the gated form silu(X.W^T) * (X.U^T) of a
+ * feed-forward block in one kernel; norm_weight and up_zeros must be NULL.
+ * Wq and up_weights 32-byte aligned, Xq, Y and workspace 16-byte.
+ * workspace: mbw_gemm_fp8_b128_workspace_bytes() bytes, zero before its first
+ * use and left so by every call (one per stream). Smaller or NULL: few rows run
+ * on fewer CTAs and take longer, and their sums are taken in another order.
+ */
+mbw_status gemm_fp8_b128(const uint8_t *Xq, const float *x_scales, const uint8_t *Wq, const float *w_scales, void *Y,
+                         int64_t M, int64_t N, int64_t K, const mbw_fusion *fusion, void *workspace, size_t ws_bytes,
+                         mbw_stream_t stream);
+size_t mbw_gemm_fp8_b128_workspace_bytes(void);
 
 /*
  * 4-bit paged key/value cache: what stands between the QKV product and the
@@ -398,6 +448,24 @@ mbw_status mbw_kv4_attention(const mbw_kv4_cache *cache, const void *q, int64_t 
 size_t mbw_kv4_attention_workspace_bytes(int32_t head_dim);
 
 /*
+ * mbw_kv4_attention_shared -- mbw_kv4_attention for requests that begin with the
+ * same shared_len tokens, in the same pages: the first shared_len / page_size
+ * entries of the requests' block table rows are equal as far as each request's
+ * length goes (what is left of shared_len lies in each request's own pages).
+ * The result is that of mbw_kv4_attention up to the order of sums; the shared
+ * pages are read and multiplied once for all requests, by the row of the longest.
+ * workspace: mbw_kv4_attention_shared_workspace_bytes(head_dim, T, q_heads)
+ * bytes, otherwise as mbw_kv4_attention's. Smaller or NULL: shared pages are
+ * read for each request.
+ */
+mbw_status mbw_kv4_attention_shared(const mbw_kv4_cache *cache, const void *q, int64_t q_stride, void *out,
+                                    int64_t out_stride, float *lse, const int32_t *block_table, int64_t table_stride,
+                                    int64_t table_width, const int32_t *ctx_lens, const int32_t *q_starts, int64_t B,
+                                    int64_t T, int64_t q_heads, float scale, int64_t window, int64_t shared_len,
+                                    void *workspace, size_t ws_bytes, mbw_stream_t stream);
+size_t mbw_kv4_attention_shared_workspace_bytes(int32_t head_dim, int64_t T, int64_t q_heads);
+
+/*
  * mbw_token_logprobs -- what a row of logits says about tokens, in one read of
  * the logits (behind the LM head product). Over y = scale * logits:
  *   logits       : bf16 (fp32 when `fp32` is 1), rows of V, row_stride elements
@@ -486,7 +554,7 @@ mbw_status mbw_selftest_wait_expiry(int64_t tries, mbw_stream_t stream);
 
 /* Host-side fault injection (test hook). The next `count` calls on the
  * calling thread that pass their argument checks and would launch a kernel
- * (the GEMV/GEMM entry points, mbw_repack_int4, mbw_quantize_int8_pc, the
+ * (the GEMV/GEMM entry points, mbw_repack_int4, the mbw_quantize_* calls, the
  * dequant helpers, the mbw_kv4_* calls and mbw_token_logprobs) launch nothing and return MBW_ERR_CUDA, as a failed launch
  * would, with mbw_last_error() naming the injection. count = 0 (the default)
  * turns it off; a negative count is MBW_ERR_INVALID_ARG. */

@@ -69,12 +69,21 @@ SIGNATURES = {
     "gemv_fused": ([ctypes.c_int, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.POINTER(MbwFusion), _P, _SZ, _P], _ST),
     "gemv_fused_awq_g128": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.POINTER(MbwFusion), _P, _SZ,
                              _P], _ST),
+    "mbw_quantize_fp8_g128": ([_P, _I64, _P, _P, _I64, _I64, _P, ctypes.c_double, _P], _ST),
+    "mbw_quantize_fp8_b128": ([_P, _P, _P, _I64, _I64, _P], _ST),
+    "mbw_dequant_fp8_g128": ([_P, _P, _P, _I64, _I64, _P], _ST),
+    "mbw_dequant_fp8_b128": ([_P, _P, _P, _I64, _I64, _P], _ST),
+    "gemm_fp8_b128": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.POINTER(MbwFusion), _P, _SZ, _P], _ST),
+    "mbw_gemm_fp8_b128_workspace_bytes": ([], _SZ),
     "mbw_kv4_page_bytes": ([_I32, _I32, _I32, _I32], _SZ),
     "mbw_kv4_append": ([_P, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _I64, _P], _ST),
     "mbw_kv4_gather": ([_P, _P, _P, _P, _I64, _P], _ST),
     "mbw_kv4_attention": ([_P, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, ctypes.c_float, _I64,
                            _P, _SZ, _P], _ST),
     "mbw_kv4_attention_workspace_bytes": ([_I32], _SZ),
+    "mbw_kv4_attention_shared": ([_P, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, ctypes.c_float,
+                                  _I64, _I64, _P, _SZ, _P], _ST),
+    "mbw_kv4_attention_shared_workspace_bytes": ([_I32, _I64, _I64], _SZ),
     "mbw_token_logprobs": ([_P, ctypes.c_int, _I64, _P, _I64, _I64, ctypes.c_float, _I32, _P, _P, _P, _P, _P, _P, _SZ,
                             _P], _ST),
     "mbw_token_logprobs_workspace_bytes": ([], _SZ),
@@ -514,7 +523,7 @@ def _types():
     global _dtypes
     if _dtypes is None:
         torch = _torch()
-        _dtypes = (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8, torch.empty)
+        _dtypes = (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8, torch.empty, torch.float8_e4m3fn)
     return _dtypes
 
 
@@ -633,7 +642,7 @@ def kv4_append(cache, k, v, slots, q=None, positions=None, cos_sin=None, interle
         if r is not None:
             return r[0] if r.__class__ is tuple else check("mbw_kv4_append", r)
     cache._check()
-    bf16, f32, i32, i64, _, empty = _types()
+    bf16, f32, i32, i64, _, empty, _ = _types()
     hk, d = cache.kv_heads, cache.head_dim
     T, _, ks = _need_rows(k, "k", hk, d)
     Tv, _, vs = _need_rows(v, "v", hk, d)
@@ -681,7 +690,7 @@ def kv4_gather(cache, slots):
         if r is not None:
             return r if r.__class__ is tuple else check("mbw_kv4_gather", r)
     cache._check()
-    bf16, _, _, i64, _, empty = _types()
+    bf16, _, _, i64, _, empty, _ = _types()
     T, = _plain(slots, "slots", i64, 1)
     dev = _check_devices(cache.pages, slots)
     shape, device = (T, cache.kv_heads, cache.head_dim), slots.device
@@ -713,8 +722,29 @@ def kv4_attention(cache, q, block_table, ctx_lens, q_starts=None, scale=None, wi
                                 cache.head_dim ** -0.5 if scale is None else scale, window, return_lse, workspace)
         if r is not None:
             return check("mbw_kv4_attention", r) if r.__class__ is int else r
+    return _kv4_attention(cache, q, block_table, ctx_lens, q_starts, scale, window, out, return_lse, workspace)
+
+
+def kv4_attention_shared_workspace(head_dim, tokens, q_heads, device="cuda"):
+    """A workspace for kv4_attention_shared of up to `tokens` query tokens (zero, as it has to be before its first use); one
+    per stream. It serves kv4_attention too."""
+    torch = _torch()
+    return torch.zeros(int(lib().mbw_kv4_attention_shared_workspace_bytes(head_dim, tokens, q_heads)), dtype=torch.uint8,
+                       device=device)
+
+
+def kv4_attention_shared(cache, q, block_table, ctx_lens, shared_len, q_starts=None, scale=None, window=0, out=None,
+                         return_lse=False, workspace=None):
+    """kv4_attention for requests that begin with the same shared_len tokens in the same pages: the first shared_len //
+    page_size entries of the rows of block_table are equal, as far as each request's length goes. The shared pages are
+    read and multiplied once for the queries of all requests. The other arguments and the result are kv4_attention's.
+    workspace: from kv4_attention_shared_workspace; without one, shared pages are read for each request."""
+    return _kv4_attention(cache, q, block_table, ctx_lens, q_starts, scale, window, out, return_lse, workspace, shared_len)
+
+
+def _kv4_attention(cache, q, block_table, ctx_lens, q_starts, scale, window, out, return_lse, workspace, shared_len=None):
     cache._check()
-    bf16, f32, i32, _, _, empty = _types()
+    bf16, f32, i32, _, _, empty, _ = _types()
     d = cache.head_dim
     T, hq, qs = _need_rows(q, "q", None, d)
     B, width = _plain(block_table, "block_table", i32, 2)
@@ -739,12 +769,136 @@ def kv4_attention(cache, q, block_table, ctx_lens, q_starts=None, scale=None, wi
         lp = lse.data_ptr()
     dev = _check_devices(cache.pages, q, block_table, ctx_lens, q_starts, out, workspace)
     wp, wn = _ws(workspace)
-    st = lib().mbw_kv4_attention(
-        ctypes.byref(cache._c), q.data_ptr(), qs, out.data_ptr(), os_, lp, block_table.data_ptr(), width, width,
-        ctx_lens.data_ptr(), sp, B, T, hq, d ** -0.5 if scale is None else scale, window, wp, wn, _raw_stream(dev))
+    args = (ctypes.byref(cache._c), q.data_ptr(), qs, out.data_ptr(), os_, lp, block_table.data_ptr(), width, width,
+            ctx_lens.data_ptr(), sp, B, T, hq, d ** -0.5 if scale is None else scale, window)
+    if shared_len is None:
+        name, st = "mbw_kv4_attention", lib().mbw_kv4_attention(*args, wp, wn, _raw_stream(dev))
+    else:
+        name, st = "mbw_kv4_attention_shared", lib().mbw_kv4_attention_shared(*args, shared_len, wp, wn, _raw_stream(dev))
     if st:
-        check("mbw_kv4_attention", st)
+        check(name, st)
     return (out, lse) if return_lse else out
+
+
+def _codes(t, name):
+    """e4m3 codes, a matrix whose width is a multiple of 128; returns its shape."""
+    shape = _plain(t, name, _types()[6], 2)
+    if shape[1] % 128 or not shape[1]:
+        raise ValueError(f"{name} must have a positive multiple of 128 columns, got {shape[1]}")
+    return shape
+
+
+def _matrix(t, name, dtype, shape):
+    if _plain(t, name, dtype, 2) != shape:
+        _need_shape(t, name, shape)
+
+
+def quantize_fp8_g128(X, norm_weight=None, norm_eps=1e-6):
+    """Activations bf16 (M, K) (rows may be apart) -> (Xq float8_e4m3fn (M, K), x_scales fp32 (M, K/128)): per row and
+    128 columns scale = max|x| / 448, code = e4m3(x / scale). With norm_weight bf16 (K,), of the RMS-normed rows."""
+    torch = _torch()
+    bf16, f32 = _types()[:2]
+    if not isinstance(X, torch.Tensor):
+        raise TypeError("X must be a torch.Tensor")
+    if not X.is_cuda:
+        raise ValueError("X must be a CUDA tensor")
+    if X.dtype != bf16:
+        raise TypeError(f"X must be {bf16}, got {X.dtype}")
+    if X.dim() != 2 or (X.stride(1) != 1 and X.shape[1] > 1):
+        raise ValueError("X must have 2 dimensions and contiguous rows")
+    M, K = X.shape
+    if K % 128 or not K:
+        raise ValueError(f"X must have a positive multiple of 128 columns, got {K}")
+    np_ = None
+    if norm_weight is not None:
+        _vector(norm_weight, "norm_weight", bf16, K)
+        np_ = norm_weight.data_ptr()
+    dev = _check_devices(X, norm_weight)
+    Xq = torch.empty((M, K), dtype=_types()[6], device=X.device)
+    xs = torch.empty((M, K // 128), dtype=f32, device=X.device)
+    st = lib().mbw_quantize_fp8_g128(X.data_ptr(), X.stride(0) if M > 1 else K, Xq.data_ptr(), xs.data_ptr(), M, K, np_,
+                                     norm_eps, _raw_stream(dev))
+    if st:
+        check("mbw_quantize_fp8_g128", st)
+    return Xq, xs
+
+
+def quantize_fp8_b128(W):
+    """Weights bf16 (N, K) -> (Wq float8_e4m3fn (N, K), w_scales fp32 (ceil(N/128), K/128)), a scale per 128 x 128."""
+    torch = _torch()
+    N, K = _plain(W, "W", torch.bfloat16, 2)
+    if K % 128 or not K:
+        raise ValueError(f"W must have a positive multiple of 128 columns, got {K}")
+    dev = _check_devices(W)
+    Wq = torch.empty((N, K), dtype=_types()[6], device=W.device)
+    ws = torch.empty(((N + 127) // 128, K // 128), dtype=torch.float32, device=W.device)
+    st = lib().mbw_quantize_fp8_b128(W.data_ptr(), Wq.data_ptr(), ws.data_ptr(), N, K, _raw_stream(dev))
+    if st:
+        check("mbw_quantize_fp8_b128", st)
+    return Wq, ws
+
+
+def _dequant_fp8(name, codes, scales, rows):
+    torch = _torch()
+    M, K = _codes(codes, "codes")
+    _matrix(scales, "scales", torch.float32, ((M + rows - 1) // rows, K // 128))
+    dev = _check_devices(codes, scales)
+    out = torch.empty((M, K), dtype=torch.float32, device=codes.device)
+    st = getattr(lib(), name)(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), M, K, _raw_stream(dev))
+    if st:
+        check(name, st)
+    return out
+
+
+def dequant_fp8_g128(Xq, x_scales):
+    """The fp32 values (M, K) of quantize_fp8_g128's codes and scales."""
+    return _dequant_fp8("mbw_dequant_fp8_g128", Xq, x_scales, 1)
+
+
+def dequant_fp8_b128(Wq, w_scales):
+    """The fp32 values (N, K) of quantize_fp8_b128's codes and scales."""
+    return _dequant_fp8("mbw_dequant_fp8_b128", Wq, w_scales, 128)
+
+
+def gemm_fp8_workspace(device="cuda"):
+    """A workspace for gemm_fp8_b128 (zero, as it has to be before its first use); one per stream."""
+    torch = _torch()
+    return torch.zeros(int(lib().mbw_gemm_fp8_b128_workspace_bytes()), dtype=torch.uint8, device=device)
+
+
+def gemm_fp8_b128(Xq, x_scales, Wq, w_scales, out=None, residual=None, up_weights=None, up_scales=None, workspace=None):
+    """Y = X . W^T of 8-bit floating point operands with a scale for each block of 128: Xq float8_e4m3fn (M, K),
+    x_scales fp32 (M, K/128) (quantize_fp8_g128), Wq float8_e4m3fn (N, K), w_scales fp32 (ceil(N/128), K/128)
+    (quantize_fp8_b128) -> Y bf16 (M, N). With up_weights and up_scales, laid out as Wq and w_scales, the gated form
+    silu(X . W^T) * (X . U^T); residual bf16 (M, N) (may be `out`) is added. workspace: from gemm_fp8_workspace; without
+    one, few rows take longer."""
+    f32 = _types()[1]
+    M, K = _codes(Xq, "Xq")
+    N, Kw = _codes(Wq, "Wq")
+    if Kw != K:
+        raise ValueError(f"Wq must be (N, {K}), got {tuple(Wq.shape)}")
+    _matrix(x_scales, "x_scales", f32, (M, K // 128))
+    blocks = ((N + 127) // 128, K // 128)
+    _matrix(w_scales, "w_scales", f32, blocks)
+    f = MbwFusion()
+    if (up_weights is None) != (up_scales is None):
+        raise ValueError("up_weights and up_scales go together")
+    if up_weights is not None:
+        if _codes(up_weights, "up_weights") != (N, K):
+            _need_shape(up_weights, "up_weights", (N, K))
+        _matrix(up_scales, "up_scales", f32, blocks)
+        f.up_weights, f.up_scales = up_weights.data_ptr(), up_scales.data_ptr()
+    if residual is not None:
+        _matrix(residual, "residual", _types()[0], (M, N))
+        f.residual = residual.data_ptr()
+    Y = _alloc_out((M, N), Xq, out)
+    dev = _check_devices(Xq, x_scales, Wq, w_scales, Y, residual, up_weights, up_scales, workspace)
+    wp, wn = _ws(workspace)
+    st = lib().gemm_fp8_b128(Xq.data_ptr(), x_scales.data_ptr(), Wq.data_ptr(), w_scales.data_ptr(), Y.data_ptr(), M, N, K,
+                             ctypes.byref(f), wp, wn, _raw_stream(dev))
+    if st:
+        check("gemm_fp8_b128", st)
+    return Y
 
 
 TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprob rank entropy top_ids top_logprobs")
@@ -767,7 +921,7 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, workspace=None):
         r = _fast.token_logprobs(logits, targets, top_k, scale, workspace)
         if r is not None:
             return TokenLogprobs._make(r) if r.__class__ is tuple else check("mbw_token_logprobs", r)
-    bf16, f32, i32, _, _, empty = _types()
+    bf16, f32, i32, _, _, empty, _ = _types()
     try:
         shape, dtype, device = logits.shape, logits.dtype, logits.device
     except AttributeError:

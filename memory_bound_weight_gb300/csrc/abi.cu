@@ -448,15 +448,14 @@ size_t mbw_kv4_attention_workspace_bytes(int32_t head_dim) {
     return (head_dim == 64 || head_dim == 128 || head_dim == 256) ? kv4_attention_workspace(head_dim) : 0;
 }
 
-mbw_status mbw_kv4_attention(const mbw_kv4_cache* cache, const void* q, int64_t q_stride, void* out,
-                             int64_t out_stride, float* lse, const int32_t* block_table, int64_t table_stride,
-                             int64_t table_width, const int32_t* ctx_lens, const int32_t* q_starts, int64_t B,
-                             int64_t T, int64_t q_heads, float scale, int64_t window, void* workspace,
-                             size_t ws_bytes, mbw_stream_t stream) {
-    const char* fn = "mbw_kv4_attention";
+static mbw_status kv4_attention_call(const char* fn, const mbw_kv4_cache* cache, const void* q, int64_t q_stride, void* out,
+                                     int64_t out_stride, float* lse, const int32_t* block_table, int64_t table_stride,
+                                     int64_t table_width, const int32_t* ctx_lens, const int32_t* q_starts, int64_t B,
+                                     int64_t T, int64_t q_heads, float scale, int64_t window, int64_t shared_len,
+                                     void* workspace, size_t ws_bytes, mbw_stream_t stream) {
     mbw_status st = check_cache(fn, cache);
     if (st != MBW_OK) return st;
-    if (B < 0 || T < 0 || table_stride < 0 || table_width < 0 || window < 0)
+    if (B < 0 || T < 0 || table_stride < 0 || table_width < 0 || window < 0 || shared_len < 0)
         return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": negative size");
     if (q_heads < 1 || q_heads % cache->kv_heads != 0)
         return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": q_heads must be a positive multiple of kv_heads");
@@ -464,6 +463,8 @@ mbw_status mbw_kv4_attention(const mbw_kv4_cache* cache, const void* q, int64_t 
         return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": at most 2^20 requests and MBW_MAX_DIM query rows");
     if (table_width * cache->page_size > MBW_MAX_DIM)
         return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": at most MBW_MAX_DIM tokens per request");
+    if (shared_len > table_width * cache->page_size)
+        return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": shared_len is longer than the block table's rows");
     if (T == 0) return MBW_OK;
     if (B == 0) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": queries of no request");
     if (!q_starts && T % B != 0)
@@ -508,8 +509,35 @@ mbw_status mbw_kv4_attention(const mbw_kv4_cache* cache, const void* q, int64_t 
     a.workspace = workspace;
     a.ws_bytes = workspace ? ws_bytes : 0;
     if (take_injected_failure("attention launch")) return MBW_ERR_CUDA;
-    cudaError_t e = launch_kv4_attention(a, (cudaStream_t)stream);
+    const int whole = (int)(shared_len / cache->page_size * cache->page_size);
+    cudaError_t e = whole > 0 ? launch_kv4_attention_shared(a, whole, (cudaStream_t)stream) : launch_kv4_attention(a, (cudaStream_t)stream);
     return e == cudaSuccess ? MBW_OK : cuda_fail(e, "attention launch");
+}
+
+mbw_status mbw_kv4_attention(const mbw_kv4_cache* cache, const void* q, int64_t q_stride, void* out,
+                             int64_t out_stride, float* lse, const int32_t* block_table, int64_t table_stride,
+                             int64_t table_width, const int32_t* ctx_lens, const int32_t* q_starts, int64_t B,
+                             int64_t T, int64_t q_heads, float scale, int64_t window, void* workspace,
+                             size_t ws_bytes, mbw_stream_t stream) {
+    return kv4_attention_call("mbw_kv4_attention", cache, q, q_stride, out, out_stride, lse, block_table, table_stride, table_width,
+                              ctx_lens, q_starts, B, T, q_heads, scale, window, 0, workspace, ws_bytes, stream);
+}
+
+mbw_status mbw_kv4_attention_shared(const mbw_kv4_cache* cache, const void* q, int64_t q_stride, void* out,
+                                    int64_t out_stride, float* lse, const int32_t* block_table, int64_t table_stride,
+                                    int64_t table_width, const int32_t* ctx_lens, const int32_t* q_starts, int64_t B,
+                                    int64_t T, int64_t q_heads, float scale, int64_t window, int64_t shared_len,
+                                    void* workspace, size_t ws_bytes, mbw_stream_t stream) {
+    return kv4_attention_call("mbw_kv4_attention_shared", cache, q, q_stride, out, out_stride, lse, block_table, table_stride,
+                              table_width, ctx_lens, q_starts, B, T, q_heads, scale, window, shared_len, workspace, ws_bytes,
+                              stream);
+}
+
+size_t mbw_kv4_attention_shared_workspace_bytes(int32_t head_dim, int64_t T, int64_t q_heads) {
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || T < 0 || q_heads < 1 || q_heads > 65536 ||
+        T > MBW_MAX_DIM || T * q_heads > MBW_MAX_DIM)
+        return 0;
+    return kv4_attention_shared_workspace(head_dim, T, q_heads);
 }
 
 size_t mbw_token_logprobs_workspace_bytes(void) { return token_logprobs_workspace(); }
@@ -552,6 +580,107 @@ mbw_status mbw_token_logprobs(const void* logits, int fp32, int64_t row_stride, 
     if (take_injected_failure("logprobs launch")) return MBW_ERR_CUDA;
     cudaError_t e = launch_token_logprobs(a, (cudaStream_t)stream);
     return e == cudaSuccess ? MBW_OK : cuda_fail(e, "logprobs launch");
+}
+
+// Sizes of a matrix held with a scale for each block of 128 columns.
+static mbw_status check_fp8(const char* fn, int64_t M, int64_t N, int64_t K) {
+    mbw_status st = check_sizes(fn, M, N, K, 128);
+    if (st != MBW_OK) return st;
+    if (K == 0) return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": K must be positive");
+    return MBW_OK;
+}
+
+mbw_status mbw_quantize_fp8_g128(const void* X, int64_t x_stride, uint8_t* Xq, float* x_scales, int64_t M, int64_t K,
+                                 const void* norm_weight, double norm_eps, mbw_stream_t stream) {
+    const char* fn = "mbw_quantize_fp8_g128";
+    mbw_status st = check_fp8(fn, M, 0, K);
+    if (st != MBW_OK) return st;
+    if (norm_weight && !(norm_eps >= 0 && norm_eps <= 3.0e38))
+        return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": norm_eps must be finite and not negative");
+    if (M == 0) return MBW_OK;
+    if (x_stride < K) return fail(MBW_ERR_BAD_SHAPE, std::string(fn) + ": x_stride is shorter than the row");
+    if (!X || !Xq || !x_scales) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    if (!aligned(X, 16) || !aligned(Xq, 16) || !aligned(norm_weight, 16) || x_stride % 8 || !aligned(x_scales, 4))
+        return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": X, Xq and norm_weight must be 16-byte aligned, x_stride a "
+                                                          "multiple of 8, x_scales 4-byte aligned");
+    if (take_injected_failure("quantize launch")) return MBW_ERR_CUDA;
+    cudaError_t e = launch_quantize_fp8_rows((const uint16_t*)X, x_stride, Xq, x_scales, M, K, (const uint16_t*)norm_weight,
+                                             norm_eps, (cudaStream_t)stream);
+    return e == cudaSuccess ? MBW_OK : cuda_fail(e, "quantize launch");
+}
+
+mbw_status mbw_quantize_fp8_b128(const void* W, uint8_t* Wq, float* w_scales, int64_t N, int64_t K, mbw_stream_t stream) {
+    const char* fn = "mbw_quantize_fp8_b128";
+    mbw_status st = check_fp8(fn, 0, N, K);
+    if (st != MBW_OK) return st;
+    if (N == 0) return MBW_OK;
+    if (!W || !Wq || !w_scales) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    if (!aligned(W, 16) || !aligned(Wq, 16) || !aligned(w_scales, 4))
+        return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": W and Wq must be 16-byte aligned, w_scales 4-byte");
+    if (take_injected_failure("quantize launch")) return MBW_ERR_CUDA;
+    cudaError_t e = launch_quantize_fp8_blocks((const uint16_t*)W, Wq, w_scales, N, K, (cudaStream_t)stream);
+    return e == cudaSuccess ? MBW_OK : cuda_fail(e, "quantize launch");
+}
+
+static mbw_status dequant_fp8_call(const char* fn, const uint8_t* Q, const float* scales, float* out, int64_t M, int64_t K,
+                                   int rows_per_scale, mbw_stream_t stream) {
+    mbw_status st = check_fp8(fn, M, 0, K);
+    if (st != MBW_OK) return st;
+    if (M == 0) return MBW_OK;
+    if (!Q || !scales || !out) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    if (!aligned(Q, 16) || !aligned(out, 16) || !aligned(scales, 4))
+        return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": codes and out must be 16-byte aligned, scales 4-byte");
+    if (take_injected_failure("dequant launch")) return MBW_ERR_CUDA;
+    cudaError_t e = launch_dequant_fp8(Q, scales, out, M, K, rows_per_scale, (cudaStream_t)stream);
+    return e == cudaSuccess ? MBW_OK : cuda_fail(e, "dequant launch");
+}
+
+mbw_status mbw_dequant_fp8_g128(const uint8_t* Xq, const float* x_scales, float* out, int64_t M, int64_t K, mbw_stream_t stream) {
+    return dequant_fp8_call("mbw_dequant_fp8_g128", Xq, x_scales, out, M, K, 1, stream);
+}
+
+mbw_status mbw_dequant_fp8_b128(const uint8_t* Wq, const float* w_scales, float* out, int64_t N, int64_t K, mbw_stream_t stream) {
+    return dequant_fp8_call("mbw_dequant_fp8_b128", Wq, w_scales, out, N, K, 128, stream);
+}
+
+size_t mbw_gemm_fp8_b128_workspace_bytes(void) { return gemm_fp8_workspace(); }
+
+mbw_status gemm_fp8_b128(const uint8_t* Xq, const float* x_scales, const uint8_t* Wq, const float* w_scales, void* Y, int64_t M,
+                         int64_t N, int64_t K, const mbw_fusion* fusion, void* workspace, size_t ws_bytes, mbw_stream_t stream) {
+    const char* fn = "gemm_fp8_b128";
+    mbw_status st = check_fp8(fn, M, N, K);
+    if (st != MBW_OK) return st;
+    const mbw_fusion none{};
+    const mbw_fusion& f = fusion ? *fusion : none;
+    if (f.norm_weight)
+        return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": the norm belongs to mbw_quantize_fp8_g128, norm_weight must be NULL");
+    if (f.up_zeros) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": up_zeros must be NULL");
+    if (!f.up_weights != !f.up_scales)
+        return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": up_weights and up_scales go together");
+    if (M == 0 || N == 0) return MBW_OK;
+    if (!Xq || !x_scales || !Wq || !w_scales || !Y) return fail(MBW_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    if (!aligned(Xq, 16) || !aligned(Wq, 32) || !aligned(f.up_weights, 32) || !aligned(Y, 16) || !aligned(x_scales, 4) ||
+        !aligned(w_scales, 4) || !aligned(f.up_scales, 4) || !aligned(f.residual, 2) || !aligned(workspace, 16))
+        return fail(MBW_ERR_MISALIGNED, std::string(fn) + ": weights must be 32-byte aligned, Xq, Y and workspace 16-byte, "
+                                                          "scales 4-byte, residual 2-byte");
+    Fp8Args a{};
+    a.X = Xq;
+    a.xs = x_scales;
+    a.W = Wq;
+    a.ws = w_scales;
+    a.U = static_cast<const uint8_t*>(f.up_weights);
+    a.us = static_cast<const float*>(f.up_scales);
+    a.y = Y;
+    a.residual = static_cast<const uint16_t*>(f.residual);
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.out_f32 = g_out_f32;
+    a.workspace = workspace;
+    a.ws_bytes = workspace ? ws_bytes : 0;
+    if (take_injected_failure("GEMM launch")) return MBW_ERR_CUDA;
+    cudaError_t e = launch_gemm_fp8(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MBW_OK : cuda_fail(e, "GEMM launch");
 }
 
 size_t mbw_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
@@ -598,22 +727,22 @@ mbw_status mbw_check_device_error(void) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     const int f = tma_take_fault();
-    const int f2 = tc_take_fault(), f3 = kv4_attn_tc_take(true);
+    const int f2 = tc_take_fault(), f3 = kv4_attn_tc_take(true), f4 = gemm_fp8_take_fault();
     const int r = kv4_cache_take_range(), r2 = kv4_attn_take_range(), r3 = logprobs_take_range();
     const int r4 = kv4_attn_tc_take(false);
-    if (f < 0 || f2 < 0 || f3 < 0 || r < 0 || r2 < 0 || r3 < 0 || r4 < 0)
+    if (f < 0 || f2 < 0 || f3 < 0 || f4 < 0 || r < 0 || r2 < 0 || r3 < 0 || r4 < 0)
         return cuda_fail(cudaGetLastError(), "reading the device fault flag");
     // Every flag is cleared, so every one is named; the status is that of the gravest.
     std::string what;
     auto name = [&](bool set, const char* text) {
         if (set) what += (what.empty() ? "" : "; ") + std::string(text);
     };
-    name(f || f2 || f3, "a bounded wait inside a kernel expired");
+    name(f || f2 || f3 || f4, "a bounded wait inside a kernel expired");
     name(r, "a cache slot or position was out of range");
     name(r2 || r4, "a page id, context length or query offset was out of range");
     name(r3, "a target token id was out of range");
     if (what.empty()) return MBW_OK;
-    return fail(f || f2 || f3 ? MBW_ERR_DEVICE_TIMEOUT : MBW_ERR_DEVICE_RANGE, what);
+    return fail(f || f2 || f3 || f4 ? MBW_ERR_DEVICE_TIMEOUT : MBW_ERR_DEVICE_RANGE, what);
 }
 
 mbw_status mbw_selftest_wait_expiry(int64_t tries, mbw_stream_t stream) {

@@ -238,6 +238,29 @@ cudaError_t launch_quantize_int8_pc(const uint16_t* W, int8_t* Wq, float* scales
 // Load-time INT4 repack (quantize.cu): N x K/8 words, in place allowed.
 cudaError_t launch_repack_int4(const uint8_t* Wq, uint8_t* Wr, int64_t N, int64_t K, cudaStream_t s);
 
+// 8-bit floating point with a scale for each block of 128 (quantize_fp8.cu, gemm_fp8.cu). Codes are e4m3.
+struct Fp8Args {
+    const uint8_t* X;  // [M][K]
+    const float* xs;   // [M][K / 128]
+    const uint8_t* W;  // [N][K]
+    const float* ws;   // [ceil(N / 128)][K / 128]
+    const uint8_t* U;  // the up matrix of the gated form, or NULL
+    const float* us;
+    void* y;                   // bf16 or fp32 [M][N]
+    const uint16_t* residual;  // bf16 [M][N] or NULL; may be y
+    int M, N, K;
+    int out_f32;
+    void* workspace;
+    size_t ws_bytes;
+};
+cudaError_t launch_gemm_fp8(const Fp8Args& a, cudaStream_t s);
+size_t gemm_fp8_workspace();
+int gemm_fp8_take_fault();
+cudaError_t launch_quantize_fp8_rows(const uint16_t* X, int64_t stride, uint8_t* Q, float* S, int64_t M, int64_t K, const uint16_t* norm_w,
+                                     double eps, cudaStream_t s);
+cudaError_t launch_quantize_fp8_blocks(const uint16_t* W, uint8_t* Q, float* S, int64_t N, int64_t K, cudaStream_t s);
+cudaError_t launch_dequant_fp8(const uint8_t* Q, const float* S, float* out, int64_t M, int64_t K, int rows_per_scale, cudaStream_t s);
+
 // 4-bit paged key/value cache (kv4_cache.cu, kv4_attention.cu; layout in kv4.cuh).
 struct Kv4AppendArgs {
     uint8_t* pages;
@@ -290,6 +313,9 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s);
 size_t kv4_attention_workspace(int head_dim);
+// The first shared_len tokens (whole pages) of every request lie in the same pages.
+cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int shared_len, cudaStream_t s);
+size_t kv4_attention_shared_workspace(int head_dim, int64_t T, int64_t q_heads);
 cudaError_t launch_kv4_attention_tc(const Kv4AttnArgs& a, cudaStream_t s);  // head dimensions 64 and 128
 size_t kv4_attention_tc_workspace(int head_dim);
 cudaError_t kv4_allow_smem(const void* kernel, int bytes);  // its dynamic shared memory, once per kernel and device

@@ -1217,6 +1217,10 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     return cudaLaunchKernelExC(&cfg, e.fn, params);
 }
 
+size_t kv4_attention_shared_workspace(int head_dim, int64_t, int64_t) { return kv4_attention_workspace(head_dim); }
+
+cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int, cudaStream_t s) { return launch_kv4_attention(a, s); }
+
 int kv4_attn_take_range() {
     int v = 0, z = 0;
     if (cudaMemcpyFromSymbol(&v, g_kv4_attn_range, sizeof(int)) != cudaSuccess) return -1;
