@@ -326,15 +326,12 @@ mbw_status gemv_fused_awq_g128(const uint8_t *Wq, const void *scales, const uint
  * fusion (NULL: none): residual (may be Y), and with up_weights and up_scales,
  * a second matrix of the same layout, the gated form silu(X.W^T) * (X.U^T) of a
  * feed-forward block in one kernel; norm_weight and up_zeros must be NULL.
- * Wq and up_weights 32-byte aligned, Xq, Y and workspace 16-byte.
- * workspace: mbw_gemm_fp8_b128_workspace_bytes() bytes, zero before its first
- * use and left so by every call (one per stream). Smaller or NULL: few rows run
- * on fewer CTAs and take longer, and their sums are taken in another order.
+ * Wq and up_weights 32-byte aligned, Xq, Y and workspace 16-byte. No variant
+ * needs a workspace.
  */
 mbw_status gemm_fp8_b128(const uint8_t *Xq, const float *x_scales, const uint8_t *Wq, const float *w_scales, void *Y,
                          int64_t M, int64_t N, int64_t K, const mbw_fusion *fusion, void *workspace, size_t ws_bytes,
                          mbw_stream_t stream);
-size_t mbw_gemm_fp8_b128_workspace_bytes(void);
 
 /*
  * 4-bit paged key/value cache: what stands between the QKV product and the

@@ -16,7 +16,7 @@ _EXPORTS = frozenset((
     "OP_GEMV_INT8_PC",
     "Kv4Cache", "kv4_page_bytes", "kv4_append", "kv4_gather", "kv4_attention", "kv4_attention_workspace",
     "token_logprobs", "token_logprobs_workspace", "TokenLogprobs",
-    "quantize_fp8_g128", "quantize_fp8_b128", "dequant_fp8_g128", "dequant_fp8_b128", "gemm_fp8_b128", "gemm_fp8_workspace",
+    "quantize_fp8_g128", "quantize_fp8_b128", "dequant_fp8_g128", "dequant_fp8_b128", "gemm_fp8_b128",
     "kv4_attention_shared", "kv4_attention_shared_workspace",
 ))
 

@@ -74,7 +74,6 @@ SIGNATURES = {
     "mbw_dequant_fp8_g128": ([_P, _P, _P, _I64, _I64, _P], _ST),
     "mbw_dequant_fp8_b128": ([_P, _P, _P, _I64, _I64, _P], _ST),
     "gemm_fp8_b128": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.POINTER(MbwFusion), _P, _SZ, _P], _ST),
-    "mbw_gemm_fp8_b128_workspace_bytes": ([], _SZ),
     "mbw_kv4_page_bytes": ([_I32, _I32, _I32, _I32], _SZ),
     "mbw_kv4_append": ([_P, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _I64, _P], _ST),
     "mbw_kv4_gather": ([_P, _P, _P, _P, _I64, _P], _ST),
@@ -860,18 +859,11 @@ def dequant_fp8_b128(Wq, w_scales):
     return _dequant_fp8("mbw_dequant_fp8_b128", Wq, w_scales, 128)
 
 
-def gemm_fp8_workspace(device="cuda"):
-    """A workspace for gemm_fp8_b128 (zero, as it has to be before its first use); one per stream."""
-    torch = _torch()
-    return torch.zeros(int(lib().mbw_gemm_fp8_b128_workspace_bytes()), dtype=torch.uint8, device=device)
-
-
 def gemm_fp8_b128(Xq, x_scales, Wq, w_scales, out=None, residual=None, up_weights=None, up_scales=None, workspace=None):
     """Y = X . W^T of 8-bit floating point operands with a scale for each block of 128: Xq float8_e4m3fn (M, K),
     x_scales fp32 (M, K/128) (quantize_fp8_g128), Wq float8_e4m3fn (N, K), w_scales fp32 (ceil(N/128), K/128)
     (quantize_fp8_b128) -> Y bf16 (M, N). With up_weights and up_scales, laid out as Wq and w_scales, the gated form
-    silu(X . W^T) * (X . U^T); residual bf16 (M, N) (may be `out`) is added. workspace: from gemm_fp8_workspace; without
-    one, few rows take longer."""
+    silu(X . W^T) * (X . U^T); residual bf16 (M, N) (may be `out`) is added."""
     f32 = _types()[1]
     M, K = _codes(Xq, "Xq")
     N, Kw = _codes(Wq, "Wq")

@@ -643,10 +643,9 @@ mbw_status mbw_dequant_fp8_b128(const uint8_t* Wq, const float* w_scales, float*
     return dequant_fp8_call("mbw_dequant_fp8_b128", Wq, w_scales, out, N, K, 128, stream);
 }
 
-size_t mbw_gemm_fp8_b128_workspace_bytes(void) { return gemm_fp8_workspace(); }
-
 mbw_status gemm_fp8_b128(const uint8_t* Xq, const float* x_scales, const uint8_t* Wq, const float* w_scales, void* Y, int64_t M,
                          int64_t N, int64_t K, const mbw_fusion* fusion, void* workspace, size_t ws_bytes, mbw_stream_t stream) {
+    (void)ws_bytes;
     const char* fn = "gemm_fp8_b128";
     mbw_status st = check_fp8(fn, M, N, K);
     if (st != MBW_OK) return st;
@@ -676,8 +675,6 @@ mbw_status gemm_fp8_b128(const uint8_t* Xq, const float* x_scales, const uint8_t
     a.N = (int)N;
     a.K = (int)K;
     a.out_f32 = g_out_f32;
-    a.workspace = workspace;
-    a.ws_bytes = workspace ? ws_bytes : 0;
     if (take_injected_failure("GEMM launch")) return MBW_ERR_CUDA;
     cudaError_t e = launch_gemm_fp8(a, (cudaStream_t)stream);
     return e == cudaSuccess ? MBW_OK : cuda_fail(e, "GEMM launch");

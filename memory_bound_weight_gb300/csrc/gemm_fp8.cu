@@ -9,15 +9,19 @@
 // y is kept in registers, y += (xs ws) d. Two accumulators in turn, so that the
 // products of a block run while the one before is added.
 //
-// Two orientations of one kernel. With few rows of X (ROWS_X = false) the 128
-// lanes of the accumulator are rows of W, its columns the rows of X (16 to 128 of
-// them): the call is a stream of W, and the factor changes by column. With many,
-// lanes are rows of X and columns rows of W.
-//
 // Gated: a second matrix U of W's shape, two sums a tile, y = silu(W sum) (U sum).
 //
-// A CTA is 10 warps: one that issues the copies, one that issues the products, 8
-// that add (two for each quarter of the lanes, half of the columns each).
+// A pair of CTAs takes a tile of 256 rows of X by 256 rows of W (cta_group::2), or 128
+// of W and the same 128 of U. Each stages its own 128 rows of X and half of the other
+// side (gated: one W, the other U), 32 KB a block of k, where a CTA alone would need 48
+// for as many products, adds its 128 lanes x 256 columns into registers, 128 a thread,
+// and writes them. A CTA is 12 warps: one that issues the copies, one (the even CTA's)
+// that issues the products of both, two that multiply the scales, 8 that add.
+//
+// Where there are fewer tiles than pairs, k is cut between up to four pairs of a
+// cluster, whose sums are joined in order through their shared memory.
+//
+// Up to 16 rows of X are gemv_fp8.cu's.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -37,8 +41,10 @@ __device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__
 __device__ __forceinline__ void bar_init(uint64_t* bar, int count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_at(bar)), "r"(count));
 }
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(bar)) : "memory");
+// An accumulator is read. Relaxed: what it orders, reads of TMEM before the next products, the tcgen05 fence does, and a
+// release would wait for the warp's loads of scales (256 x 256 tiles: 1.28 us a block of k instead of 0.58).
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_at(bar)), "r"(bytes) : "memory");
@@ -52,9 +58,17 @@ __device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, bool& o
                      : "=r"(r) : "r"(smem_at(bar)), "r"(parity) : "memory");
         got = r != 0;
     }
-    got = __all_sync(0xFFFFFFFFu, got);
     if (!got) atomicExch(&g_f8_fault, 1), ok = false;
+    __syncwarp();
 }
+// Whether a phase is over, without waiting; to be looked at later (all_of), when the answer is there.
+__device__ __forceinline__ uint32_t bar_ask(uint64_t* bar, uint32_t parity) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"(smem_at(bar)), "r"(parity) : "memory");
+    return r;
+}
+__device__ __forceinline__ bool all_of(uint32_t r) { return __all_sync(0xFFFFFFFFu, r != 0); }
 __device__ __forceinline__ bool elect() {
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
@@ -119,332 +133,348 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
-constexpr int kAdders = 8, kThreads = (kAdders + 2) * 32;
-constexpr int kCounters = 1024;  // of tiles cut between CTAs; every call leaves them at zero
-__device__ __forceinline__ void bar_adders() { asm volatile("bar.sync 1, %0;" ::"n"(kAdders * 32) : "memory"); }
 
-// Lanes are 128 rows of X (ROWS_X) or of W, columns BN rows of the other; GLU: two sums of BN columns.
-template <bool ROWS_X, int BN, bool GLU>
-struct Shape {
-    static constexpr int SETS = GLU ? 2 : 1, HC = BN / 2;                       // columns a thread adds, of each set
-    static constexpr int LANE_BOX = 128 * 128, COL_BOX = BN * 128;              // bytes
-    static constexpr int LANE_BOXES = GLU && !ROWS_X ? 2 : 1, COL_BOXES = GLU && ROWS_X ? 2 : 1;
-    static constexpr int STAGE = LANE_BOXES * LANE_BOX + COL_BOXES * COL_BOX;
-    static constexpr int DEPTH = 196608 / STAGE < 12 ? 196608 / STAGE : 12;
-    static constexpr int COLS = 2 * SETS * BN;                                  // of TMEM
-    static constexpr int TABLE = ROWS_X ? 0 : kAdders * 4 * SETS * HC * 4;      // factors of 4 blocks by column, a warp's own
-    static constexpr int OFF_TABLE = DEPTH * STAGE, OFF_BAR = OFF_TABLE + TABLE;
-    static constexpr int SMEM = OFF_BAR + (2 * DEPTH + 5) * 8 + 16 + 1024;
-    static constexpr int PART = SETS * BN * 128;                                // floats of a part
-    static_assert(COLS >= 32 && COLS <= 512 && (COLS & (COLS - 1)) == 0 && DEPTH >= 3 && SMEM <= 227 * 1024, "");
-};
 
-template <bool ROWS_X, int BN, bool GLU>
+// Eight outputs of a row, `left` of them inside the matrix; wide: at lies on 8.
+__device__ __forceinline__ void put8(const Fp8Args& a, int64_t at, float* o, int left, bool wide) {
+    if (wide && left >= 8 && !a.out_f32 && (!a.residual || ((uintptr_t)a.residual & 15) == 0)) {
+        if (a.residual) {
+            const uint4 v = *reinterpret_cast<const uint4*>(a.residual + at);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[2 * i] += bf16lo_to_f32(w[i]), o[2 * i + 1] += bf16hi_to_f32(w[i]);
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) {
+            if (a.residual) o[i] += bf16lo_to_f32(a.residual[at + i]);
+            store_out(a.y, at + i, o[i], a.out_f32);
+        }
+}
+
+constexpr int kAdders = 8, kThreads = (4 + kAdders) * 32;
+// Registers: 168 a thread at launch; then by warpgroup 56 for the issuers and 2 x 224 for the adders, 504 = 3 x 168.
+constexpr int kRegsLaunch = 168, kRegsIssuers = 56, kRegsAdders = 224;
+static_assert(4 * kRegsIssuers + kAdders * kRegsAdders <= (4 + kAdders) * kRegsLaunch, "");
+constexpr int kStage = 2 * 128 * 128, kDepth = 6;
+// Factors of four blocks of k by [block][row], two each: of the columns of the even CTA's W and of the odd one's W or U.
+constexpr int kGroups = 4, kGroup = 4 * 128 * 8;
+constexpr int kOffFactor = kDepth * kStage, kOffBar = kOffFactor + kGroups * kGroup, kSmem = kOffBar + (2 * kDepth + 4 + 2 * kGroups) * 8 + 16 + 1024;
+constexpr int kPitch = 260;  // floats of a row that the CTAs of a cluster are joined in: 4 to spread the banks
+static_assert(kSmem <= 227 * 1024, "");
+static_assert(128 * kPitch * 4 <= kOffFactor, "over the ring, which is drained then");
+
+template <int N>
+__device__ __forceinline__ void registers(bool more) {
+    if (more)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <bool GLU>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                    const __grid_constant__ CUtensorMap map_u, const Fp8Args a, const int split) {
-    using S = Shape<ROWS_X, BN, GLU>;
-    constexpr int SETS = S::SETS, HC = S::HC, DEPTH = S::DEPTH;
+                    const __grid_constant__ CUtensorMap map_u, const Fp8Args a) {
+    constexpr int OUT = GLU ? 128 : 256;  // columns of Y a tile has
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_at(smem_raw) & 1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
-    uint64_t *empty = full + DEPTH, *sfull = empty + DEPTH, *sempty = sfull + 2, *done = sempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-    __shared__ uint32_t sh_last;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // the even CTA's count both of the pair
+    uint64_t *empty = full + kDepth, *sfull = empty + kDepth, *sempty = sfull + 2;  // sempty: the even CTA's count both
+    uint64_t *ffull = sempty + 2, *fempty = ffull + kGroups;  // of factors
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fempty + kGroups);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t crank, csize;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+    const int rank = crank & 1, split = csize / 2;  // of the pair; pairs that share a tile's k
     bool ok = true;
+    auto cluster_sync = [] { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); };
 
     if (tid == 0) {
-        for (int i = 0; i < DEPTH; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
-        for (int i = 0; i < 2; ++i) bar_init(&sfull[i], 1), bar_init(&sempty[i], kAdders);
-        bar_init(done, 1);
+        for (int i = 0; i < kDepth; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
+        for (int i = 0; i < 2; ++i) bar_init(&sfull[i], 1), bar_init(&sempty[i], 2 * kAdders);
+        for (int i = 0; i < kGroups; ++i) bar_init(&ffull[i], 2), bar_init(&fempty[i], kAdders);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(tmem_slot)), "n"(S::COLS));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     fence_before();
     __syncthreads();
+    cluster_sync();  // the peer's barriers exist before any copy, arrival or commit reaches them
     fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
 
-    // ---- the line: the blocks of k of all tiles, cut into equal shares, or whole tiles in turn ----
-    const int KB = a.K / 128;
-    const int tiles_m = ROWS_X ? (a.M + 127) / 128 : (a.M + BN - 1) / BN, tiles_n = ROWS_X ? (a.N + BN - 1) / BN : (a.N + 127) / 128;
-    const long long all = (long long)tiles_m * tiles_n * KB, each = all / gridDim.x, rest = all - each * gridDim.x;
-    auto start_of = [&](long long i) { return i * each + (i < rest ? i : rest); };
-    auto owner_of = [&](long long p) {
-        const long long big = rest * (each + 1);
-        return (int)(p < big ? p / (each + 1) : rest + (p - big) / each);
-    };
-    struct Piece {
-        int m0, n0, kb0, kb1;
-        long long tile;
-    };
-    struct Line {
-        long long pos, end, stride;
-    };
-    auto line = [&]() {
-        Line l;
-        l.pos = split ? start_of(blockIdx.x) : (long long)blockIdx.x * KB;
-        l.end = split ? start_of(blockIdx.x + 1) : all;
-        l.stride = split ? 0 : (long long)(gridDim.x - 1) * KB;
-        return l;
-    };
-    auto next = [&](Line& l, Piece& p) {
-        if (l.pos >= l.end) return false;
-        p.tile = l.pos / KB;
-        p.kb0 = (int)(l.pos - p.tile * KB);
-        p.kb1 = (int)min((long long)KB, p.kb0 + l.end - l.pos);
-        l.pos += p.kb1 - p.kb0 + l.stride;
-        const int tn = (int)(p.tile / tiles_m), tm = (int)(p.tile - (long long)tn * tiles_m);  // tiles of one W one behind the other
-        p.m0 = tm * (ROWS_X ? 128 : BN), p.n0 = tn * (ROWS_X ? BN : 128);
-        return true;
+    // ---- a pair takes whole tiles in turn, or of one tile its share of the blocks of k ----
+    const int KB = a.K / 128, tiles_m = (a.M + 255) / 256, tiles_n = (a.N + OUT - 1) / OUT;
+    const long long tiles = (long long)tiles_m * tiles_n, first = blockIdx.x / csize, stride = gridDim.x / csize;
+    const int kb0 = (int)((long long)KB * (crank / 2) / split), kb1 = (int)((long long)KB * (crank / 2 + 1) / split);
+    auto tile_n = [&](long long t) { return (int)(t / tiles_m); };  // tiles of one W one behind the other
+    auto tile_m0 = [&](long long t) { return (int)(t % tiles_m) * 256 + rank * 128; };
+    auto even = [&](const void* p) {  // its address in the pair's even CTA
+        uint32_t r;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_at(p)), "r"(crank & ~1u));
+        return r;
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ copies ----
-        const bool leader = elect();
-        auto weights = [&](uint8_t* st, const Piece& p, int kb, uint64_t* bar) {
-            uint8_t* to = ROWS_X ? st + S::LANE_BOX : st;
-            tma_2d(to, &map_w, kb * 128, p.n0, bar);
-            if (GLU) tma_2d(to + (ROWS_X ? S::COL_BOX : S::LANE_BOX), &map_u, kb * 128, p.n0, bar);
-        };
-        auto rows = [&](uint8_t* st, const Piece& p, int kb, uint64_t* bar) {
-            tma_2d(ROWS_X ? st : st + S::LANE_BOXES * S::LANE_BOX, &map_x, kb * 128, p.m0, bar);
-        };
-        Line l = line();
-        Piece p;
-        uint32_t it = 0;
-        bool first = true;
-        while (next(l, p)) {
-            int kb = p.kb0;
-            if (first) {  // weights do not depend on the kernel before: the ring is filled with them, then X is waited for
-                const int pre = min(DEPTH, p.kb1 - p.kb0);
-                if (leader)
-                    for (int i = 0; i < pre; ++i) {
-                        bar_expect(&full[i], S::STAGE);
-                        weights(smem + i * S::STAGE, p, p.kb0 + i, &full[i]);
-                    }
-                __syncwarp();
-                pdl_wait();
-                if (leader)
-                    for (int i = 0; i < pre; ++i) rows(smem + i * S::STAGE, p, p.kb0 + i, &full[i]);
-                __syncwarp();
-                it = pre, kb += pre, first = false;
-            }
-            for (; kb < p.kb1 && ok; ++kb, ++it) {
-                const uint32_t s = it % DEPTH;
-                if (it >= DEPTH) bar_wait(&empty[s], (it / DEPTH - 1) & 1, ok);
-                if (!ok) break;
-                if (leader) {
-                    bar_expect(&full[s], S::STAGE);
-                    weights(smem + s * S::STAGE, p, kb, &full[s]);
-                    rows(smem + s * S::STAGE, p, kb, &full[s]);
-                }
-                __syncwarp();
-            }
-            if (!ok) break;
-        }
-        if (!ok) {  // no copy lands behind the CTA's end
-            const uint32_t stop = it;
-            for (uint32_t j = stop > DEPTH ? stop - DEPTH : 0; j < stop; ++j) {
-                bool o = true;
-                bar_wait(&full[j % DEPTH], (j / DEPTH) & 1, o);
-            }
-        }
-    } else if (warp == 1) {
-        // ---------------------------------------------------------- products ----
-        const bool leader = elect();
-        constexpr uint32_t ID = idesc(128, GLU && ROWS_X ? 2 * BN : BN);
-        Line l = line();
-        Piece p;
-        uint32_t it = 0;
-        while (next(l, p))
-            for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                const uint32_t s = it % DEPTH, b = it & 1;
-                if (it >= 2) bar_wait(&sempty[b], (it / 2 - 1) & 1, ok);
-                bar_wait(&full[s], (it / DEPTH) & 1, ok);
-                fence_after();
-                if (leader) {
-                    if (ok) {
-                        const uint32_t at = smem_at(smem + s * S::STAGE), d = tmem + b * SETS * BN;
-                        const uint64_t da = desc(at), db = desc(at + S::LANE_BOXES * S::LANE_BOX);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {  // 32 codes each: 32 bytes further inside the swizzle atom
-                            mma(d, da + 2 * k, db + 2 * k, ID, k > 0);
-                            if (GLU && !ROWS_X) mma(d + BN, da + S::LANE_BOX / 16 + 2 * k, db + 2 * k, ID, k > 0);
+    if (warp < 4) {
+        registers<kRegsIssuers>(false);
+        if (warp == 0) {
+            // -------------------------------------------------------- copies ----
+            const bool leader = elect();
+            const uint32_t full0 = even(full);
+            auto copy = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1, uint32_t s) {
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                        smem_at(dst)),
+                    "l"(map), "r"(c0), "r"(c1), "r"(full0 + 8 * s)
+                    : "memory");
+            };
+            const CUtensorMap* w = GLU && rank ? &map_u : &map_w;
+            uint32_t it = 0;
+            for (long long t = first; t < tiles && ok; t += stride) {
+                const int n0 = tile_n(t) * OUT + (GLU ? 0 : rank * 128), m0 = tile_m0(t);
+                int kb = kb0;
+                if (t == first) {  // weights do not depend on the kernel before: the ring is filled with them, then X is waited for
+                    const int pre = min(kDepth, kb1 - kb0);
+                    if (leader)
+                        for (int i = 0; i < pre; ++i) {
+                            if (rank == 0) bar_expect(&full[i], 2 * kStage);
+                            copy(smem + i * kStage + 128 * 128, w, (kb + i) * 128, n0, i);
                         }
-                    }
-                    commit(&empty[s]);
-                    commit(&sfull[b]);
+                    __syncwarp();
+                    pdl_wait();
+                    if (leader)
+                        for (int i = 0; i < pre; ++i) copy(smem + i * kStage, &map_x, (kb + i) * 128, m0, i);
+                    __syncwarp();
+                    it = pre, kb += pre;
                 }
-                __syncwarp();
+                for (; kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % kDepth;
+                    if (it >= kDepth) bar_wait(&empty[s], (it / kDepth - 1) & 1, ok);
+                    if (!ok) break;
+                    if (leader) {
+                        if (rank == 0) bar_expect(&full[s], 2 * kStage);
+                        copy(smem + s * kStage + 128 * 128, w, kb * 128, n0, s);
+                        copy(smem + s * kStage, &map_x, kb * 128, m0, s);
+                    }
+                    __syncwarp();
+                }
             }
-        // every product issued has completed before TMEM is released
-        if (leader) commit(done);
-        __syncwarp();
-        bool last = true;
-        bar_wait(done, 0, last);
+            if (!ok && rank == 0)  // no copy lands behind the pair's end: both CTAs' complete here
+                for (uint32_t j = it > kDepth ? it - kDepth : 0; j < it; ++j) {
+                    bool o = true;
+                    bar_wait(&full[j % kDepth], (j / kDepth) & 1, o);
+                }
+        } else if (warp == 1 && rank == 0) {
+            // ------------------------------------------------------ products ----
+            const bool leader = elect();
+            constexpr uint32_t ID = idesc(256, 256);
+            auto commit2 = [&](uint64_t* bar) {
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_at(bar)),
+                             "h"((uint16_t)(3 << crank))
+                             : "memory");
+            };
+            uint32_t it = 0, s = 0, turn = 0, there = 0;  // the stage, the ring's turns before it, and whether it is full
+            for (long long t = first; t < tiles; t += stride)
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t b = it & 1;
+                    const uint32_t free = it < 2 ? 1u : bar_ask(&sempty[b], (it / 2 - 1) & 1);
+                    if (!all_of(there)) bar_wait(&full[s], turn & 1, ok);
+                    if (!all_of(free)) bar_wait(&sempty[b], (it / 2 - 1) & 1, ok);
+                    fence_after();
+                    const uint32_t cur = s;
+                    if (++s == kDepth) s = 0, ++turn;
+                    there = bar_ask(&full[s], turn & 1);  // the next one's answer comes under the products' issue
+                    if (leader) {
+                        if (ok) {
+                            const uint64_t da = desc(smem_at(smem + cur * kStage)), db = da + 128 * 128 / 16;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // 32 codes each: 32 bytes further inside the swizzle atom
+                                asm volatile(
+                                    "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+                                        tmem + b * 256),
+                                    "l"(da + 2 * k), "l"(db + 2 * k), "r"(ID), "r"(k > 0 ? 1u : 0u)
+                                    : "memory");
+                        }
+                        commit2(&sfull[b]);
+                        commit2(&empty[cur]);
+                    }
+                    __syncwarp();
+                }
+            // every product issued has completed before TMEM is released: the adders wait for the last one's commit
+        } else if (warp >= 2) {
+            // ------------------------------------------------------- factors ----
+            // by two warps of their own: the loads, 32 rows apart, held the adders up by a fifth
+            const bool by4 = KB % 4 == 0 && (((uintptr_t)a.xs | (uintptr_t)a.ws | (GLU ? (uintptr_t)a.us : 0)) & 15) == 0;
+            auto fetch = [&](const float* from, int kb, bool there) {
+                if (by4) return there ? *reinterpret_cast<const float4*>(from + kb) : make_float4(0.f, 0.f, 0.f, 0.f);
+                return make_float4(there ? from[kb] : 0.f, there && kb + 1 < KB ? from[kb + 1] : 0.f, there && kb + 2 < KB ? from[kb + 2] : 0.f,
+                                   there && kb + 3 < KB ? from[kb + 3] : 0.f);
+            };
+            pdl_wait();
+            uint32_t turn = 0;
+            for (long long t = first; t < tiles; t += stride) {
+                const int m0 = tile_m0(t), nb = tile_n(t) * (OUT / 128);
+                const bool cols = nb * 128 < a.N, cols2 = GLU ? cols : (nb + 1) * 128 < a.N;
+                const float *wsp = a.ws + (int64_t)nb * KB, *usp = GLU ? a.us + (int64_t)nb * KB : wsp + KB;
+                for (int kb = kb0 & ~3; kb < kb1; kb += 4, ++turn) {
+                    const float4 ws = fetch(wsp, kb, cols), us = fetch(usp, kb, cols2);
+                    float4 xs[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int m = m0 + (warp - 2) * 64 + i * 32 + lane;
+                        xs[i] = fetch(a.xs + (int64_t)m * KB, kb, m < a.M);
+                    }
+                    const uint32_t slot = turn % kGroups;
+                    if (turn >= kGroups) bar_wait(&fempty[slot], (turn / kGroups - 1) & 1, ok);
+                    float2* to = reinterpret_cast<float2*>(smem + kOffFactor + slot * kGroup) + (warp - 2) * 64 + lane;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        to[i * 32] = make_float2(xs[i].x * ws.x, xs[i].x * us.x), to[i * 32 + 128] = make_float2(xs[i].y * ws.y, xs[i].y * us.y);
+                        to[i * 32 + 256] = make_float2(xs[i].z * ws.z, xs[i].z * us.z), to[i * 32 + 384] = make_float2(xs[i].w * ws.w, xs[i].w * us.w);
+                    }
+                    __syncwarp();
+                    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(&ffull[slot])) : "memory");
+                }
+            }
+        }
     } else {
         // ------------------------------------------------- sums by their scales ----
-        const int aw = warp - 2, quarter = warp & 3, half = aw >> 2;  // lanes, columns
-        const int r = quarter * 32 + lane;                            // the thread's row of the lanes' side
-        const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16) + half * HC;
-        float* table = reinterpret_cast<float*>(smem + S::OFF_TABLE) + aw * (4 * SETS * HC);
-        constexpr int CH = HC < 32 ? HC : 32, PER = (HC + 31) / 32;
-        float2 acc[SETS][HC / 2];
-        float* parts = reinterpret_cast<float*>(static_cast<uint32_t*>(a.workspace) + kCounters);
+        registers<kRegsAdders>(true);
+        const int quarter = warp & 3, half = (warp - 4) >> 2, r = quarter * 32 + lane;
+        const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
+        const uint32_t sempty0 = even(sempty);
+        auto column = [](int j) { return (j >> 1) * 128 + (j & 1) * 32; };  // of the j-th 32 of the thread's columns
+        float2 acc[64];  // 64 columns of the even CTA's W, 64 of the odd one's W or U
+        uint32_t v[2][32];
         pdl_wait();
-
-        auto write = [&](const Piece& p) {
+        uint32_t it = 0, group = 0;
+        for (long long t = first; t < tiles; t += stride) {
+            const int m = tile_m0(t) + r, n0 = tile_n(t) * OUT + half * 64;
+            const bool row = m < a.M;
 #pragma unroll
-            for (int c = 0; c < HC; ++c) {
-                const int m = ROWS_X ? p.m0 + r : p.m0 + half * HC + c, n = ROWS_X ? p.n0 + half * HC + c : p.n0 + r;
-                if (m >= a.M || n >= a.N) continue;
-                float v = c & 1 ? acc[0][c / 2].y : acc[0][c / 2].x;
-                if (GLU) v = silu_f32(v) * (c & 1 ? acc[SETS - 1][c / 2].y : acc[SETS - 1][c / 2].x);
-                const int64_t at = (int64_t)m * a.N + n;
-                if (a.residual) v += bf16lo_to_f32(a.residual[at]);
-                store_out(a.y, at, v, a.out_f32);
-            }
-        };
-
-        Line l = line();
-        Piece p;
-        uint32_t it = 0;
-        while (next(l, p)) {
-#pragma unroll
-            for (int s = 0; s < SETS; ++s)
-#pragma unroll
-                for (int c = 0; c < HC / 2; ++c) acc[s][c] = make_float2(0.f, 0.f);
-            // scales of 4 blocks at a time, the next ones on their way
-            const int nb = ROWS_X ? (p.n0 + (GLU ? 0 : half * HC)) / 128 : p.n0 / 128;
-            const bool nb_there = nb * 128 < a.N;
-            const float* wsp = a.ws + (int64_t)nb * KB;
-            const float* usp = a.us + (int64_t)nb * KB;
-            constexpr int XR = ROWS_X ? 1 : PER;
-            float xs[XR][4], ws[4], us[4];
-            auto fetch = [&](int kb) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool there = kb + i < p.kb1;
-                    ws[i] = there && nb_there ? __ldg(wsp + kb + i) : 0.f;
-                    us[i] = GLU && there && nb_there ? __ldg(usp + kb + i) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < XR; ++j) {
-                        const int m = ROWS_X ? p.m0 + r : p.m0 + half * HC + lane + 32 * j;
-                        const bool has = there && m < a.M && (ROWS_X || lane + 32 * j < HC);
-                        xs[j][i] = has ? a.xs[(int64_t)m * KB + kb + i] : 0.f;
-                    }
+            for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
+            float2 fg[4];  // factors of four blocks
+            bool begun = false;  // the first 32 columns of the next block are on their way
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const uint32_t b = it & 1, at = my + b * 256;
+                if (!begun) {
+                    bar_wait(&sfull[b], (it / 2) & 1, ok);
+                    fence_after();
+                    ld<32>(v[0], at);
                 }
-            };
-            fetch(p.kb0);
-            float f4[4], g4[4];  // ROWS_X: the row's factors
-            for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                const int i = (kb - p.kb0) & 3;
-                if (i == 0) {
-                    if (ROWS_X) {
+                if ((kb & 3) == 0 || kb == kb0) {
+                    const uint32_t slot = group % kGroups;
+                    bar_wait(&ffull[slot], (group / kGroups) & 1, ok);
+                    const float2* from = reinterpret_cast<const float2*>(smem + kOffFactor + slot * kGroup) + r;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) f4[q] = xs[0][q] * ws[q], g4[q] = GLU ? xs[0][q] * us[q] : 0.f;
+                    for (int i = 0; i < 4; ++i) fg[i] = from[128 * i];
+                    __syncwarp();
+                    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(&fempty[slot])) : "memory");
+                    ++group;
+                }
+                const float2 now = kb & 2 ? (kb & 1 ? fg[3] : fg[2]) : (kb & 1 ? fg[1] : fg[0]);
+                uint32_t ready = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    wait_ld<32>(v[j & 1]);
+                    if (j < 3) {
+                        ld<32>(v[(j + 1) & 1], at + column(j + 1));
                     } else {
-                        __syncwarp();  // the factors before are read
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int j = 0; j < XR; ++j)
-                                if (HC >= 32 || lane < HC) {
-                                    table[q * SETS * HC + lane + 32 * j] = xs[j][q] * ws[q];
-                                    if (GLU) table[q * SETS * HC + HC + lane + 32 * j] = xs[j][q] * us[q];
-                                }
+                        fence_before();
                         __syncwarp();
+                        if (lane == 0) bar_arrive(sempty0 + 8 * b);
+                        if (kb + 1 < kb1) ready = bar_ask(&sfull[b ^ 1], ((it + 1) / 2) & 1);
                     }
-                    fetch(kb + 4);
+                    const float2 ff = j >= 2 ? make_float2(now.y, now.y) : make_float2(now.x, now.x);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        acc[16 * j + c] = fma2(make_float2(__uint_as_float(v[j & 1][2 * c]), __uint_as_float(v[j & 1][2 * c + 1])), ff, acc[16 * j + c]);
                 }
-                const float f = i & 2 ? (i & 1 ? f4[3] : f4[2]) : (i & 1 ? f4[1] : f4[0]);
-                const float g = i & 2 ? (i & 1 ? g4[3] : g4[2]) : (i & 1 ? g4[1] : g4[0]);
-                const uint32_t b = it & 1;
-                bar_wait(&sfull[b], (it / 2) & 1, ok);
-                fence_after();
+                begun = all_of(ready);
+                if (begun) {
+                    fence_after();
+                    ld<32>(v[0], my + (b ^ 1) * 256);
+                }
+            }
+            if (split > 1) {  // into shared memory, [row][column]
+                float* to = reinterpret_cast<float*>(smem) + r * kPitch + half * 64;
 #pragma unroll
-                for (int s = 0; s < SETS; ++s)
+                for (int c = 0; c < 128; c += 4)
+                    *reinterpret_cast<float4*>(to + (c >= 64 ? 64 + c : c)) = make_float4(acc[c / 2].x, acc[c / 2].y, acc[c / 2 + 1].x, acc[c / 2 + 1].y);
+            } else if (row) {
+                const int64_t to = (int64_t)m * a.N + n0;
+                const bool wide = a.N % 8 == 0;
 #pragma unroll
-                    for (int c0 = 0; c0 < HC; c0 += CH) {
-                        uint32_t v[CH];
-                        ld<CH>(v, my + b * SETS * BN + s * BN + c0);
-                        wait_ld<CH>(v);
-                        if (s == SETS - 1 && c0 + CH >= HC) {
-                            fence_before();
-                            __syncwarp();
-                            if (lane == 0) bar_arrive(&sempty[b]);
-                        }
+                for (int c = 0; c < (GLU ? 64 : 128); c += 8) {
+                    float o[8];
 #pragma unroll
-                        for (int c = 0; c < CH; c += 4) {
-                            float2 f0, f1;
-                            if (ROWS_X) {
-                                f0 = f1 = s ? make_float2(g, g) : make_float2(f, f);
-                            } else {
-                                const float4 t = *reinterpret_cast<const float4*>(table + (i * SETS + s) * HC + c0 + c);
-                                f0 = make_float2(t.x, t.y), f1 = make_float2(t.z, t.w);
-                            }
-                            float2* to = &acc[s][(c0 + c) / 2];
-                            to[0] = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f0, to[0]);
-                            to[1] = fma2(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), f1, to[1]);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 x = acc[(c + i) / 2];
+                        o[i] = i & 1 ? x.y : x.x;
+                        if (GLU) {
+                            const float2 u = acc[32 + ((c + i) / 2) % 32];
+                            o[i] = silu_f32(o[i]) * (i & 1 ? u.y : u.x);
                         }
                     }
-            }
-            if (p.kb0 == 0 && p.kb1 == KB) {
-                write(p);
-                continue;
-            }
-            // ---- a part of a tile; the CTA that arrives last adds them in their order ----
-            const long long t0 = p.tile * KB;
-            const int from = owner_of(t0), to = owner_of(t0 + KB - 1);
-            {
-                float* part = parts + (size_t)(2 * blockIdx.x + (p.kb0 == 0)) * S::PART;
-#pragma unroll
-                for (int s = 0; s < SETS; ++s)
-#pragma unroll
-                    for (int c = 0; c < HC; ++c)
-                        part[(s * BN + half * HC + c) * 128 + r] = c & 1 ? acc[s][c / 2].y : acc[s][c / 2].x;
-            }
-            __threadfence();
-            bar_adders();
-            if (tid == 64) {
-                const uint32_t n = to - from;
-                sh_last = atomicInc(static_cast<uint32_t*>(a.workspace) + from, n) == n;  // back to 0 behind the last
-                __threadfence();
-            }
-            bar_adders();
-            if (sh_last) {
-#pragma unroll
-                for (int s = 0; s < SETS; ++s)
-#pragma unroll
-                    for (int c = 0; c < HC / 2; ++c) acc[s][c] = make_float2(0.f, 0.f);
-                for (int i = from; i <= to; ++i) {
-                    const float* part = parts + (size_t)(2 * i + (i == from)) * S::PART;
-#pragma unroll
-                    for (int s = 0; s < SETS; ++s)
-#pragma unroll
-                        for (int c = 0; c < HC; ++c) {
-                            const float v = __ldcg(part + (s * BN + half * HC + c) * 128 + r);
-                            if (c & 1)
-                                acc[s][c / 2].y += v;
-                            else
-                                acc[s][c / 2].x += v;
-                        }
+                    const int off = c >= 64 ? 64 + c : c;
+                    put8(a, to + off, o, a.N - n0 - off, wide);
                 }
-                write(p);
             }
-            bar_adders();  // sh_last is read
+        }
+    }
+    if (split > 1) {
+        // ---- the pairs' sums in their order, each CTA a share of the columns of its rows ----
+        fence_before();
+        cluster_sync();
+        fence_after();
+        if (warp >= 4) {
+            const int m0 = tile_m0(first), rows = min(128, a.M - m0), n0 = tile_n(first) * OUT;
+            const int g0 = OUT / 8 * (int)(crank / 2) / split, groups = OUT / 8 * (int)(crank / 2 + 1) / split - g0;  // of 8 columns
+            const bool wide = a.N % 8 == 0;
+            for (int e = tid - 128; e < rows * groups; e += kAdders * 32) {
+                const int row = e / groups, c = (g0 + e % groups) * 8;
+                float o[2][8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[0][i] = o[1][i] = 0.f;
+                const uint32_t at = smem_at(reinterpret_cast<float*>(smem) + row * kPitch + c);
+                for (int q = 0; q < split; ++q) {
+                    uint32_t from;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(2 * q + rank));
+#pragma unroll
+                    for (int u = 0; u < (GLU ? 4 : 2); ++u) {
+                        float4 x;
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(from + (u & 1) * 16 + (u >> 1) * 512) : "memory");
+                        float* to = &o[u >> 1][(u & 1) * 4];
+                        to[0] += x.x, to[1] += x.y, to[2] += x.z, to[3] += x.w;
+                    }
+                }
+                if (GLU)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[0][i] = silu_f32(o[0][i]) * o[1][i];
+                put8(a, (int64_t)(m0 + row) * a.N + n0 + c, o[0], a.N - n0 - c, wide);
+            }
         }
     }
     fence_before();
     __syncthreads();
+    cluster_sync();  // all CTAs are done with each other's memory, barriers and copies, and the pair with its TMEM
     fence_after();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::COLS));
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ------------------------------------------------------------ host side ----
@@ -470,52 +500,74 @@ bool encode(CUtensorMap* map, const uint8_t* base, int64_t K, int64_t rows, int 
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool ROWS_X, int BN, bool GLU>
-cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
-    using S = Shape<ROWS_X, BN, GLU>;
-    CUtensorMap mx, mw, mu;
-    if (!encode(&mx, a.X, a.K, a.M, ROWS_X ? 128 : BN) || !encode(&mw, a.W, a.K, a.N, ROWS_X ? BN : 128) ||
-        !encode(&mu, GLU ? a.U : a.W, a.K, a.N, ROWS_X ? BN : 128))
-        return cudaErrorInvalidValue;
-    auto* fn = gemm_fp8_kernel<ROWS_X, BN, GLU>;
-    const cudaError_t err = kv4_allow_smem((const void*)fn, S::SMEM);
-    if (err != cudaSuccess) return err;
-    const int64_t tiles = ROWS_X ? ((a.M + 127) / 128) * (((int64_t)a.N + BN - 1) / BN) : (((int64_t)a.M + BN - 1) / BN) * ((a.N + 127) / 128);
-    const int sms = device_sm_count() < kCounters ? device_sm_count() : kCounters;
-    const size_t need = kCounters * sizeof(uint32_t) + (size_t)2 * sms * S::PART * sizeof(float);
-    int split = !ROWS_X && a.ws_bytes >= need ? 1 : 0;
-    const int64_t most = split ? tiles * (a.K / 128) : tiles;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = S::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attrs[1];
-    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attrs;
-    cfg.numAttrs = 1;
-    count_launch();
-    return cudaLaunchKernelEx(&cfg, fn, mx, mw, mu, a, (const int)split);
-}
+// A tile's k is cut between pairs of a cluster where that leaves fewer blocks of k in a row: in blocks, of 0.4 us, what the
+// start of a CTA and what the join of a cluster take.
+constexpr int kMaxSplit = 4, kStart = 8, kJoin = 8;
 
 template <bool GLU>
 cudaError_t launch_for(const Fp8Args& a, cudaStream_t s) {
-    if (a.M <= 16) return launch<false, 16, GLU>(a, s);
-    if (a.M <= 32) return launch<false, 32, GLU>(a, s);
-    if (a.M <= 64) return launch<false, 64, GLU>(a, s);
-    if (a.M <= 128) return launch<false, 128, GLU>(a, s);
-    return launch<true, 128, GLU>(a, s);
+    CUtensorMap mx, mw, mu;
+    if (!encode(&mx, a.X, a.K, a.M, 128) || !encode(&mw, a.W, a.K, a.N, 128) || !encode(&mu, GLU ? a.U : a.W, a.K, a.N, 128))
+        return cudaErrorInvalidValue;
+    auto* fn = gemm_fp8_kernel<GLU>;
+    const cudaError_t err = kv4_allow_smem((const void*)fn, kSmem);
+    if (err != cudaSuccess) return err;
+    static std::atomic<int> regs{0};
+    if (!regs.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes attr;
+        const cudaError_t e = cudaFuncGetAttributes(&attr, fn);
+        if (e != cudaSuccess) return e;
+        regs.store(attr.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return cudaErrorLaunchOutOfResources;  // the split would wait forever
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attrs;
+    // Clusters of 1 to 4 pairs that the device holds at once, asked for once per device.
+    static std::atomic<int> known[16][kMaxSplit];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256)), KB = a.K / 128;
+    int split = 1, held = 1;
+    int64_t best = INT64_MAX;
+    for (int n = 1; n <= kMaxSplit && n <= KB; ++n) {
+        int h = dev < 16 ? known[dev][n - 1].load(std::memory_order_relaxed) : 0;
+        if (!h) {
+            attrs[0].val.clusterDim.x = 2 * n;
+            cfg.gridDim = dim3(2 * n, 1, 1);
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&h, fn, &cfg);
+            if (e != cudaSuccess) return e;
+            if (h < 1) h = 1;
+            if (dev < 16) known[dev][n - 1].store(h, std::memory_order_relaxed);
+        }
+        const int64_t waves = (tiles + h - 1) / h, blocks = (KB + n - 1) / n;
+        const int64_t cost = n == 1 ? waves * blocks + kStart : waves * (blocks + kStart) + kJoin;
+        if (cost < best) best = cost, split = n, held = h;
+    }
+    const int64_t clusters = split > 1 || tiles < held ? tiles : held;
+    attrs[0].val.clusterDim.x = 2 * split;
+    cfg.gridDim = dim3((unsigned)(2 * split * clusters), 1, 1);
+    cfg.numAttrs = 2;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, fn, mx, mw, mu, a);
 }
 
 }  // namespace
 
-size_t gemm_fp8_workspace() {
-    const int sms = device_sm_count() < kCounters ? device_sm_count() : kCounters;
-    return kCounters * sizeof(uint32_t) + (size_t)2 * sms * Shape<false, 128, true>::PART * sizeof(float);
+cudaError_t launch_gemm_fp8(const Fp8Args& a, cudaStream_t s) {
+    // Up to 16 rows as a stream of W on mma.sync: 16 rows, 3584 x 18944: 19.6 us against 24.2 (one row, 2048 x 2048: 2.6, 7.0).
+    if (a.M <= 16) return launch_gemv_fp8(a, s);
+    return a.U ? launch_for<true>(a, s) : launch_for<false>(a, s);
 }
-
-cudaError_t launch_gemm_fp8(const Fp8Args& a, cudaStream_t s) { return a.U ? launch_for<true>(a, s) : launch_for<false>(a, s); }
 
 int gemm_fp8_take_fault() {
     int v = 0, z = 0;

@@ -250,11 +250,9 @@ struct Fp8Args {
     const uint16_t* residual;  // bf16 [M][N] or NULL; may be y
     int M, N, K;
     int out_f32;
-    void* workspace;
-    size_t ws_bytes;
 };
 cudaError_t launch_gemm_fp8(const Fp8Args& a, cudaStream_t s);
-size_t gemm_fp8_workspace();
+cudaError_t launch_gemv_fp8(const Fp8Args& a, cudaStream_t s);  // up to 16 rows
 int gemm_fp8_take_fault();
 cudaError_t launch_quantize_fp8_rows(const uint16_t* X, int64_t stride, uint8_t* Q, float* S, int64_t M, int64_t K, const uint16_t* norm_w,
                                      double eps, cudaStream_t s);

@@ -83,27 +83,19 @@ SIZES = [(1, 1, 128), (1, 2048, 2048), (2, 7, 256), (3, 128, 128), (5, 129, 640)
          (130, 1, 512), (200, 1031, 768), (256, 256, 256), (257, 4608, 3584), (500, 127, 2560), (777, 640, 1408), (1025, 385, 128)]
 
 
-@pytest.fixture(scope="module")
-def ws():
-    return mbw.gemm_fp8_workspace()
-
-
 @pytest.mark.parametrize("m,n,k", SIZES)
-def test_product(ws, m, n, k):
+def test_product(m, n, k):
     x, xs, w, sc = operands(gen(m * 7 + n + k), m, n, k)
     y, mass, eps = exact(x, xs, w, sc)
-    got = mbw.gemm_fp8_b128(x, xs, w, sc, workspace=ws)
+    got = mbw.gemm_fp8_b128(x, xs, w, sc)
     check(got, y, mass * eps + half_step(y), "bf16")
-    assert torch.equal(mbw.gemm_fp8_b128(x, xs, w, sc, workspace=ws), got)  # the same again, and the workspace is as it was
-    alone = mbw.gemm_fp8_b128(x, xs, w, sc)
-    check(alone, y, mass * eps + half_step(y), "no workspace")
+    assert torch.equal(mbw.gemm_fp8_b128(x, xs, w, sc, workspace=torch.empty(64, device="cuda")), got)  # the same again
     with mbw.output_fp32():
-        check(mbw.gemm_fp8_b128(x, xs, w, sc, workspace=ws), y, mass * eps + 2.0 ** -149, "fp32")
-    assert not ws[:4096].any()
+        check(mbw.gemm_fp8_b128(x, xs, w, sc), y, mass * eps + 2.0 ** -149, "fp32")
 
 
 @pytest.mark.parametrize("m,n,k", SIZES[::2] + [(40, 5632, 2048)])
-def test_gated_product_with_a_residual(ws, m, n, k):
+def test_gated_product_with_a_residual(m, n, k):
     g = gen(m + 3 * n + k)
     x, xs, w, sc = operands(g, m, n, k)
     _, _, u, su = operands(g, 1, n, k)
@@ -116,28 +108,28 @@ def test_gated_product_with_a_residual(ws, m, n, k):
     tol = 1.1 * mass_a * eps * b.abs() + act.abs() * mass_b * eps + 1.1 * mass_a * mass_b * eps * eps
     tol = tol + (act * b).abs() * 2.0 ** -20 + r.double().abs() * 2.0 ** -23
     want = act * b + r.double()
-    got = mbw.gemm_fp8_b128(x, xs, w, sc, residual=r, up_weights=u, up_scales=su, workspace=ws)
+    got = mbw.gemm_fp8_b128(x, xs, w, sc, residual=r, up_weights=u, up_scales=su)
     check(got, want, tol + half_step(want), "gated, residual")
     check(mbw.gemm_fp8_b128(x, xs, w, sc, up_weights=u, up_scales=su), act * b, tol + half_step(act * b), "gated")
     # the residual may be the output
     y, mass, eps = exact(x, xs, w, sc)
     out = r.clone()
-    assert mbw.gemm_fp8_b128(x, xs, w, sc, out=out, residual=out, workspace=ws) is out
+    assert mbw.gemm_fp8_b128(x, xs, w, sc, out=out, residual=out) is out
     want = y + r.double()
     check(out, want, mass * eps + want.abs() * 2.0 ** -24 + half_step(want), "in place")
 
 
-def test_no_rows_or_no_outputs(ws):
+def test_no_rows_or_no_outputs():
     x, xs, w, sc = operands(gen(1), 4, 130, 256)
-    assert mbw.gemm_fp8_b128(x[:0], xs[:0], w, sc, workspace=ws).shape == (0, 130)
-    assert mbw.gemm_fp8_b128(x, xs, w[:0], sc[:0], workspace=ws).shape == (4, 0)
+    assert mbw.gemm_fp8_b128(x[:0], xs[:0], w, sc).shape == (0, 130)
+    assert mbw.gemm_fp8_b128(x, xs, w[:0], sc[:0]).shape == (4, 0)
     assert mbw.quantize_fp8_g128(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"))[0].shape == (0, 256)
     assert mbw.quantize_fp8_b128(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"))[1].shape == (0, 2)
     assert mbw.dequant_fp8_g128(x[:0], xs[:0]).shape == (0, 256)
 
 
 @pytest.mark.parametrize("m", [1, 20, 300])
-def test_codes_of_every_kind_and_scales_far_apart(ws, m):
+def test_codes_of_every_kind_and_scales_far_apart(m):
     """All finite codes, among them the subnormal ones, with scales over many powers of two whose products cancel."""
     g = gen(m)
     n, k = 260, 640
@@ -147,7 +139,7 @@ def test_codes_of_every_kind_and_scales_far_apart(ws, m):
     xs = torch.exp2(torch.randint(-40, 40, (m, k // 128), generator=g, device="cuda").float()) * 1.1
     sc = torch.exp2(torch.randint(-40, 40, (3, k // 128), generator=g, device="cuda").float()) * 1.3
     y, mass, eps = exact(x, xs, w, sc)
-    check(mbw.gemm_fp8_b128(x, xs, w, sc, workspace=ws), y, mass * eps + half_step(y))
+    check(mbw.gemm_fp8_b128(x, xs, w, sc), y, mass * eps + half_step(y))
     # within a block: large terms that cancel, and a small one that remains
     x = torch.zeros(m, 128, device="cuda")
     x[:, 0], x[:, 77], x[:, 100] = 448.0, 448.0, 2.0 ** -9
@@ -155,11 +147,11 @@ def test_codes_of_every_kind_and_scales_far_apart(ws, m):
     w[:, 0], w[:, 77], w[:, 100] = 448.0, -448.0, 1.0
     one = torch.ones(m, 1, device="cuda"), torch.ones(3, 1, device="cuda")
     y, mass, eps = exact(x.to(E4M3), one[0], w.to(E4M3), one[1])
-    check(mbw.gemm_fp8_b128(x.to(E4M3), one[0], w.to(E4M3), one[1], workspace=ws), y, mass * eps + half_step(y), "cancelling")
+    check(mbw.gemm_fp8_b128(x.to(E4M3), one[0], w.to(E4M3), one[1]), y, mass * eps + half_step(y), "cancelling")
 
 
 @pytest.mark.parametrize("m,n", [(3, 300), (100, 300), (300, 500)])
-def test_what_is_no_number_stays_in_its_row_and_column(ws, m, n):
+def test_what_is_no_number_stays_in_its_row_and_column(m, n):
     k = 512
     x, xs, w, sc = operands(gen(m), m, n, k)
     y, mass, eps = exact(x, xs, w, sc)
@@ -169,7 +161,7 @@ def test_what_is_no_number_stays_in_its_row_and_column(ws, m, n):
     xs2[0, 3] = float("inf")
     wbits = w.view(torch.uint8).clone()
     wbits[n - 1, 5] = 0xFF
-    got = mbw.gemm_fp8_b128(bits.view(E4M3), xs2, wbits.view(E4M3), sc, workspace=ws)
+    got = mbw.gemm_fp8_b128(bits.view(E4M3), xs2, wbits.view(E4M3), sc)
     assert got[1].isnan().all() and got[:, n - 1].isnan().all()
     assert not got[0, :n - 1].isfinite().any()
     check(got[2:, :n - 1], y[2:, :n - 1], (mass * eps + half_step(y))[2:, :n - 1])
@@ -184,13 +176,13 @@ def test_rows_do_not_depend_on_the_rows_beside_them():
         assert torch.equal(whole[:b], part)
 
 
-def test_rows_behind_the_last_are_left_as_they_were(ws):
+def test_rows_behind_the_last_are_left_as_they_were():
     """The output is part of a larger buffer; so are the operands, which end where the buffer does."""
     for m, n in ((3, 200), (70, 333), (200, 385)):
         x, xs, w, sc = operands(gen(m), m, n, 384)
         big = torch.full((m * n + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
         out = big[:m * n].view(m, n)
-        mbw.gemm_fp8_b128(x, xs, w, sc, out=out, workspace=ws)
+        mbw.gemm_fp8_b128(x, xs, w, sc, out=out)
         assert big[m * n:].eq(7).all()
         y, mass, eps = exact(x, xs, w, sc)
         check(out, y, mass * eps + half_step(y))
@@ -199,31 +191,30 @@ def test_rows_behind_the_last_are_left_as_they_were(ws):
 def test_captured_and_on_two_streams():
     sizes = [(1, 2048, 2048), (50, 700, 1152), (300, 1000, 512)]
     data = [operands(gen(i), *s) for i, s in enumerate(sizes)]
-    spaces = [mbw.gemm_fp8_workspace() for _ in range(2)]
-    want = [[mbw.gemm_fp8_b128(*d, workspace=spaces[0]) for d in data] for _ in range(2)]
+    want = [[mbw.gemm_fp8_b128(*d) for d in data] for _ in range(2)]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
     got = [[], []]
     for _ in range(5):
         for i, s in enumerate(streams):
             with torch.cuda.stream(s):
-                got[i] = [mbw.gemm_fp8_b128(*d, workspace=spaces[i]) for d in data]
+                got[i] = [mbw.gemm_fp8_b128(*d) for d in data]
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
     g = torch.cuda.CUDAGraph()
     h = torch.randn(50, 1152, device="cuda").bfloat16()
     with torch.cuda.graph(g):
-        outs = [mbw.gemm_fp8_b128(*d, workspace=spaces[0]) for d in data]
+        outs = [mbw.gemm_fp8_b128(*d) for d in data]
         q, qs = mbw.quantize_fp8_g128(h)
-        chain = mbw.gemm_fp8_b128(q, qs, data[1][2], data[1][3], workspace=spaces[0])
+        chain = mbw.gemm_fp8_b128(q, qs, data[1][2], data[1][3])
     for _ in range(3):
         h.copy_(torch.randn(50, 1152, device="cuda"))
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want[0]))
         x, xs = plain_rows(h)
-        assert torch.equal(chain, mbw.gemm_fp8_b128(x, xs, data[1][2], data[1][3], workspace=spaces[1]))
+        assert torch.equal(chain, mbw.gemm_fp8_b128(x, xs, data[1][2], data[1][3]))
 
 
 # ------------------------------------------------------------ quantization ----
@@ -300,7 +291,7 @@ def test_norm_of_awkward_rows():
         assert same(s, scale) and same(q, want)
 
 
-def test_weights_are_there_for_a_product_queued_behind_them(ws):
+def test_weights_are_there_for_a_product_queued_behind_them():
     """A product reads weights before it waits for the kernel in front of it; the quantizer ends so that it may."""
     g = gen(9)
     x, xs, _, _ = operands(g, 8, 4, 2048)
@@ -308,6 +299,6 @@ def test_weights_are_there_for_a_product_queued_behind_them(ws):
     torch.cuda.synchronize()
     for w in mats * 3:
         q, s = mbw.quantize_fp8_b128(w)
-        got = mbw.gemm_fp8_b128(x, xs, q, s, workspace=ws)
+        got = mbw.gemm_fp8_b128(x, xs, q, s)
         y, mass, eps = exact(x, xs, *plain_blocks(w))
         check(got, y, mass * eps + half_step(y))

@@ -190,7 +190,6 @@ def test_host_tensors_are_refused():
 
 
 def test_workspaces(L):
-    assert L.mbw_gemm_fp8_b128_workspace_bytes() > 0
     for args in ((96, 4, 4), (128, -1, 4), (128, 4, 0), (128, 1 << 31, 1), (128, 1 << 20, 1 << 16)):
         assert L.mbw_kv4_attention_shared_workspace_bytes(*args) == 0
     for d in (64, 128, 256):
