@@ -306,6 +306,11 @@ struct Kv4AttnArgs {
     int out_f32;
     void* workspace;
     size_t ws_bytes;
+    // Requests that share their first shared_len tokens (whole pages): attention over these, normalized, and its log2 of the
+    // sum of the powers of two, which the kernel of the other tokens joins to its own.
+    int shared_len;
+    float* shared_out;  // fp32 [T][q_heads][head_dim]
+    float* shared_lse;  // fp32 [T][q_heads]
 };
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
@@ -315,6 +320,7 @@ size_t kv4_attention_workspace(int head_dim);
 cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int shared_len, cudaStream_t s);
 size_t kv4_attention_shared_workspace(int head_dim, int64_t T, int64_t q_heads);
 cudaError_t launch_kv4_attention_tc(const Kv4AttnArgs& a, cudaStream_t s);  // head dimensions 64 and 128
+cudaError_t launch_kv4_attention_prefix(const Kv4AttnArgs& a, cudaStream_t s);  // the shared tokens alone, into shared_out and shared_lse
 size_t kv4_attention_tc_workspace(int head_dim);
 cudaError_t kv4_allow_smem(const void* kernel, int bytes);  // its dynamic shared memory, once per kernel and device
 int kv4_attn_tc_take(bool fault);  // its range flag, or its flag of an expired wait; cleared

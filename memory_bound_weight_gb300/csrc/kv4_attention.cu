@@ -162,7 +162,9 @@ struct Shape {
 // The workspace begins with a counter of finished parts per worker; an item cut between workers has that of its first.
 constexpr int kCounters = 4096;
 
-template <int D, int G, int NT, int NW, int NB, int DEPTH, int OCC, bool COOP>
+// SHARED: the first shared_len tokens' part is there already (kv4_attention_tc.cu); the items are those of the others, and what
+// they give is joined to it as it is stored.
+template <int D, int G, int NT, int NW, int NB, int DEPTH, int OCC, bool COOP, bool SHARED>
 __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs a, int split, int shift) {
     using S = Shape<D, G, NT, NW, NB, DEPTH, COOP>;
     constexpr int NG = S::NG, J = S::J, BB = S::BB, ROWS = S::ROWS, THREADS = NW * 32, NV = D / 64;
@@ -211,7 +213,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
         Request r;
         r.q0 = q0, r.nq = nq, r.ctx = ctx;
         r.fb = kv4_first_seen(ctx - nq, a.window) / 16;
-        r.units = max(1u, ((uint32_t)((ctx + 15) / 16 - r.fb) + unit - 1) / unit);
+        if (SHARED) r.fb = max(r.fb, a.shared_len / 16);
+        r.units = max(1u, ((uint32_t)(SHARED ? max((ctx + 15) / 16 - r.fb, 0) : (ctx + 15) / 16 - r.fb) + unit - 1) / unit);
         r.qt = ((uint32_t)nq * gq + ROWS - 1) / ROWS;  // at most MBW_MAX_DIM query rows
         r.tiles = (uint32_t)r.qt * a.kv_heads;
         return r;
@@ -346,6 +349,19 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 
     float o[NT][D / 16][4], z[RAW ? NG : 1][4], r[NT][NG][2], M[NT][2], L[NT][2];
 
+    // SHARED: of a row's maximum and sum here (of 4 p) and its shared part, the factors of their outputs, and their sum's log2.
+    struct Joint {
+        float own, shared, lse;
+    };
+    auto joint = [&](long long at, float m, float l) {
+        const float x = l == 0.f ? -CUDART_INF_F : m + log2f(l) - 2.f, y = __ldcg(a.shared_lse + at), top = fmaxf(x, y);
+        const float ex = x == -CUDART_INF_F ? 0.f : exp2_fast(x - top), ey = y == -CUDART_INF_F ? 0.f : exp2_fast(y - top), sum = ex + ey;
+        Joint j;
+        j.own = l == 0.f ? 0.f : ex / (sum * l);
+        j.shared = sum == 0.f ? 0.f : ey / sum;
+        j.lse = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718055994530942f;
+        return j;
+    };
     // Outputs of rows f0 .. f0 + ROWS - 1 from the sums in o, by one warp.
     auto store = [&](int q0, int nq, int hh, int f0) {
 #pragma unroll
@@ -358,7 +374,18 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                 if (f >= nq * gq) continue;
                 const long long row = q0 + qi;
                 const int head = hh * gq + f - qi * gq;
-                if (a.lse && g == 0)
+                if constexpr (SHARED) {
+                    const long long at = row * a.q_heads + head;
+                    const Joint j = joint(at, M[nt][e], L[nt][e]);
+                    inv[e] = 1.f;
+                    if (a.lse && g == 0) a.lse[at] = j.lse;
+                    const float* from = a.shared_out + at * D + g;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        o[nt][i][e] = fmaf(o[nt][i][e], j.own, __ldcg(from + 16 * i) * j.shared);
+                        o[nt][i][2 + e] = fmaf(o[nt][i][2 + e], j.own, __ldcg(from + 16 * i + 8) * j.shared);
+                    }
+                } else if (a.lse && g == 0)
                     a.lse[row * a.q_heads + head] =
                         L[nt][e] == 0.f ? -CUDART_INF_F : (M[nt][e] + log2f(L[nt][e]) - 2.f) * 0.69314718055994530942f;
                 if (a.out_f32) {
@@ -511,6 +538,15 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                 const long long row = p.q0 + qi;
                 const int head = p.h * gq + f - qi * gq, d = 16 * (tile % (D / 16)) + (ln >> 2);
                 const long long to = row * a.out_stride + (long long)head * D + d;
+                if constexpr (SHARED) {
+                    const long long at = row * a.q_heads + head;
+                    const Joint j = joint(at, m, l);
+                    const float* from = a.shared_out + at * D + d;
+                    store_out(a.out, to, fmaf(e ? x.s.y : x.s.x, j.own, __ldcg(from) * j.shared), a.out_f32);
+                    store_out(a.out, to + 8, fmaf(e ? x.s.w : x.s.z, j.own, __ldcg(from + 8) * j.shared), a.out_f32);
+                    if (a.lse && d == 0) a.lse[at] = j.lse;
+                    continue;
+                }
                 store_out(a.out, to, (e ? x.s.y : x.s.x) * inv, a.out_f32);
                 store_out(a.out, to + 8, (e ? x.s.w : x.s.z) * inv, a.out_f32);
                 if (a.lse && d == 0)
@@ -1086,11 +1122,11 @@ struct Entry {
     int threads, smem, occ, rows, part, workers, step;
 };
 
-template <int D, int G, int NT, int NW, int NB, int DEPTH, int OCC, bool COOP>
+template <int D, int G, int NT, int NW, int NB, int DEPTH, int OCC, bool COOP, bool SHARED = false>
 Entry entry() {
     using S = Shape<D, G, NT, NW, NB, DEPTH, COOP>;
     static_assert(S::SMEM * OCC <= 225 * 1024, "shared memory of the CTAs of an SM");
-    return {(const void*)kv4_attention_kernel<D, G, NT, NW, NB, DEPTH, OCC, COOP>, NW * 32, S::SMEM, OCC, S::ROWS, S::PART,
+    return {(const void*)kv4_attention_kernel<D, G, NT, NW, NB, DEPTH, OCC, COOP, SHARED>, NW * 32, S::SMEM, OCC, S::ROWS, S::PART,
             S::WORKERS, S::STEP};
 }
 
@@ -1116,7 +1152,17 @@ Entry pick(int rows, bool few) {
     }
 }
 
-Entry pick_for(int head_dim, int group, int rows, bool few) {
+// Of the requests' own tokens behind shared ones: few rows, and at most 128 dimensions.
+template <int D, int G>
+Entry pick_shared(bool few) {
+    return few ? entry<D, G, 1, 16, 2, D == 64 ? 4 : 2, 1, true, true>() : entry<D, G, 1, 4, 2, D == 64 ? 4 : 3, D == 64 ? 4 : 3, false, true>();
+}
+
+Entry pick_for(int head_dim, int group, int rows, bool few, bool shared = false) {
+    if (shared) {
+        if (group == 32) return head_dim == 64 ? pick_shared<64, 32>(few) : pick_shared<128, 32>(few);
+        return head_dim == 64 ? pick_shared<64, 64>(few) : pick_shared<128, 64>(few);
+    }
     if (group == 32)
         return head_dim == 64 ? pick<64, 32>(rows, few) : head_dim == 128 ? pick<128, 32>(rows, few) : pick<256, 32>(rows, few);
     return head_dim == 64 ? pick<64, 64>(rows, few) : head_dim == 128 ? pick<128, 64>(rows, few) : pick<256, 64>(rows, few);
@@ -1185,7 +1231,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     // CTAs as workers cut whole items among them, so there have to be more CTAs than items by enough (12 requests of 8
     // KV heads and 32768 tokens, 96 items: 123 us against 92 with warps; 64 items: 68 against 69; 8: 19.5 against 84).
     const bool few = 2 * items <= sms && most_items <= kItemsPerCta * sms;
-    const Entry e = pick_for(a.head_dim, a.group, (int)(rows < kWideRows ? rows : kWideRows), few);
+    const Entry e = pick_for(a.head_dim, a.group, (int)(rows < kWideRows ? rows : kWideRows), few, a.shared_len > 0);
     if (e.smem > 48 * 1024) {
         const cudaError_t err = kv4_allow_smem(e.fn, e.smem);
         if (err != cudaSuccess) return err;
@@ -1217,9 +1263,24 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
     return cudaLaunchKernelExC(&cfg, e.fn, params);
 }
 
-size_t kv4_attention_shared_workspace(int head_dim, int64_t, int64_t) { return kv4_attention_workspace(head_dim); }
+// Behind the plain call's workspace, the shared part's outputs and log sums of all rows.
+size_t kv4_attention_shared_workspace(int head_dim, int64_t T, int64_t q_heads) {
+    const size_t plain = (kv4_attention_workspace(head_dim) + 15) / 16 * 16;
+    return head_dim == 256 ? plain : plain + (size_t)(T * q_heads) * (head_dim + 1) * sizeof(float);
+}
 
-cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int, cudaStream_t s) { return launch_kv4_attention(a, s); }
+cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int shared_len, cudaStream_t s) {
+    const int64_t gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
+    if (a.head_dim == 256 || rows >= kWideRows || a.ws_bytes < kv4_attention_shared_workspace(a.head_dim, a.T, a.q_heads)) return launch_kv4_attention(a, s);
+    const size_t plain = (kv4_attention_workspace(a.head_dim) + 15) / 16 * 16;
+    Kv4AttnArgs b = a;
+    b.ws_bytes = plain;
+    b.shared_len = shared_len;
+    b.shared_out = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + plain);
+    b.shared_lse = b.shared_out + (size_t)a.T * a.q_heads * a.head_dim;
+    const cudaError_t e = launch_kv4_attention_prefix(b, s);
+    return e == cudaSuccess ? launch_kv4_attention(b, s) : e;
+}
 
 int kv4_attn_take_range() {
     int v = 0, z = 0;

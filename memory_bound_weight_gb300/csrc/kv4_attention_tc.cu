@@ -265,6 +265,7 @@ static_assert(kSoftmax * kRegsSoftmax + 2 * kUnpack * kRegsUnpack + 4 * kRegsIss
 constexpr int kCounters = 4096;  // of items cut between CTAs, as the other kernel's: both leave them at zero
 constexpr int kUp = 7;           // weights are 2^kUp p
 constexpr int kPieces = 8;       // of an item: the CTA that joins them reads 64 KB a piece, some 0.5 us
+constexpr int kSharedPieces = 16;
 constexpr float kGrow = 8.f;     // growth of the maximum, in powers of two, that is let pass
 
 // All warps but those that have nothing to do.
@@ -283,7 +284,9 @@ struct Layout {
     static constexpr int PART = kRows * (D + 2);                      // floats of a part: [row][column], then maxima and sums of the rows
 };
 
-template <int D, int G>
+// SHARED: the items are those of one request, of all the call's queries, whose keys are the shared tokens; a row's position
+// is that of its query in its own request. (The items of different requests have their rows in one tile then.)
+template <int D, int G, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnArgs a, int slots) {
     using L = Layout<D>;
     constexpr int NG = D / G, KS = D / 16;  // groups; steps of 16 in Q K, the offsets' one not counted
@@ -362,11 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     // Offsets that fall make ranges that overlap: then there is no work, as in kv4_attention.cu. Looked for once, at the start.
     auto offsets_fall = [&](int b) { return a.q_starts && a.q_starts[b + 1] < a.q_starts[b]; };
     // Up to 32 requests are a lane's each, and every warp finds its items by itself; more are shared out over the threads.
-    const bool lanes = a.B <= 32;
+    const bool lanes = !SHARED && a.B <= 32;
+    struct Batch {  // SHARED: of the requests that have queries and tokens, the first and last query's position, and the longest
+        int lo, hi, b, keys;  // with its shared tokens
+    };
+    __shared__ Batch sh_batch;
     const int stride = (a.B + kThreads - 1) / kThreads;  // requests per thread
     uint32_t W = 0;
     float per_unit = 0.f;
-    auto pieces_of = [&](const Request& r) { return min((uint32_t)min(max(1, r.units / 2), kPieces), max(1u, (uint32_t)((float)r.units * per_unit))); };
+    auto pieces_of = [&](const Request& r) { return min((uint32_t)min(max(1, r.units / 2), SHARED ? kSharedPieces : kPieces), max(1u, (uint32_t)((float)r.units * per_unit))); };
     auto set_per_unit = [&](float units, uint32_t items) {
         per_unit = 2 * items <= (uint32_t)gridDim.x && items + gridDim.x <= (uint32_t)slots ? (float)gridDim.x / (units * a.kv_heads) : 0.f;
     };
@@ -378,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         }
         return n;
     };
-    if (!lanes) {
+    if (!SHARED && !lanes) {
         float units = 0.f;
         uint32_t items = 0, n = 0;
         bool falls = false;
@@ -427,7 +434,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         Item it;
         Request r;
         uint32_t base;
-        if (lanes) {
+        int b0, b1;
+        if constexpr (SHARED) {
+            const Batch all = sh_batch;
+            b0 = kv4_first_seen(all.lo, a.window) / 16, b1 = (all.keys + 15) / 16;
+            r = sized(0, a.T, 0);
+            r.units = max(0, b1 - b0 + 7) / 8;
+            const uint32_t items = (uint32_t)r.tiles * a.kv_heads;
+            set_per_unit((float)r.tiles * (float)max(1, r.units), items);
+            W = items * pieces_of(r);
+            it.n = -1, it.b = all.b, base = 0;
+            if (place >= W) return it;
+        } else if (lanes) {
             Request mine = {0, 0, 0, 0, 0};
             if (lane < a.B) mine = request(lane);
             set_per_unit(warp_sum((float)mine.tiles * (float)mine.units), __reduce_add_sync(0xFFFFFFFFu, (uint32_t)mine.tiles) * a.kv_heads);
@@ -465,9 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         it.h = (int)(at / (uint32_t)r.tiles);
         it.f0 = (r.tiles - 1 - (int)(at - (uint32_t)it.h * r.tiles)) * kRows;  // those of most keys first
         it.q0 = r.q0, it.nq = r.nq, it.ctx = r.ctx;
-        it.pos_lo = r.ctx - r.nq + it.f0 / gq;
-        it.pos_hi = r.ctx - r.nq + min(r.nq - 1, (it.f0 + kRows - 1) / gq);
-        const int b0 = kv4_first_seen(it.pos_lo, a.window) / 16, b1 = max(it.pos_hi + 16, 0) / 16;
+        if constexpr (SHARED) {
+            it.pos_hi = sh_batch.keys - 1, it.pos_lo = min(sh_batch.lo, it.pos_hi);  // keys past pos_hi are not the item's
+        } else {
+            it.pos_lo = r.ctx - r.nq + it.f0 / gq;
+            it.pos_hi = r.ctx - r.nq + min(r.nq - 1, (it.f0 + kRows - 1) / gq);
+            b0 = kv4_first_seen(it.pos_lo, a.window) / 16, b1 = max(it.pos_hi + 16, 0) / 16;
+        }
         const int total = max(0, b1 - b0 + 7) / 8;
         const int each = total / (int)it.pieces, rest = total - each * (int)it.pieces, p = (int)it.piece;
         it.bs = b0 + (p * each + min(p, rest)) * 8;
@@ -481,7 +503,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     __shared__ int sh_cut, sh_last[2];
     __shared__ float sh_per_unit;
     if (warp == kIssuer) {
+        bool falls = false;
+        if constexpr (SHARED) {
+            Batch all = {0x7FFFFFFF, -1, 0, 0};
+            for (int b = lane; b < a.B; b += 32) {
+                const Request r = request(b);
+                falls |= offsets_fall(b);
+                if (r.nq == 0 || r.ctx == 0) continue;
+                all.lo = min(all.lo, r.ctx - r.nq), all.hi = max(all.hi, r.ctx - 1);
+                if (r.ctx > all.keys) all.keys = r.ctx, all.b = b;
+            }
+            const int keys = __reduce_max_sync(0xFFFFFFFFu, all.keys);
+            all.b = __reduce_min_sync(0xFFFFFFFFu, all.keys == keys ? all.b : 0x7FFFFFFF);
+            all.lo = __reduce_min_sync(0xFFFFFFFFu, all.lo), all.hi = __reduce_max_sync(0xFFFFFFFFu, all.hi);
+            all.keys = min(keys, a.shared_len);
+            if (keys == 0) all.lo = 0, all.b = 0;
+            if (lane == 0) sh_batch = all;
+            __syncwarp();
+        }
         Item it = item_at(blockIdx.x);
+        if (SHARED && __any_sync(0xFFFFFFFFu, falls)) it.n = -1, W = 0;
         if (lanes && __any_sync(0xFFFFFFFFu, lane < a.B && offsets_fall(lane))) it.n = -1, W = 0;
         if (lane == 0) sh_first = it, sh_places = W, sh_per_unit = per_unit, sh_cut = 0;
     }
@@ -526,6 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 }
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            if constexpr (SHARED) {
+                const long long at = (long long)qi * a.q_heads + it.h * gq + f - qi * gq;
+                *reinterpret_cast<float4*>(a.shared_out + at * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                if (d == 0) a.shared_lse[at] = l == 0.f ? -CUDART_INF_F : m + log2f(l) - kUp;
+                continue;
+            }
             const long long to = (long long)(it.q0 + qi) * a.out_stride + (long long)(it.h * gq + f - qi * gq) * D + d;
             store_out(a.out, to, o.x * inv, a.out_f32), store_out(a.out, to + 1, o.y * inv, a.out_f32);
             store_out(a.out, to + 2, o.z * inv, a.out_f32), store_out(a.out, to + 3, o.w * inv, a.out_f32);
@@ -563,7 +610,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         for (uint32_t place = blockIdx.x;; place += gridDim.x) {
             const Item it = next_item(place);
             if (it.n < 0) break;
-            const int f = it.f0 + r, qi = min(f / gq, it.nq - 1), pos = it.ctx - it.nq + qi;
+            const int f = it.f0 + r, qi = min(f / gq, it.nq - 1);
+            int pos = it.ctx - it.nq + qi, last = pos;  // the query's, and the last key's that it sees here
+            if constexpr (SHARED) {
+                int b = qi / max(1, a.T / a.B), first = b * (a.T / a.B), n = a.T / a.B;
+                if (a.q_starts) {  // the last request that begins with the query or before it
+                    int lo = 0, hi = a.B - 1;
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) / 2;
+                        if (a.q_starts[mid] <= qi)
+                            lo = mid;
+                        else
+                            hi = mid - 1;
+                    }
+                    b = lo, first = a.q_starts[lo], n = a.q_starts[lo + 1] - first;
+                }
+                const int ctx = min(max(a.ctx_lens[b], 0), cap);
+                pos = ctx == 0 || qi < first || qi - first >= n ? -1 : ctx - n + qi - first;
+                last = min(pos, it.pos_hi);
+            }
             const bool there = f < it.nq * gq;
             const long long row = it.q0 + qi;
             const int head = it.h * gq + f - (f / gq) * gq;
@@ -637,9 +702,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             for (int k = 0; k < it.n; ++k, ++tile) {
                 const uint32_t sb = tile & 1, s_at = my + L::S_COL + sb * 128 + 64 * half;
                 const int t0 = (it.bs + 8 * k) * 16;
-                const bool edge = t0 + kKeys - 1 > it.pos_lo || (a.window && t0 <= it.pos_hi - a.window);
+                const bool edge = t0 + kKeys - 1 > it.pos_lo || (a.window && t0 <= (SHARED ? sh_batch.hi : it.pos_hi) - a.window);
                 // the columns that the row sees: lo .. lo + span
-                int c_lo = a.window ? max(0, pos - a.window + 1 - t0) : 0, span = min(pos - t0, kKeys - 1) - c_lo;
+                int c_lo = a.window ? max(0, pos - a.window + 1 - t0) : 0, span = min(last - t0, kKeys - 1) - c_lo;
                 if (span < 0) c_lo = 1 << 20, span = 0;
                 c_lo -= 64 * half;
                 bar_wait(&sfull[sb], (tile >> 1) & 1, ok);
@@ -715,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 bar_wait(&odone[(tile - 1) & 1], ((tile - 1) >> 1) & 1, ok);
                 fence_after();
                 if (*reinterpret_cast<volatile uint32_t*>(&sh_bad) > tile0) {
-                    const int end = min(pos + 1, (it.bs + 8 * it.n) * 16);
+                    const int end = min(last + 1, (it.bs + 8 * it.n) * 16);
                     for (int t = max(it.bs * 16, a.window ? pos - a.window + 1 : 0); t < end; ++t) {
                         const int p = t / a.page_size, page = a.table[(long long)it.b * a.table_stride + p];
                         const long long blk = ((long long)(page < 0 || page >= a.num_pages ? 0 : page) * a.kv_heads + it.h) * bpp + (t - p * a.page_size) / 16;
@@ -733,6 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 for (int gr = 0; gr < NG; ++gr)
                     off[gr] = poison >> gr & 1 ? CUDART_NAN_F : __uint_as_float(v[2 * gr]) + __uint_as_float(v[2 * gr + 1]);
             }
+            const bool none = SHARED && pos < 0;  // a query of no request or before its first token: its tiles were not looked at key by key
+            if (none) M = -CUDART_INF_F, l = 0.f;
             const float m2 = M == -CUDART_INF_F ? M : kUp - offset_to(M);  // what the weights refer to
             const float inv = it.pieces > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
             float* part = parts + (size_t)place * L::PART;
@@ -747,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) o = c / G == gr ? off[gr] : o;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint((__uint_as_float(v[i]) + o) * inv);
+                    for (int i = 0; i < 32; ++i) v[i] = none ? 0u : __float_as_uint((__uint_as_float(v[i]) + o) * inv);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0;
@@ -755,6 +822,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 if (it.pieces > 1) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(part + r * D + c)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                } else if (SHARED) {
+                    if (there)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<uint4*>(a.shared_out + (row * a.q_heads + head) * D + c)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 } else if (there) {
                     if (a.out_f32) {
                         float* p = static_cast<float*>(a.out) + to + c;
@@ -778,7 +850,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             if (half) {
             } else if (it.pieces > 1)
                 part[D * kRows + r] = m2, part[(D + 1) * kRows + r] = l;
-            else if (there && a.lse)
+            else if (SHARED) {
+                if (there) a.shared_lse[row * a.q_heads + head] = l == 0.f ? -CUDART_INF_F : m2 + log2f(l) - kUp;
+            } else if (there && a.lse)
                 a.lse[row * a.q_heads + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - kUp) * 0.69314718055994530942f;
             fence_before();
             if (it.pieces > 1 && tid == 0) sh_items_cut[sh_cut++] = it;
@@ -1003,16 +1077,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     if (bad) atomicExch(&g_kv4_tc_range, 1);
 }
 
-template <int D, int G>
+template <int D, int G, bool SHARED>
 cudaError_t launch(const Kv4AttnArgs& a, int slots, int grid, cudaStream_t s) {
     constexpr int smem = Layout<D>::SMEM;
     static_assert(smem <= 227 * 1024, "");
-    const cudaError_t err = kv4_allow_smem((const void*)kv4_attention_tc_kernel<D, G>, smem);
+    const cudaError_t err = kv4_allow_smem((const void*)kv4_attention_tc_kernel<D, G, SHARED>, smem);
     if (err != cudaSuccess) return err;
     static std::atomic<int> regs{0};
     if (!regs.load(std::memory_order_relaxed)) {
         cudaFuncAttributes attr;
-        const cudaError_t e = cudaFuncGetAttributes(&attr, kv4_attention_tc_kernel<D, G>);
+        const cudaError_t e = cudaFuncGetAttributes(&attr, kv4_attention_tc_kernel<D, G, SHARED>);
         if (e != cudaSuccess) return e;
         regs.store(attr.numRegs, std::memory_order_relaxed);
     }
@@ -1028,7 +1102,16 @@ cudaError_t launch(const Kv4AttnArgs& a, int slots, int grid, cudaStream_t s) {
     cfg.attrs = attrs;
     cfg.numAttrs = 1;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, kv4_attention_tc_kernel<D, G>, a, slots);
+    return cudaLaunchKernelEx(&cfg, kv4_attention_tc_kernel<D, G, SHARED>, a, slots);
+}
+
+template <bool SHARED>
+cudaError_t launch_for(const Kv4AttnArgs& a, cudaStream_t s) {
+    const size_t part = (size_t)kRows * (a.head_dim + 2) * sizeof(float), counters = kCounters * sizeof(uint32_t);
+    const size_t room = a.ws_bytes > counters ? (a.ws_bytes - counters) / part : 0;
+    const int sms = device_sm_count(), slots = (int)(room < (size_t)kCounters ? room : (size_t)kCounters);
+    if (a.head_dim == 64) return a.group == 32 ? launch<64, 32, SHARED>(a, slots, sms, s) : launch<64, 64, SHARED>(a, slots, sms, s);
+    return a.group == 32 ? launch<128, 32, SHARED>(a, slots, sms, s) : launch<128, 64, SHARED>(a, slots, sms, s);
 }
 
 }  // namespace
@@ -1038,13 +1121,8 @@ size_t kv4_attention_tc_workspace(int head_dim) {
     return kCounters * sizeof(uint32_t) + (size_t)(2 * device_sm_count()) * (kRows * (head_dim + 2)) * sizeof(float);
 }
 
-cudaError_t launch_kv4_attention_tc(const Kv4AttnArgs& a, cudaStream_t s) {
-    const size_t part = (size_t)kRows * (a.head_dim + 2) * sizeof(float), counters = kCounters * sizeof(uint32_t);
-    const size_t room = a.ws_bytes > counters ? (a.ws_bytes - counters) / part : 0;
-    const int sms = device_sm_count(), slots = (int)(room < (size_t)kCounters ? room : (size_t)kCounters);
-    if (a.head_dim == 64) return a.group == 32 ? launch<64, 32>(a, slots, sms, s) : launch<64, 64>(a, slots, sms, s);
-    return a.group == 32 ? launch<128, 32>(a, slots, sms, s) : launch<128, 64>(a, slots, sms, s);
-}
+cudaError_t launch_kv4_attention_tc(const Kv4AttnArgs& a, cudaStream_t s) { return launch_for<false>(a, s); }
+cudaError_t launch_kv4_attention_prefix(const Kv4AttnArgs& a, cudaStream_t s) { return launch_for<true>(a, s); }
 
 int kv4_attn_tc_take(bool fault) {
     int v = 0, z = 0;

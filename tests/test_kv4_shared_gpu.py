@@ -106,10 +106,6 @@ def test_nan_in_the_prefix_reaches_the_queries_that_see_it_alone(which, d):
     k, v = normal(g, 1, hk, d), normal(g, 1, hk, d)
     (k if which == "k" else v)[0, 1, d - 1] = float("nan")  # the last group of KV head 1
     mbw.kv4_append(cache, k, v, (table[1, at // 16].long() * 16 + at % 16).reshape(1).cuda())
-    for b in (0, 1, 3):
-        for x, (n, s, m) in zip((k, v), kv[b]):
-            for to, new in zip((n, s, m), ref.quantize(x, group)):
-                to[at] = new[0]
     starts = starts_of(nq)
     q = normal(g, starts[-1], hq, d)
     ws = mbw.kv4_attention_shared_workspace(d, starts[-1], hq)
