@@ -309,9 +309,11 @@ struct Kv4AttnArgs {
     // Requests that share their first shared_len tokens (whole pages): attention over these, normalized, and its log2 of the
     // sum of the powers of two, which the kernel of the other tokens joins to its own.
     int shared_len;
-    float* shared_out;  // fp32 [T][q_heads][head_dim]
-    float* shared_lse;  // fp32 [T][q_heads]
+    int shared_parts;   // of the shared tokens, one behind the other
+    float* shared_out;  // fp32 [shared_parts][T][q_heads][head_dim]
+    float* shared_lse;  // fp32 [shared_parts][T][q_heads]
 };
+constexpr int kKv4SharedParts = 4;  // at most
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s);
@@ -320,7 +322,14 @@ size_t kv4_attention_workspace(int head_dim);
 cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int shared_len, cudaStream_t s);
 size_t kv4_attention_shared_workspace(int head_dim, int64_t T, int64_t q_heads);
 cudaError_t launch_kv4_attention_tc(const Kv4AttnArgs& a, cudaStream_t s);  // head dimensions 64 and 128
-cudaError_t launch_kv4_attention_prefix(const Kv4AttnArgs& a, cudaStream_t s);  // the shared tokens alone, into shared_out and shared_lse
+// The shared tokens alone: how they are cut, in parts of clusters of some CTAs an item (0: not worth a kernel of their own),
+// and the kernel, which leaves the parts in shared_out and shared_lse.
+struct Kv4SharedPlan {
+    int parts, ctas;
+};
+cudaError_t plan_kv4_attention_prefix(const Kv4AttnArgs& a, int shared_len, Kv4SharedPlan* plan);
+cudaError_t launch_kv4_attention_prefix(const Kv4AttnArgs& a, const Kv4SharedPlan& plan, cudaStream_t s);
+size_t kv4_attention_prefix_rows(int64_t T, int64_t q_heads);  // of all parts together, at most
 size_t kv4_attention_tc_workspace(int head_dim);
 cudaError_t kv4_allow_smem(const void* kernel, int bytes);  // its dynamic shared memory, once per kernel and device
 int kv4_attn_tc_take(bool fault);  // its range flag, or its flag of an expired wait; cleared

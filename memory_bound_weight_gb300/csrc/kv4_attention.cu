@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     if ((COOP ? tid : lane) < 2) sh_pend[own][COOP ? tid : lane].n = 0;
 
     pdl_launch_dependents();
-    pdl_wait();
+    if (!SHARED) pdl_wait();  // else what this kernel reads is there, but for the shared part, which is waited for where it is joined
 
     // ---- the line: per item, EXTRA and its units of STEP << shift blocks ----
     const int unit = S::STEP << shift;
@@ -351,19 +351,34 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 
     // SHARED: of a row's maximum and sum here (of 4 p) and its shared part, the factors of their outputs, and their sum's log2.
     struct Joint {
-        float own, shared, lse;
+        float own, shared[kKv4SharedParts], lse;
     };
+    const long long all_rows = (long long)a.T * a.q_heads;  // of a part
     auto joint = [&](long long at, float m, float l) {
-        const float x = l == 0.f ? -CUDART_INF_F : m + log2f(l) - 2.f, y = __ldcg(a.shared_lse + at), top = fmaxf(x, y);
-        const float ex = x == -CUDART_INF_F ? 0.f : exp2_fast(x - top), ey = y == -CUDART_INF_F ? 0.f : exp2_fast(y - top), sum = ex + ey;
+        const float x = l == 0.f ? -CUDART_INF_F : m + log2f(l) - 2.f;
+        float y[kKv4SharedParts], top = x;
+#pragma unroll
+        for (int p = 0; p < kKv4SharedParts; ++p) y[p] = p < a.shared_parts ? __ldcg(a.shared_lse + p * all_rows + at) : -CUDART_INF_F;
+#pragma unroll
+        for (int p = 0; p < kKv4SharedParts; ++p) top = fmaxf(top, y[p]);
+        const float ex = x == -CUDART_INF_F ? 0.f : exp2_fast(x - top);
+        float sum = ex;
         Joint j;
-        j.own = l == 0.f ? 0.f : ex / (sum * l);
-        j.shared = sum == 0.f ? 0.f : ey / sum;
+#pragma unroll
+        for (int p = 0; p < kKv4SharedParts; ++p) {
+            j.shared[p] = y[p] == -CUDART_INF_F ? 0.f : exp2_fast(y[p] - top);
+            sum += j.shared[p];
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        j.own = l == 0.f ? 0.f : ex * inv / l;
+#pragma unroll
+        for (int p = 0; p < kKv4SharedParts; ++p) j.shared[p] *= inv;
         j.lse = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718055994530942f;
         return j;
     };
     // Outputs of rows f0 .. f0 + ROWS - 1 from the sums in o, by one warp.
     auto store = [&](int q0, int nq, int hh, int f0) {
+        if (SHARED) pdl_wait();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float inv[2];
@@ -379,11 +394,17 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                     const Joint j = joint(at, M[nt][e], L[nt][e]);
                     inv[e] = 1.f;
                     if (a.lse && g == 0) a.lse[at] = j.lse;
-                    const float* from = a.shared_out + at * D + g;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        o[nt][i][e] = fmaf(o[nt][i][e], j.own, __ldcg(from + 16 * i) * j.shared);
-                        o[nt][i][2 + e] = fmaf(o[nt][i][2 + e], j.own, __ldcg(from + 16 * i + 8) * j.shared);
+                    for (int i = 0; i < D / 16; ++i) o[nt][i][e] *= j.own, o[nt][i][2 + e] *= j.own;
+#pragma unroll
+                    for (int p = 0; p < kKv4SharedParts; ++p) {
+                        if (p >= a.shared_parts) break;
+                        const float* from = a.shared_out + (p * all_rows + at) * D + g;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[nt][i][e] = fmaf(__ldcg(from + 16 * i), j.shared[p], o[nt][i][e]);
+                            o[nt][i][2 + e] = fmaf(__ldcg(from + 16 * i + 8), j.shared[p], o[nt][i][2 + e]);
+                        }
                     }
                 } else if (a.lse && g == 0)
                     a.lse[row * a.q_heads + head] =
@@ -490,6 +511,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
             float2 m, l;
         };
         Sum* meet = reinterpret_cast<Sum*>(smem);
+        if (SHARED) pdl_wait();
         auto join = [&](Sum& x, float4 v, float2 m, float2 l) {
             const float m0 = fmaxf(x.m.x, m.x), m1 = fmaxf(x.m.y, m.y);
             const float f0 = x.m.x == -CUDART_INF_F ? 0.f : exp2_fast(x.m.x - m0), f1 = x.m.y == -CUDART_INF_F ? 0.f : exp2_fast(x.m.y - m1);
@@ -541,9 +563,15 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
                 if constexpr (SHARED) {
                     const long long at = row * a.q_heads + head;
                     const Joint j = joint(at, m, l);
-                    const float* from = a.shared_out + at * D + d;
-                    store_out(a.out, to, fmaf(e ? x.s.y : x.s.x, j.own, __ldcg(from) * j.shared), a.out_f32);
-                    store_out(a.out, to + 8, fmaf(e ? x.s.w : x.s.z, j.own, __ldcg(from + 8) * j.shared), a.out_f32);
+                    float v0 = (e ? x.s.y : x.s.x) * j.own, v1 = (e ? x.s.w : x.s.z) * j.own;
+#pragma unroll
+                    for (int p = 0; p < kKv4SharedParts; ++p)
+                        if (p < a.shared_parts) {
+                            const float* from = a.shared_out + (p * all_rows + at) * D + d;
+                            v0 = fmaf(__ldcg(from), j.shared[p], v0), v1 = fmaf(__ldcg(from + 8), j.shared[p], v1);
+                        }
+                    store_out(a.out, to, v0, a.out_f32);
+                    store_out(a.out, to + 8, v1, a.out_f32);
                     if (a.lse && d == 0) a.lse[at] = j.lse;
                     continue;
                 }
@@ -1114,6 +1142,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
     }
     if (!there) break;
     }
+    if (SHARED) pdl_wait();  // no CTA ends before the shared part's kernel: who waits for this one waits for both
     if (bad) atomicExch(&g_kv4_attn_range, 1);
 }
 
@@ -1266,7 +1295,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t s) {
 // Behind the plain call's workspace, the shared part's outputs and log sums of all rows.
 size_t kv4_attention_shared_workspace(int head_dim, int64_t T, int64_t q_heads) {
     const size_t plain = (kv4_attention_workspace(head_dim) + 15) / 16 * 16;
-    return head_dim == 256 ? plain : plain + (size_t)(T * q_heads) * (head_dim + 1) * sizeof(float);
+    return head_dim == 256 ? plain : plain + kv4_attention_prefix_rows(T, q_heads) * (head_dim + 1) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int shared_len, cudaStream_t s) {
@@ -1277,8 +1306,13 @@ cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int shared_len, cu
     b.ws_bytes = plain;
     b.shared_len = shared_len;
     b.shared_out = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + plain);
-    b.shared_lse = b.shared_out + (size_t)a.T * a.q_heads * a.head_dim;
-    const cudaError_t e = launch_kv4_attention_prefix(b, s);
+    b.shared_lse = b.shared_out + kv4_attention_prefix_rows(a.T, a.q_heads) * a.head_dim;
+    Kv4SharedPlan plan;
+    cudaError_t e = plan_kv4_attention_prefix(b, shared_len, &plan);
+    if (e != cudaSuccess) return e;
+    if (plan.parts == 0) return launch_kv4_attention(a, s);
+    b.shared_parts = plan.parts;
+    e = launch_kv4_attention_prefix(b, plan, s);
     return e == cudaSuccess ? launch_kv4_attention(b, s) : e;
 }
 

@@ -265,7 +265,6 @@ static_assert(kSoftmax * kRegsSoftmax + 2 * kUnpack * kRegsUnpack + 4 * kRegsIss
 constexpr int kCounters = 4096;  // of items cut between CTAs, as the other kernel's: both leave them at zero
 constexpr int kUp = 7;           // weights are 2^kUp p
 constexpr int kPieces = 8;       // of an item: the CTA that joins them reads 64 KB a piece, some 0.5 us
-constexpr int kSharedPieces = 16;
 constexpr float kGrow = 8.f;     // growth of the maximum, in powers of two, that is let pass
 
 // All warps but those that have nothing to do.
@@ -285,7 +284,10 @@ struct Layout {
 };
 
 // SHARED: the items are those of one request, of all the call's queries, whose keys are the shared tokens; a row's position
-// is that of its query in its own request. (The items of different requests have their rows in one tile then.)
+// is that of its query in its own request. (The items of different requests have their rows in one tile then.) An item's
+// keys are cut into a.shared_parts parts of `slots` pieces, each a CTA's of a cluster, which join theirs through shared memory;
+// the parts are left to the kernel of the other tokens. (With pieces in the workspace, as elsewhere, one CTA read them all for
+// 15 of a call's 40 us: 16 items of 9 pieces of 7 tiles.)
 template <int D, int G, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnArgs a, int slots) {
     using L = Layout<D>;
@@ -332,8 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     __syncthreads();
     fence_after();
 
-    pdl_launch_dependents();
+    // SHARED: the other tokens' kernel may start only where what came before this one is complete, since it waits for this one's
+    // results alone, and not before it joins them.
+    if (!SHARED) pdl_launch_dependents();
     pdl_wait();
+    if (SHARED) pdl_launch_dependents();
 
     // ---- places: per request, its items times the pieces each is cut into ----
     struct Request {
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     const int stride = (a.B + kThreads - 1) / kThreads;  // requests per thread
     uint32_t W = 0;
     float per_unit = 0.f;
-    auto pieces_of = [&](const Request& r) { return min((uint32_t)min(max(1, r.units / 2), SHARED ? kSharedPieces : kPieces), max(1u, (uint32_t)((float)r.units * per_unit))); };
+    auto pieces_of = [&](const Request& r) { return min((uint32_t)min(max(1, r.units / 2), kPieces), max(1u, (uint32_t)((float)r.units * per_unit))); };
     auto set_per_unit = [&](float units, uint32_t items) {
         per_unit = 2 * items <= (uint32_t)gridDim.x && items + gridDim.x <= (uint32_t)slots ? (float)gridDim.x / (units * a.kv_heads) : 0.f;
     };
@@ -440,9 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             b0 = kv4_first_seen(all.lo, a.window) / 16, b1 = (all.keys + 15) / 16;
             r = sized(0, a.T, 0);
             r.units = max(0, b1 - b0 + 7) / 8;
-            const uint32_t items = (uint32_t)r.tiles * a.kv_heads;
-            set_per_unit((float)r.tiles * (float)max(1, r.units), items);
-            W = items * pieces_of(r);
+            W = (uint32_t)r.tiles * a.kv_heads * a.shared_parts * slots;
             it.n = -1, it.b = all.b, base = 0;
             if (place >= W) return it;
         } else if (lanes) {
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 base += n, r = request(++it.b);
             }
         }
-        it.pieces = pieces_of(r);
+        it.pieces = SHARED ? (uint32_t)(a.shared_parts * slots) : pieces_of(r);
         const uint32_t at = (place - base) / it.pieces;
         it.piece = place - base - at * it.pieces, it.first = base + at * it.pieces;
         it.h = (int)(at / (uint32_t)r.tiles);
@@ -567,12 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 }
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            if constexpr (SHARED) {
-                const long long at = (long long)qi * a.q_heads + it.h * gq + f - qi * gq;
-                *reinterpret_cast<float4*>(a.shared_out + at * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-                if (d == 0) a.shared_lse[at] = l == 0.f ? -CUDART_INF_F : m + log2f(l) - kUp;
-                continue;
-            }
             const long long to = (long long)(it.q0 + qi) * a.out_stride + (long long)(it.h * gq + f - qi * gq) * D + d;
             store_out(a.out, to, o.x * inv, a.out_f32), store_out(a.out, to + 1, o.y * inv, a.out_f32);
             store_out(a.out, to + 2, o.z * inv, a.out_f32), store_out(a.out, to + 3, o.w * inv, a.out_f32);
@@ -599,6 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         for (int i = 0; i < sh_cut; ++i)
             if (sh_last[i]) join(sh_items_cut[i]);
     };
+
+    // SHARED, items of several pieces: behind it the pieces' sums lie in the CTAs' shared memory, behind the second no CTA
+    // reads another's. Every thread of the cluster comes to both.
+    auto cluster_sync = [] { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); };
+    constexpr int PITCH = D + 4;  // floats of a row there, over K's stages
+    static_assert(kRows * PITCH * 4 <= kStages * L::K_BYTES, "");
+    float* sums = reinterpret_cast<float*>(smem);
 
     uint32_t tile = 0, count = 0;  // key tiles, and items with any, before this one: the phases of every barrier
     if (warp < kSoftmax) {
@@ -801,7 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             const bool none = SHARED && pos < 0;  // a query of no request or before its first token: its tiles were not looked at key by key
             if (none) M = -CUDART_INF_F, l = 0.f;
             const float m2 = M == -CUDART_INF_F ? M : kUp - offset_to(M);  // what the weights refer to
-            const float inv = it.pieces > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const float inv = (SHARED ? slots : (int)it.pieces) > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const long long shared_row = SHARED ? ((long long)(it.piece / (uint32_t)slots) * a.T + row) * a.q_heads + head : 0;  // in its part
             float* part = parts + (size_t)place * L::PART;
             const long long to = row * a.out_stride + (long long)head * D;
 #pragma unroll 1
@@ -819,14 +824,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0;
                 }
-                if (it.pieces > 1) {
+                if (SHARED && slots > 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(sums + r * PITCH + c)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                } else if (!SHARED && it.pieces > 1) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(part + r * D + c)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 } else if (SHARED) {
                     if (there)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            reinterpret_cast<uint4*>(a.shared_out + (row * a.q_heads + head) * D + c)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            reinterpret_cast<uint4*>(a.shared_out + shared_row * D + c)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 } else if (there) {
                     if (a.out_f32) {
                         float* p = static_cast<float*>(a.out) + to + c;
@@ -848,14 +856,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
                 }
             }
             if (half) {
-            } else if (it.pieces > 1)
+            } else if (SHARED && slots > 1)
+                sh_sums[0][r] = m2, sh_sums[1][r] = l;
+            else if (!SHARED && it.pieces > 1)
                 part[D * kRows + r] = m2, part[(D + 1) * kRows + r] = l;
             else if (SHARED) {
-                if (there) a.shared_lse[row * a.q_heads + head] = l == 0.f ? -CUDART_INF_F : m2 + log2f(l) - kUp;
+                if (there) a.shared_lse[shared_row] = l == 0.f ? -CUDART_INF_F : m2 + log2f(l) - kUp;
             } else if (there && a.lse)
                 a.lse[row * a.q_heads + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - kUp) * 0.69314718055994530942f;
             fence_before();
-            if (it.pieces > 1 && tid == 0) sh_items_cut[sh_cut++] = it;
+            if (!SHARED && it.pieces > 1 && tid == 0) sh_items_cut[sh_cut++] = it;
+        }
+        if (SHARED && slots > 1) {
+            // A cluster's CTAs have one item, of which each joins some rows, the pieces in order.
+            cluster_sync();
+            const int rank = blockIdx.x % slots, r1 = kRows * (rank + 1) / slots;
+            constexpr int LPR = D / 4;  // lanes of a row, four columns each
+            for (int r = kRows * rank / slots + warp * (32 / LPR) + lane / LPR; r < r1 && W > 0; r += kSoftmax * (32 / LPR)) {
+                const int f = sh_first.f0 + r, d = lane % LPR * 4;
+                if (f >= a.T * gq) break;
+                float m = -CUDART_INF_F, l = 0.f;
+                float4 v[kPieces], o = make_float4(0.f, 0.f, 0.f, 0.f);
+                float mj[kPieces], lj[kPieces];
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) {
+                    mj[j] = -CUDART_INF_F, lj[j] = 0.f, v[j] = o;
+                    if (j < slots) {
+                        uint32_t at;
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_at(sums + r * PITCH + d)), "r"(j));
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[j].x), "=f"(v[j].y), "=f"(v[j].z), "=f"(v[j].w) : "r"(at) : "memory");
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_at(&sh_sums[0][r])), "r"(j));
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(mj[j]) : "r"(at) : "memory");
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(lj[j]) : "r"(at + kRows * 4) : "memory");
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) {
+                    if (mj[j] == -CUDART_INF_F && lj[j] == 0.f) continue;  // no key, or none that is a number: then l is none
+                    const float top = fmaxf(m, mj[j]), e = m == top ? 1.f : exp2_fast(m - top), x = mj[j] == top ? 1.f : exp2_fast(mj[j] - top);
+                    m = top, l = fmaf(l, e, lj[j] * x);
+                    o = make_float4(fmaf(o.x, e, v[j].x * x), fmaf(o.y, e, v[j].y * x), fmaf(o.z, e, v[j].z * x), fmaf(o.w, e, v[j].w * x));
+                }
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int qi = f / gq;
+                const long long at = ((long long)(sh_first.piece / (uint32_t)slots) * a.T + qi) * a.q_heads + sh_first.h * gq + f - qi * gq;
+                *reinterpret_cast<float4*>(a.shared_out + at * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                if (d == 0) a.shared_lse[at] = l == 0.f ? -CUDART_INF_F : m + log2f(l) - kUp;
+            }
+            cluster_sync();
         }
         finish(true);
     } else if (warp < kIssuer) {
@@ -1015,6 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             }
             tile += it.n;
         }
+        if (SHARED && slots > 1) cluster_sync(), cluster_sync();
         finish(true);
     } else if (warp >= kIssuer) {
         registers<kRegsIssuer>(false);
@@ -1069,6 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
         bool last = true;
         bar_wait(done, 0, last);
         }
+        if (SHARED && slots > 1) cluster_sync(), cluster_sync();
     }
     fence_before();
     __syncthreads();
@@ -1077,8 +1127,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
     if (bad) atomicExch(&g_kv4_tc_range, 1);
 }
 
+// pieces: CTAs of a cluster that share an item (SHARED), else 1.
 template <int D, int G, bool SHARED>
-cudaError_t launch(const Kv4AttnArgs& a, int slots, int grid, cudaStream_t s) {
+cudaError_t launch(const Kv4AttnArgs& a, int slots, int grid, int pieces, cudaStream_t s) {
     constexpr int smem = Layout<D>::SMEM;
     static_assert(smem <= 227 * 1024, "");
     const cudaError_t err = kv4_allow_smem((const void*)kv4_attention_tc_kernel<D, G, SHARED>, smem);
@@ -1096,22 +1147,22 @@ cudaError_t launch(const Kv4AttnArgs& a, int slots, int grid, cudaStream_t s) {
     cfg.blockDim = dim3((unsigned)kThreads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
-    cudaLaunchAttribute attrs[1];
+    cudaLaunchAttribute attrs[2];
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)pieces;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pieces > 1 ? 2 : 1;
     count_launch();
     return cudaLaunchKernelEx(&cfg, kv4_attention_tc_kernel<D, G, SHARED>, a, slots);
 }
 
 template <bool SHARED>
-cudaError_t launch_for(const Kv4AttnArgs& a, cudaStream_t s) {
-    const size_t part = (size_t)kRows * (a.head_dim + 2) * sizeof(float), counters = kCounters * sizeof(uint32_t);
-    const size_t room = a.ws_bytes > counters ? (a.ws_bytes - counters) / part : 0;
-    const int sms = device_sm_count(), slots = (int)(room < (size_t)kCounters ? room : (size_t)kCounters);
-    if (a.head_dim == 64) return a.group == 32 ? launch<64, 32, SHARED>(a, slots, sms, s) : launch<64, 64, SHARED>(a, slots, sms, s);
-    return a.group == 32 ? launch<128, 32, SHARED>(a, slots, sms, s) : launch<128, 64, SHARED>(a, slots, sms, s);
+cudaError_t launch_for(const Kv4AttnArgs& a, int slots, int grid, int pieces, cudaStream_t s) {
+    if (a.head_dim == 64) return a.group == 32 ? launch<64, 32, SHARED>(a, slots, grid, pieces, s) : launch<64, 64, SHARED>(a, slots, grid, pieces, s);
+    return a.group == 32 ? launch<128, 32, SHARED>(a, slots, grid, pieces, s) : launch<128, 64, SHARED>(a, slots, grid, pieces, s);
 }
 
 }  // namespace
@@ -1121,8 +1172,89 @@ size_t kv4_attention_tc_workspace(int head_dim) {
     return kCounters * sizeof(uint32_t) + (size_t)(2 * device_sm_count()) * (kRows * (head_dim + 2)) * sizeof(float);
 }
 
-cudaError_t launch_kv4_attention_tc(const Kv4AttnArgs& a, cudaStream_t s) { return launch_for<false>(a, s); }
-cudaError_t launch_kv4_attention_prefix(const Kv4AttnArgs& a, cudaStream_t s) { return launch_for<true>(a, s); }
+cudaError_t launch_kv4_attention_tc(const Kv4AttnArgs& a, cudaStream_t s) {
+    const size_t part = (size_t)kRows * (a.head_dim + 2) * sizeof(float), counters = kCounters * sizeof(uint32_t);
+    const size_t room = a.ws_bytes > counters ? (a.ws_bytes - counters) / part : 0;
+    const int slots = (int)(room < (size_t)kCounters ? room : (size_t)kCounters);
+    return launch_for<false>(a, slots, device_sm_count(), 1, s);
+}
+
+namespace {
+
+// Clusters of n CTAs of the kernel that the device holds at once (a GPC's SMs hold them or not), asked for once per device.
+template <int D, int G>
+cudaError_t held(int n, int* out) {
+    static std::atomic<int> known[16][kPieces];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    *out = dev < 16 ? known[dev][n - 1].load(std::memory_order_relaxed) : 0;
+    if (*out) return cudaSuccess;
+    e = kv4_allow_smem((const void*)kv4_attention_tc_kernel<D, G, true>, Layout<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n, 1, 1);
+    cfg.blockDim = dim3((unsigned)kThreads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)Layout<D>::SMEM;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)n;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(out, kv4_attention_tc_kernel<D, G, true>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (*out < 1) *out = 1;
+    if (dev < 16) known[dev][n - 1].store(*out, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+cudaError_t held_for(const Kv4AttnArgs& a, int n, int* out) {
+    if (a.head_dim == 64) return a.group == 32 ? held<64, 32>(n, out) : held<64, 64>(n, out);
+    return a.group == 32 ? held<128, 32>(n, out) : held<128, 64>(n, out);
+}
+
+int64_t prefix_items(const Kv4AttnArgs& a) { return ((int64_t)a.T * (a.q_heads / a.kv_heads) + kRows - 1) / kRows * a.kv_heads; }
+
+}  // namespace
+
+// An item is 128 rows or fewer of a KV head, so that there are q_heads T / 128 or more; more than one part only where the
+// CTAs have one of them each.
+size_t kv4_attention_prefix_rows(int64_t T, int64_t q_heads) {
+    const int64_t rows = T * q_heads, most = (int64_t)device_sm_count() * kRows;
+    return (size_t)(rows > most ? rows : most);
+}
+
+cudaError_t plan_kv4_attention_prefix(const Kv4AttnArgs& a, int shared_len, Kv4SharedPlan* plan) {
+    const int64_t sms = device_sm_count(), items = prefix_items(a), units = (shared_len + kKeys - 1) / kKeys;
+    // Pieces of two key tiles or more, as many as find an SM each.
+    int64_t best = 1;
+    *plan = {1, 1};
+    for (int c = 1; c <= kPieces; ++c) {
+        int n = 0;
+        const cudaError_t e = held_for(a, c, &n);
+        if (e != cudaSuccess) return e;
+        for (int g = 1; g <= kKv4SharedParts; ++g) {
+            const int64_t pieces = c * g;
+            if (pieces > 1 && (items * g > n || items * pieces > sms || 2 * pieces > units)) continue;
+            if (pieces > best || (pieces == best && g < plan->parts)) best = pieces, *plan = {g, c};
+        }
+    }
+    // Worth it where reading the shared tokens for every request, once for each 8 rows, at 4.9 TB/s (the rate of 64 requests)
+    // would take longer than this kernel, 12 us and 1.25 a tile of keys, and what its SMs leave undone of the other's start
+    // where that one has many items. Measured, plain and shared, us: Qwen3-4B's heads, 8192 tokens, 2, 4, 8 and 64 requests:
+    // 13.8 19.0, 18.7 26.7, 26.0 31.4, 114.9 42.5; Qwen2.5-7B's, 12 of 2 to 5 queries, 30000 tokens: 132 53; 64, 512: 14.5 31.3.
+    const int64_t with = a.B < a.T ? a.B : a.T, gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
+    const double read = (double)with * ((rows + 7) / 8) * a.kv_heads * shared_len * (a.head_dim + 8 * (a.head_dim / a.group)) / 4900.0;
+    const int64_t waves = (items * best + sms - 1) / sms, tiles = (units + best - 1) / best * waves;
+    if (read < 12000.0 + 1250.0 * tiles + (2 * with * a.kv_heads > sms ? 5000.0 : 0.0)) plan->parts = 0;
+    return cudaSuccess;
+}
+
+cudaError_t launch_kv4_attention_prefix(const Kv4AttnArgs& a, const Kv4SharedPlan& plan, cudaStream_t s) {
+    const int64_t sms = device_sm_count(), all = prefix_items(a) * plan.parts * plan.ctas;
+    return launch_for<true>(a, plan.ctas, (int)(plan.parts * plan.ctas > 1 || all < sms ? all : sms), plan.ctas, s);
+}
 
 int kv4_attn_tc_take(bool fault) {
     int v = 0, z = 0;
