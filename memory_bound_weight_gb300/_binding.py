@@ -514,7 +514,9 @@ def _load_fast():
         warnings.warn(f"{path} is not used, calls are marshalled in Python (build() makes it anew): {e}", RuntimeWarning)
         return
     mod.init(*(ctypes.cast(f, ctypes.c_void_p).value
-               for f in (L.mbw_kv4_append, L.mbw_kv4_gather, L.mbw_kv4_attention, L.mbw_token_logprobs)))
+               for f in (L.mbw_kv4_append, L.mbw_kv4_gather, L.mbw_kv4_attention, L.mbw_token_logprobs,
+                         L.mbw_kv4_attention_shared, L.mbw_quantize_fp8_g128, L.mbw_quantize_fp8_b128,
+                         L.mbw_dequant_fp8_g128, L.mbw_dequant_fp8_b128, L.gemm_fp8_b128)))
     _fast = mod
 
 
@@ -738,6 +740,13 @@ def kv4_attention_shared(cache, q, block_table, ctx_lens, shared_len, q_starts=N
     page_size entries of the rows of block_table are equal, as far as each request's length goes. The shared pages are
     read and multiplied once for the queries of all requests. The other arguments and the result are kv4_attention's.
     workspace: from kv4_attention_shared_workspace; without one, shared pages are read for each request."""
+    if _fast is None:
+        _load_fast()
+    if _fast and out is None and not getattr(_tls, "fp32", False):
+        r = _fast.kv4_attention(cache._addr, cache.pages, q, block_table, ctx_lens, q_starts,
+                                cache.head_dim ** -0.5 if scale is None else scale, window, return_lse, workspace, shared_len)
+        if r is not None:
+            return check("mbw_kv4_attention_shared", r) if r.__class__ is int else r
     return _kv4_attention(cache, q, block_table, ctx_lens, q_starts, scale, window, out, return_lse, workspace, shared_len)
 
 
@@ -795,6 +804,12 @@ def _matrix(t, name, dtype, shape):
 def quantize_fp8_g128(X, norm_weight=None, norm_eps=1e-6):
     """Activations bf16 (M, K) (rows may be apart) -> (Xq float8_e4m3fn (M, K), x_scales fp32 (M, K/128)): per row and
     128 columns scale = max|x| / 448, code = e4m3(x / scale). With norm_weight bf16 (K,), of the RMS-normed rows."""
+    if _fast is None:
+        _load_fast()
+    if _fast:
+        r = _fast.quantize_fp8_g128(X, norm_weight, norm_eps)
+        if r is not None:
+            return r if r.__class__ is tuple else check("mbw_quantize_fp8_g128", r)
     torch = _torch()
     bf16, f32 = _types()[:2]
     if not isinstance(X, torch.Tensor):
@@ -824,6 +839,12 @@ def quantize_fp8_g128(X, norm_weight=None, norm_eps=1e-6):
 
 def quantize_fp8_b128(W):
     """Weights bf16 (N, K) -> (Wq float8_e4m3fn (N, K), w_scales fp32 (ceil(N/128), K/128)), a scale per 128 x 128."""
+    if _fast is None:
+        _load_fast()
+    if _fast:
+        r = _fast.quantize_fp8_b128(W)
+        if r is not None:
+            return r if r.__class__ is tuple else check("mbw_quantize_fp8_b128", r)
     torch = _torch()
     N, K = _plain(W, "W", torch.bfloat16, 2)
     if K % 128 or not K:
@@ -838,6 +859,12 @@ def quantize_fp8_b128(W):
 
 
 def _dequant_fp8(name, codes, scales, rows):
+    if _fast is None:
+        _load_fast()
+    if _fast:
+        r = _fast.dequant_fp8(codes, scales, rows)
+        if r is not None:
+            return check(name, r) if r.__class__ is int else r
     torch = _torch()
     M, K = _codes(codes, "codes")
     _matrix(scales, "scales", torch.float32, ((M + rows - 1) // rows, K // 128))
@@ -864,6 +891,12 @@ def gemm_fp8_b128(Xq, x_scales, Wq, w_scales, out=None, residual=None, up_weight
     x_scales fp32 (M, K/128) (quantize_fp8_g128), Wq float8_e4m3fn (N, K), w_scales fp32 (ceil(N/128), K/128)
     (quantize_fp8_b128) -> Y bf16 (M, N). With up_weights and up_scales, laid out as Wq and w_scales, the gated form
     silu(X . W^T) * (X . U^T); residual bf16 (M, N) (may be `out`) is added."""
+    if _fast is None:
+        _load_fast()
+    if _fast and out is None and not getattr(_tls, "fp32", False):
+        r = _fast.gemm_fp8(Xq, x_scales, Wq, w_scales, residual, up_weights, up_scales, workspace)
+        if r is not None:
+            return check("gemm_fp8_b128", r) if r.__class__ is int else r
     f32 = _types()[1]
     M, K = _codes(Xq, "Xq")
     N, Kw = _codes(Wq, "Wq")

@@ -1,6 +1,6 @@
 // fast_calls.cpp -- the binding's checks and marshalling of the calls that a
-// decode step makes many times, in C++: kv4_append, kv4_gather, kv4_attention
-// and token_logprobs. Each function checks what the Python function of its name
+// decode step makes many times, in C++: kv4_append, kv4_gather, kv4_attention,
+// kv4_attention_shared, token_logprobs, the 8-bit quantizers and products. Each function checks what the Python function of its name
 // checks, allocates the outputs, makes the library's call on the current stream
 // and returns the outputs, or the library's status where that is not 0. What it
 // does not take as it is (a wrong argument, a tensor's subclass, a missing
@@ -22,7 +22,12 @@ namespace {
 decltype(&mbw_kv4_append) append_fn;
 decltype(&mbw_kv4_gather) gather_fn;
 decltype(&mbw_kv4_attention) attention_fn;
+decltype(&mbw_kv4_attention_shared) shared_fn;
 decltype(&mbw_token_logprobs) logprobs_fn;
+decltype(&mbw_quantize_fp8_g128) rows_fn;
+decltype(&mbw_quantize_fp8_b128) blocks_fn;
+decltype(&mbw_dequant_fp8_g128) row_values_fn, block_values_fn;
+decltype(&gemm_fp8_b128) product_fn;
 
 struct Unusual {};  // left to the Python function
 
@@ -152,10 +157,10 @@ PyObject* kv4_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (address, pages, q, block_table, ctx_lens, q_starts, scale, window, return_lse, workspace)
+// (address, pages, q, block_table, ctx_lens, q_starts, scale, window, return_lse, workspace[, shared_len])
 PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        if (n != 10) throw Unusual();
+        if (n != 10 && n != 11) throw Unusual();
         const int dev = device_now();
         const mbw_kv4_cache* c = cache_of(a[0], a[1], dev);
         const Rows q = rows(a[2], dev, -1, c->head_dim);
@@ -172,10 +177,14 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor out = empty({q.n, q.heads, c->head_dim}, *q.t, at::kBFloat16);
         at::Tensor lse;
         if (want_lse) lse = empty({q.n, q.heads}, *q.t, at::kFloat);
-        const mbw_status st = attention_fn(c, q.t->data_ptr(), q.stride, out.data_ptr(), q.heads * c->head_dim,
-                                           want_lse ? lse.data_ptr<float>() : nullptr, table->data_ptr<int32_t>(), width, width,
-                                           ctx->data_ptr<int32_t>(), starts ? starts->data_ptr<int32_t>() : nullptr, B, q.n,
-                                           q.heads, (float)scale, window, ws, bytes, stream(dev));
+        float* lse_at = want_lse ? lse.data_ptr<float>() : nullptr;
+        const int32_t* starts_at = starts ? starts->data_ptr<int32_t>() : nullptr;
+        const mbw_status st = n == 11 ? shared_fn(c, q.t->data_ptr(), q.stride, out.data_ptr(), q.heads * c->head_dim, lse_at, table->data_ptr<int32_t>(),
+                                                  width, width, ctx->data_ptr<int32_t>(), starts_at, B, q.n, q.heads, (float)scale, window,
+                                                  whole(a[10]), ws, bytes, stream(dev))
+                                      : attention_fn(c, q.t->data_ptr(), q.stride, out.data_ptr(), q.heads * c->head_dim, lse_at,
+                                                     table->data_ptr<int32_t>(), width, width, ctx->data_ptr<int32_t>(), starts_at, B, q.n, q.heads,
+                                                     (float)scale, window, ws, bytes, stream(dev));
         if (st) return PyLong_FromLong(st);
         PyObject* o = THPVariable_Wrap(out);
         return want_lse ? Py_BuildValue("(NN)", o, THPVariable_Wrap(lse)) : o;
@@ -210,12 +219,106 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A matrix of e4m3 codes, whose width is a positive multiple of 128.
+const at::Tensor* codes(PyObject* o, int dev) {
+    const at::Tensor* t = plain(o, dev, at::kFloat8_e4m3fn, 2);
+    if (t->size(1) % 128 || t->size(1) == 0) throw Unusual();
+    return t;
+}
+const at::Tensor* matrix(PyObject* o, int dev, at::ScalarType type, int64_t rows, int64_t columns) {
+    const at::Tensor* t = plain(o, dev, type, 2);
+    if (t->size(0) != rows || t->size(1) != columns) throw Unusual();
+    return t;
+}
+
+// (X, norm_weight, norm_eps)
+PyObject* quantize_fp8_g128(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 3) throw Unusual();
+        const int dev = device_now();
+        const at::Tensor* x = tensor(a[0], dev, at::kBFloat16);
+        if (x->dim() != 2 || x->stride(1) != 1) throw Unusual();
+        const int64_t M = x->size(0), K = x->size(1);
+        if (K % 128 || K == 0) throw Unusual();
+        const at::Tensor* w = a[1] == Py_None ? nullptr : vector(a[1], dev, at::kBFloat16, K);
+        const double eps = number(a[2]);
+        const at::Tensor q = empty({M, K}, *x, at::kFloat8_e4m3fn), s = empty({M, K / 128}, *x, at::kFloat);
+        const mbw_status st = rows_fn(x->data_ptr(), M > 1 ? x->stride(0) : K, static_cast<uint8_t*>(q.data_ptr()), s.data_ptr<float>(), M, K,
+                                      w ? w->data_ptr() : nullptr, eps, stream(dev));
+        if (st) return PyLong_FromLong(st);
+        return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(s));
+    });
+}
+
+// (W)
+PyObject* quantize_fp8_b128(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 1) throw Unusual();
+        const int dev = device_now();
+        const at::Tensor* w = plain(a[0], dev, at::kBFloat16, 2);
+        const int64_t N = w->size(0), K = w->size(1);
+        if (K % 128 || K == 0) throw Unusual();
+        const at::Tensor q = empty({N, K}, *w, at::kFloat8_e4m3fn), s = empty({(N + 127) / 128, K / 128}, *w, at::kFloat);
+        const mbw_status st = blocks_fn(w->data_ptr(), static_cast<uint8_t*>(q.data_ptr()), s.data_ptr<float>(), N, K, stream(dev));
+        if (st) return PyLong_FromLong(st);
+        return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(s));
+    });
+}
+
+// (codes, scales, rows of a scale: 1 or 128)
+PyObject* dequant_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 3) throw Unusual();
+        const int dev = device_now();
+        const at::Tensor* q = codes(a[0], dev);
+        const int64_t M = q->size(0), K = q->size(1), rows = whole(a[2]);
+        const at::Tensor* s = matrix(a[1], dev, at::kFloat, (M + rows - 1) / rows, K / 128);
+        const at::Tensor out = empty({M, K}, *q, at::kFloat);
+        const mbw_status st = (rows == 1 ? row_values_fn : block_values_fn)(static_cast<const uint8_t*>(q->data_ptr()), s->data_ptr<float>(),
+                                                                             out.data_ptr<float>(), M, K, stream(dev));
+        return st ? PyLong_FromLong(st) : THPVariable_Wrap(out);
+    });
+}
+
+// (Xq, x_scales, Wq, w_scales, residual, up_weights, up_scales, workspace)
+PyObject* gemm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 8) throw Unusual();
+        const int dev = device_now();
+        const at::Tensor *x = codes(a[0], dev), *w = codes(a[2], dev);
+        const int64_t M = x->size(0), K = x->size(1), N = w->size(0), blocks = (N + 127) / 128;
+        if (w->size(1) != K) throw Unusual();
+        const at::Tensor *xs = matrix(a[1], dev, at::kFloat, M, K / 128), *ws = matrix(a[3], dev, at::kFloat, blocks, K / 128);
+        mbw_fusion f{};
+        if (a[4] != Py_None) f.residual = matrix(a[4], dev, at::kBFloat16, M, N)->data_ptr();
+        if ((a[5] == Py_None) != (a[6] == Py_None)) throw Unusual();
+        if (a[5] != Py_None) {
+            const at::Tensor* u = codes(a[5], dev);
+            if (u->size(0) != N || u->size(1) != K) throw Unusual();
+            f.up_weights = u->data_ptr();
+            f.up_scales = matrix(a[6], dev, at::kFloat, blocks, K / 128)->data_ptr();
+        }
+        size_t bytes;
+        void* space = workspace(a[7], dev, bytes);
+        const at::Tensor y = empty({M, N}, *x, at::kBFloat16);
+        const mbw_status st = product_fn(static_cast<const uint8_t*>(x->data_ptr()), xs->data_ptr<float>(), static_cast<const uint8_t*>(w->data_ptr()),
+                                         ws->data_ptr<float>(), y.data_ptr(), M, N, K, &f, space, bytes, stream(dev));
+        return st ? PyLong_FromLong(st) : THPVariable_Wrap(y);
+    });
+}
+
 // The library's functions, by address.
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 4) {
-        PyErr_SetString(PyExc_TypeError, "four addresses");
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "ten addresses");
         return nullptr;
     }
+    shared_fn = reinterpret_cast<decltype(shared_fn)>(PyLong_AsVoidPtr(a[4]));
+    rows_fn = reinterpret_cast<decltype(rows_fn)>(PyLong_AsVoidPtr(a[5]));
+    blocks_fn = reinterpret_cast<decltype(blocks_fn)>(PyLong_AsVoidPtr(a[6]));
+    row_values_fn = reinterpret_cast<decltype(row_values_fn)>(PyLong_AsVoidPtr(a[7]));
+    block_values_fn = reinterpret_cast<decltype(block_values_fn)>(PyLong_AsVoidPtr(a[8]));
+    product_fn = reinterpret_cast<decltype(product_fn)>(PyLong_AsVoidPtr(a[9]));
     append_fn = reinterpret_cast<decltype(append_fn)>(PyLong_AsVoidPtr(a[0]));
     gather_fn = reinterpret_cast<decltype(gather_fn)>(PyLong_AsVoidPtr(a[1]));
     attention_fn = reinterpret_cast<decltype(attention_fn)>(PyLong_AsVoidPtr(a[2]));
@@ -230,6 +333,10 @@ PyMethodDef methods[] = {
     {"kv4_gather", (PyCFunction)(void*)kv4_gather, METH_FASTCALL, nullptr},
     {"kv4_attention", (PyCFunction)(void*)kv4_attention, METH_FASTCALL, nullptr},
     {"token_logprobs", (PyCFunction)(void*)token_logprobs, METH_FASTCALL, nullptr},
+    {"quantize_fp8_g128", (PyCFunction)(void*)quantize_fp8_g128, METH_FASTCALL, nullptr},
+    {"quantize_fp8_b128", (PyCFunction)(void*)quantize_fp8_b128, METH_FASTCALL, nullptr},
+    {"dequant_fp8", (PyCFunction)(void*)dequant_fp8, METH_FASTCALL, nullptr},
+    {"gemm_fp8", (PyCFunction)(void*)gemm_fp8, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -302,3 +302,49 @@ def test_weights_are_there_for_a_product_queued_behind_them():
         got = mbw.gemm_fp8_b128(x, xs, q, s)
         y, mass, eps = exact(x, xs, *plain_blocks(w))
         check(got, y, mass * eps + half_step(y))
+
+
+def test_compiled_calls_give_the_same_and_refuse_in_the_same_words(monkeypatch):
+    from memory_bound_weight_gb300 import _binding as B
+
+    g = gen(11)
+    x, xs, w, sc = operands(g, 20, 300, 512)
+    wide = torch.randn(20, 600, generator=g, device="cuda").bfloat16()
+    wn = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    r = torch.randn(20, 300, generator=g, device="cuda").bfloat16()
+
+    def calls():
+        return [*mbw.quantize_fp8_g128(wide[:, 8:520]), *mbw.quantize_fp8_g128(wide[:, :512], norm_weight=wn, norm_eps=1e-5),
+                *mbw.quantize_fp8_g128(wide[:1, :512]), *mbw.quantize_fp8_b128(wide[:, :512].contiguous()),
+                mbw.dequant_fp8_g128(x, xs), mbw.dequant_fp8_b128(w, sc), mbw.gemm_fp8_b128(x, xs, w, sc),
+                mbw.gemm_fp8_b128(x, xs, w, sc, residual=r, up_weights=w, up_scales=sc, workspace=wn)]
+
+    bad = [lambda: mbw.quantize_fp8_g128(wide), lambda: mbw.quantize_fp8_g128(wide[:, :512].float()),
+           lambda: mbw.quantize_fp8_g128(wide.t()), lambda: mbw.quantize_fp8_g128(wide[:, :512], norm_weight=wn[:256]),
+           lambda: mbw.quantize_fp8_b128(wide[:, :512]), lambda: mbw.dequant_fp8_g128(x, sc), lambda: mbw.dequant_fp8_b128(x, xs),
+           lambda: mbw.gemm_fp8_b128(x, xs[:, :3], w, sc), lambda: mbw.gemm_fp8_b128(x, xs, w, sc, residual=r[:, :100]),
+           lambda: mbw.gemm_fp8_b128(x, xs, w[:, :256].contiguous(), sc), lambda: mbw.gemm_fp8_b128(x, xs, w, sc, up_weights=w),
+           lambda: mbw.gemm_fp8_b128(x, xs, w, sc, up_weights=w[:100].contiguous(), up_scales=sc),
+           lambda: mbw.gemm_fp8_b128(x, xs, w, sc, workspace=torch.zeros(4)), lambda: mbw.gemm_fp8_b128(x.cpu(), xs, w, sc)]
+
+    def said():
+        out = []
+        for f in bad:
+            with pytest.raises((TypeError, ValueError)) as e:
+                f()
+            out.append((e.type, str(e.value)))
+        return out
+
+    fast, words = calls(), said()
+    assert B._fast and B._fast.gemm_fp8(x, xs, w, sc, None, None, None, None) is not None
+    with monkeypatch.context() as m:
+        m.setattr(B, "_fast", False)
+        slow, slow_words = calls(), said()
+    assert words == slow_words
+    for a, b in zip(fast, slow):
+        assert a.dtype == b.dtype and a.shape == b.shape and same(a, b)
+    mbw.inject_launch_failures(1)
+    with pytest.raises(mbw.MbwError):
+        mbw.gemm_fp8_b128(x, xs, w, sc)
+    with mbw.output_fp32():
+        assert mbw.gemm_fp8_b128(x, xs, w, sc).dtype == torch.float32
