@@ -16,6 +16,12 @@ and behind the last one logits = W_head . norm(x) and token_logprobs. A step for
 one token of every request is captured into a CUDA graph and replayed: the
 lengths, positions and slots it works on are device tensors that it moves on
 itself.
+
+With --weights fp8 each product is one of 8-bit floating point operands with a
+scale for each block of 128: quantize_fp8_g128 (with the norm where there is one)
+and gemm_fp8_b128, gate and up in one call. With --shared N the requests' prompts
+begin with the same N tokens, whose keys and values are computed and held once;
+attention is then kv4_attention_shared.
 """
 from __future__ import annotations
 
@@ -48,17 +54,27 @@ SHAPES = {
 
 
 class Decoder:
-    """Weights, caches and buffers for up to `requests` requests of up to `max_tokens` tokens each."""
+    """Weights (bf16, or fp8: 8-bit floating point with a scale for each block of 128), caches and buffers for up to
+    `requests` requests of up to `max_tokens` tokens each."""
 
-    def __init__(self, shape, layers=None, requests=1, max_tokens=1024, page_size=16, group=64, seed=0):
-        self.shape, self.requests = shape, requests
+    shared = 0  # tokens that all requests begin with, in the same pages
+    fp8 = False
+
+    def __init__(self, shape, layers=None, requests=1, max_tokens=1024, page_size=16, group=64, seed=0, weights="bf16"):
+        if weights not in ("bf16", "fp8"):
+            raise ValueError(f"weights must be bf16 or fp8, got {weights}")
+        self.shape, self.requests, self.fp8 = shape, requests, weights == "fp8"
         n = shape.layers if layers is None else layers
         s, dev = shape, "cuda"
         gen = torch.Generator(device=dev)
         gen.manual_seed(seed)
 
-        def weight(rows, cols):
+        def plain(rows, cols):
             return (torch.randn(rows, cols, generator=gen, device=dev) * cols ** -0.5).bfloat16()
+
+        def weight(rows, cols):
+            w = plain(rows, cols)
+            return mbw.quantize_fp8_b128(w) if self.fp8 else w
 
         def ones(width):
             return (1 + 0.1 * torch.randn(width, generator=gen, device=dev)).bfloat16()
@@ -67,7 +83,7 @@ class Decoder:
         self.layers = [dict(norm1=ones(s.hidden), qkv=weight(width, s.hidden), o=weight(s.hidden, s.heads * s.dim),
                             norm2=ones(s.hidden), gate=weight(s.mlp, s.hidden), up=weight(s.mlp, s.hidden),
                             down=weight(s.hidden, s.mlp)) for _ in range(n)]
-        self.embedding, self.norm, self.head = weight(s.vocab, s.hidden), ones(s.hidden), weight(s.vocab, s.hidden)
+        self.embedding, self.norm, self.head = plain(s.vocab, s.hidden), ones(s.hidden), weight(s.vocab, s.hidden)
         self.embedding *= s.hidden ** 0.5
         # each request has its own pages, the same ones in every layer's cache, in no particular order
         per = -(-max_tokens // page_size)
@@ -80,11 +96,14 @@ class Decoder:
         self.ctx = torch.zeros(requests, dtype=torch.int32, device=dev)  # tokens in the cache
         self.ids = torch.zeros(requests, dtype=torch.int64, device=dev)  # the next ones
         self.longest = 0  # the largest of ctx, known on the host: a step past max_tokens would index past the tables
-        self.attn_ws = mbw.kv4_attention_workspace(s.dim)
+        self.own_table = self.table.clone()
+        self.attn_ws = mbw.kv4_attention_shared_workspace(s.dim, requests, s.heads)
         self.prob_ws = mbw.token_logprobs_workspace()
 
     def tune(self, rows=None):
-        """Measures the products' plans for `rows` tokens (those of a step by default)."""
+        """Measures the products' plans for `rows` tokens (those of a step by default). Those of 8 bits have none."""
+        if self.fp8:
+            return
         s, m, op = self.shape, rows or self.requests, mbw.OP_GEMV_BF16
         for fuse, n, k in ((mbw.FUSE_NORM, (s.heads + 2 * s.kv_heads) * s.dim, s.hidden),
                            (mbw.FUSE_RESIDUAL, s.hidden, s.heads * s.dim),
@@ -92,26 +111,41 @@ class Decoder:
                            (mbw.FUSE_NORM, s.vocab, s.hidden)):
             mbw.autotune(op | fuse, m, n, k)
 
+    def product(self, w, x, norm=None, up=None, residual=None):
+        """x . w^T (+ residual) of the normed x; with `up`, silu(x . w^T) * (x . up^T)."""
+        if self.fp8:
+            q, scales = mbw.quantize_fp8_g128(x, norm_weight=norm)
+            u, us = up or (None, None)
+            return mbw.gemm_fp8_b128(q, scales, *w, residual=residual, up_weights=u, up_scales=us)
+        return mbw.gemv_fused(mbw.OP_GEMV_BF16, w, None, x, norm_weight=norm, up_weights=up, residual=residual)
+
+    def attend(self, cache, q, q_starts):
+        if self.shared:
+            return mbw.kv4_attention_shared(cache, q, self.table, self.ctx, self.shared, q_starts, workspace=self.attn_ws)
+        return mbw.kv4_attention(cache, q, self.table, self.ctx, q_starts, workspace=self.attn_ws)
+
     def forward(self, ids, request, positions, q_starts, last):
         """Tokens `ids` at `positions` of the requests `request` (each a tensor (T,), a request's tokens together) through
-        the layers; self.ctx counts them already. Returns the logits of the tokens `last`."""
-        s, bf16 = self.shape, mbw.OP_GEMV_BF16
+        the layers; self.ctx counts them already. Returns the logits of the tokens `last`, none for None."""
+        s = self.shape
         T = ids.shape[0]
         page = self.table[request, positions // self.page_size].long()
         slots, pos32 = page * self.page_size + positions % self.page_size, positions.to(torch.int32)
         x = self.embedding[ids]
         for w, cache in zip(self.layers, self.caches):
-            qkv = mbw.gemv_fused(bf16, w["qkv"], None, x, norm_weight=w["norm1"]).view(T, -1, s.dim)
+            qkv = self.product(w["qkv"], x, norm=w["norm1"]).view(T, -1, s.dim)
             q, k, v = qkv.split((s.heads, s.kv_heads, s.kv_heads), 1)
             mbw.kv4_append(cache, k, v, slots, q=q, positions=pos32, cos_sin=self.cos_sin, q_out=q)
-            a = mbw.kv4_attention(cache, q, self.table, self.ctx, q_starts, workspace=self.attn_ws)
-            x = mbw.gemv_fused(bf16, w["o"], None, a.view(T, -1), residual=x)
-            g = mbw.gemv_fused(bf16, w["gate"], None, x, norm_weight=w["norm2"], up_weights=w["up"])
-            x = mbw.gemv_fused(bf16, w["down"], None, g, residual=x)
-        return mbw.gemv_fused(bf16, self.head, None, x[last], norm_weight=self.norm)
+            a = self.attend(cache, q, q_starts)
+            x = self.product(w["o"], a.view(T, -1), residual=x)
+            g = self.product(w["gate"], x, norm=w["norm2"], up=w["up"])
+            x = self.product(w["down"], g, residual=x)
+        return None if last is None else self.product(self.head, x[last], norm=self.norm)
 
-    def prompt(self, prompts):
-        """Fills the caches with the prompts (one list of ids per request) and returns their last logits' TokenLogprobs."""
+    def prompt(self, prompts, share=False):
+        """Fills the caches with the prompts (one list of ids per request) and returns their last logits' TokenLogprobs.
+        share: what they have in common at their beginning, in whole pages, is computed and held once, and the steps that
+        follow attend to it once for all requests."""
         dev = self.ids.device
         n = [len(p) for p in prompts]
         if len(n) != self.requests:
@@ -122,17 +156,35 @@ class Decoder:
             raise ValueError(f"a prompt of {max(n)} tokens is longer than max_tokens, {self.max_tokens}")
         if any(not 0 <= t < self.shape.vocab for p in prompts for t in p):
             raise ValueError(f"a prompt has an id outside 0 to {self.shape.vocab - 1}")
+        if self.shared:  # every request in its own pages again
+            self.table.copy_(self.own_table)
+            self.shared = 0
+        common = self.common(prompts) if share else 0
+        if common:  # as tokens of the first request, whose pages the others' tables then name
+            self.table[:, :common // self.page_size] = self.table[:1, :common // self.page_size].clone()
+            self.ctx.zero_()
+            self.ctx[:1] = common
+            at = torch.arange(common, device=dev)
+            self.forward(torch.tensor(prompts[0][:common], device=dev), torch.zeros_like(at), at,
+                         torch.tensor([0] + [common] * len(n), dtype=torch.int32, device=dev), None)
+            self.shared = common
         starts = [0]
         for x in n:
-            starts.append(starts[-1] + x)
-        ids = torch.tensor([t for p in prompts for t in p], device=dev)
-        request = torch.repeat_interleave(torch.arange(len(n), device=dev), torch.tensor(n, device=dev))
-        positions = torch.cat([torch.arange(x, device=dev) for x in n])
+            starts.append(starts[-1] + x - common)
+        ids = torch.tensor([t for p in prompts for t in p[common:]], device=dev)
+        request = torch.repeat_interleave(torch.arange(len(n), device=dev), torch.tensor(n, device=dev) - common)
+        positions = torch.cat([torch.arange(common, x, device=dev) for x in n])
         self.ctx.copy_(torch.tensor(n, dtype=torch.int32))
         self.longest = max(n)
         logits = self.forward(ids, request, positions, torch.tensor(starts, dtype=torch.int32, device=dev),
                               torch.tensor(starts[1:], device=dev) - 1)
         return self.choose(logits)
+
+    def common(self, prompts):
+        """Tokens that all prompts begin with, in whole pages; each has one more at least."""
+        most = min(len(p) for p in prompts) - 1
+        same = next((i for i in range(most) if any(p[i] != prompts[0][i] for p in prompts)), most)
+        return same // self.page_size * self.page_size
 
     def advance(self):
         """Counts a token more on the host, or raises where the longest request has no place for it."""
@@ -188,13 +240,18 @@ def main():
     ap.add_argument("--requests", type=int, default=1)
     ap.add_argument("--prompt", type=int, default=128, help="tokens of the longest prompt")
     ap.add_argument("--tokens", type=int, default=64)
+    ap.add_argument("--weights", choices=("bf16", "fp8"), default="bf16")
+    ap.add_argument("--shared", type=int, default=0, help="tokens in front of every prompt, the same ones")
     a = ap.parse_args()
     shape = SHAPES[a.model]
-    d = Decoder(shape, a.layers, a.requests, max_tokens=a.prompt + a.tokens + 2)
+    d = Decoder(shape, a.layers, a.requests, max_tokens=a.shared + a.prompt + a.tokens + 2, weights=a.weights)
     gen = torch.Generator().manual_seed(1)
     prompts = [torch.randint(shape.vocab, (max(1, a.prompt - 7 * i),), generator=gen).tolist() for i in range(a.requests)]
+    if a.shared:
+        front = torch.randint(shape.vocab, (a.shared,), generator=gen).tolist()
+        prompts = [front + p for p in prompts]
     d.tune()
-    d.prompt(prompts)
+    d.prompt(prompts, share=a.shared > 0)
     replay, out = d.graph(top_k=5)
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     torch.cuda.synchronize()
