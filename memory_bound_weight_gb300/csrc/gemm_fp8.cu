@@ -135,7 +135,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 
 
 
-// Eight outputs of a row, `left` of them inside the matrix; wide: at lies on 8.
+// silu to some 2^-21: e^-v as a power of two whose exponent's rounding is put back, and an approximate quotient. (With expf and
+// the exact quotient a gated tile of 61 rows took 9 us to write.)
+__device__ __forceinline__ float silu(float v) {
+    const float h = v * -1.44269504f, l = fmaf(v, -1.44269504f, -h) - v * 1.92596299e-8f;
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(h));
+    if (fabsf(h) < 127.f) e = fmaf(e, l * 0.693147181f, e);  // beyond, it is zero or infinite beside 1
+    return __fdividef(v, 1.f + e);
+}
+
+// Eight outputs of a row, `left` of them inside the matrix; wide: they lie on 16 bytes.
 __device__ __forceinline__ void put8(const Fp8Args& a, int64_t at, float* o, int left, bool wide) {
     if (wide && left >= 8 && !a.out_f32 && (!a.residual || ((uintptr_t)a.residual & 15) == 0)) {
         if (a.residual) {
@@ -161,6 +171,7 @@ __device__ __forceinline__ void put8(const Fp8Args& a, int64_t at, float* o, int
         }
 }
 
+constexpr int kMaxSplit = 4;  // pairs that share a tile's k
 constexpr int kAdders = 8, kThreads = (4 + kAdders) * 32;
 // Registers: 168 a thread at launch; then by warpgroup 56 for the issuers and 2 x 224 for the adders, 504 = 3 x 168.
 constexpr int kRegsLaunch = 168, kRegsIssuers = 56, kRegsAdders = 224;
@@ -427,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         o[i] = i & 1 ? x.y : x.x;
                         if (GLU) {
                             const float2 u = acc[32 + ((c + i) / 2) % 32];
-                            o[i] = silu_f32(o[i]) * (i & 1 ? u.y : u.x);
+                            o[i] = silu(o[i]) * (i & 1 ? u.y : u.x);
                         }
                     }
                     const int off = c >= 64 ? 64 + c : c;
@@ -443,30 +454,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
         if (warp >= 4) {
             const int m0 = tile_m0(first), rows = min(128, a.M - m0), n0 = tile_n(first) * OUT;
-            const int g0 = OUT / 8 * (int)(crank / 2) / split, groups = OUT / 8 * (int)(crank / 2 + 1) / split - g0;  // of 8 columns
-            const bool wide = a.N % 8 == 0;
+            const int g0 = OUT / 4 * (int)(crank / 2) / split, groups = OUT / 4 * (int)(crank / 2 + 1) / split - g0;  // of 4 columns
             for (int e = tid - 128; e < rows * groups; e += kAdders * 32) {
-                const int row = e / groups, c = (g0 + e % groups) * 8;
-                float o[2][8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[0][i] = o[1][i] = 0.f;
+                const int row = e / groups, c = (g0 + e % groups) * 4;
                 const uint32_t at = smem_at(reinterpret_cast<float*>(smem) + row * kPitch + c);
-                for (int q = 0; q < split; ++q) {
+                float4 x[kMaxSplit][GLU ? 2 : 1];  // all on their way before the first is added
+#pragma unroll
+                for (int q = 0; q < kMaxSplit; ++q) {
+                    if (q >= split) break;
                     uint32_t from;
                     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(2 * q + rank));
 #pragma unroll
-                    for (int u = 0; u < (GLU ? 4 : 2); ++u) {
-                        float4 x;
+                    for (int u = 0; u < (GLU ? 2 : 1); ++u)
                         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(from + (u & 1) * 16 + (u >> 1) * 512) : "memory");
-                        float* to = &o[u >> 1][(u & 1) * 4];
-                        to[0] += x.x, to[1] += x.y, to[2] += x.z, to[3] += x.w;
-                    }
+                                     : "=f"(x[q][u].x), "=f"(x[q][u].y), "=f"(x[q][u].z), "=f"(x[q][u].w) : "r"(from + u * 512) : "memory");
                 }
-                if (GLU)
+                float o[2][4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[0][i] = silu_f32(o[0][i]) * o[1][i];
-                put8(a, (int64_t)(m0 + row) * a.N + n0 + c, o[0], a.N - n0 - c, wide);
+                for (int i = 0; i < 4; ++i) o[0][i] = o[1][i] = 0.f;
+#pragma unroll
+                for (int q = 0; q < kMaxSplit; ++q)
+                    if (q < split)
+#pragma unroll
+                        for (int u = 0; u < (GLU ? 2 : 1); ++u) o[u][0] += x[q][u].x, o[u][1] += x[q][u].y, o[u][2] += x[q][u].z, o[u][3] += x[q][u].w;
+                const int64_t to = (int64_t)(m0 + row) * a.N + n0 + c;
+                const int left = a.N - n0 - c;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (GLU) o[0][i] = silu(o[0][i]) * o[1][i];
+                    if (a.residual && i < left) o[0][i] += bf16lo_to_f32(a.residual[to + i]);
+                }
+                if (a.N % 4 == 0 && left > 0 && !a.out_f32) {
+                    const __nv_bfloat162 h0 = __floats2bfloat162_rn(o[0][0], o[0][1]), h1 = __floats2bfloat162_rn(o[0][2], o[0][3]);
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + to) = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < left) store_out(a.y, to + i, o[0][i], a.out_f32);
+                }
             }
         }
     }
@@ -502,7 +527,7 @@ bool encode(CUtensorMap* map, const uint8_t* base, int64_t K, int64_t rows, int 
 
 // A tile's k is cut between pairs of a cluster where that leaves fewer blocks of k in a row: in blocks, of 0.4 us, what the
 // start of a CTA and what the join of a cluster take.
-constexpr int kMaxSplit = 4, kStart = 8, kJoin = 8;
+constexpr int kStart = 8, kJoin = 8;
 
 template <bool GLU>
 cudaError_t launch_for(const Fp8Args& a, cudaStream_t s) {
