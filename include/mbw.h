@@ -44,10 +44,11 @@
  *     produced by the preceding kernel, but the weights must not be: a kernel
  *     that writes weights must have completed before the GEMV is launched
  *     behind it. The library's own weight writers (mbw_quantize_int8_pc,
- *     mbw_repack_int4) see to this themselves: each ends with an empty kernel
- *     launched with plain stream ordering, which starts only after the writer
- *     has completed, so a GEMV queued next on the same stream reads the
- *     finished weights without a host synchronization.
+ *     mbw_quantize_fp8_b128, mbw_repack_int4) see to this themselves: each
+ *     ends with an empty kernel launched with plain stream ordering, which
+ *     starts only after the writer has completed, so a GEMV queued next on
+ *     the same stream reads the finished weights without a host
+ *     synchronization.
  *   - `workspace` / `ws_bytes` are accepted for split-K plans that need global
  *     scratch; a NULL or short workspace never fails a call (the plan falls
  *     back to a variant that needs none). mbw_workspace_bytes() gives the size.

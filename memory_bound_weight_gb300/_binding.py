@@ -740,6 +740,8 @@ def kv4_attention_shared(cache, q, block_table, ctx_lens, shared_len, q_starts=N
     page_size entries of the rows of block_table are equal, as far as each request's length goes. The shared pages are
     read and multiplied once for the queries of all requests. The other arguments and the result are kv4_attention's.
     workspace: from kv4_attention_shared_workspace; without one, shared pages are read for each request."""
+    if shared_len is None:
+        raise TypeError("shared_len must be a number of tokens")
     if _fast is None:
         _load_fast()
     if _fast and out is None and not getattr(_tls, "fp32", False):

@@ -148,12 +148,12 @@ __device__ __forceinline__ float silu(float v) {
     return __fdividef(v, 1.f + e);
 }
 
-// Eight outputs of a row, `left` of them inside the matrix; wide: they lie on 16 bytes.
-__device__ __forceinline__ void put8(const Fp8Args& a, int64_t at, float* o, int left, bool wide) {
-    if (wide && left >= 8 && !a.out_f32 && (!a.residual || ((uintptr_t)a.residual & 15) == 0)) {
+// Eight outputs of a row, `left` of them inside the matrix; wide: they and the residual's lie on 16 bytes as bf16, and `held`
+// are the residual's.
+__device__ __forceinline__ void put8(const Fp8Args& a, int64_t at, float* o, int left, bool wide, uint4 held) {
+    if (wide && left >= 8) {
         if (a.residual) {
-            const uint4 v = *reinterpret_cast<const uint4*>(a.residual + at);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t w[4] = {held.x, held.y, held.z, held.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[2 * i] += bf16lo_to_f32(w[i]), o[2 * i + 1] += bf16hi_to_f32(w[i]);
         }
@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 acc[64];  // 64 columns of the even CTA's W, 64 of the odd one's W or U
         uint32_t v[2][32];
         pdl_wait();
+        const bool wide = a.N % 8 == 0 && !a.out_f32 && ((uintptr_t)a.residual & 15) == 0;
         uint32_t it = 0, group = 0;
         for (long long t = first; t < tiles; t += stride) {
             const int m = tile_m0(t) + r, n0 = tile_n(t) * OUT + half * 64;
@@ -434,9 +435,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<float4*>(to + (c >= 64 ? 64 + c : c)) = make_float4(acc[c / 2].x, acc[c / 2].y, acc[c / 2 + 1].x, acc[c / 2 + 1].y);
             } else if (row) {
                 const int64_t to = (int64_t)m * a.N + n0;
-                const bool wide = a.N % 8 == 0;
+                constexpr int COLUMNS = GLU ? 64 : 128;
+                // The residual's values are read some ahead: it may be the output, and no load is moved before a store by itself
+                // (4096 x 3584 x 18944 with a residual: 228 us one by one, 222 four ahead, 221 eight, 235 the whole row, whose
+                // registers do not fit).
+                constexpr int HELD = 8;
+                uint4 held[HELD];
 #pragma unroll
-                for (int c = 0; c < (GLU ? 64 : 128); c += 8) {
+                for (int c = 0; c < COLUMNS; c += 8) {
+                    if (c / 8 % HELD == 0) {
+#pragma unroll
+                        for (int i = 0; i < HELD; ++i) {
+                            const int off = c + 8 * i >= 64 ? 64 + c + 8 * i : c + 8 * i;
+                            held[i] = make_uint4(0, 0, 0, 0);
+                            if (wide && a.residual && a.N - n0 - off >= 8) held[i] = *reinterpret_cast<const uint4*>(a.residual + to + off);
+                        }
+                    }
                     float o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -448,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const int off = c >= 64 ? 64 + c : c;
-                    put8(a, to + off, o, a.N - n0 - off, wide);
+                    put8(a, to + off, o, a.N - n0 - off, wide, held[c / 8 % HELD]);
                 }
             }
         }
@@ -461,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp >= 4) {
             const int m0 = tile_m0(first), rows = min(128, a.M - m0), n0 = tile_n(first) * OUT;
             const int g0 = OUT / 4 * (int)(crank / 2) / split, groups = OUT / 4 * (int)(crank / 2 + 1) / split - g0;  // of 4 columns
+            const bool four = a.N % 4 == 0 && !a.out_f32 && ((uintptr_t)a.residual & 7) == 0;
             for (int e = tid - 128; e < rows * groups; e += kAdders * 32) {
                 const int row = e / groups, c = (g0 + e % groups) * 4;
                 const uint32_t at = smem_at(reinterpret_cast<float*>(smem) + row * kPitch + c);
@@ -475,6 +490,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                                      : "=f"(x[q][u].x), "=f"(x[q][u].y), "=f"(x[q][u].z), "=f"(x[q][u].w) : "r"(from + u * 512) : "memory");
                 }
+                const int64_t to = (int64_t)(m0 + row) * a.N + n0 + c;
+                const int left = a.N - n0 - c;
+                float res[4] = {0.f, 0.f, 0.f, 0.f};
+                if (a.residual) {
+                    if (four && left > 0) {
+                        const uint2 h = *reinterpret_cast<const uint2*>(a.residual + to);
+                        res[0] = bf16lo_to_f32(h.x), res[1] = bf16hi_to_f32(h.x), res[2] = bf16lo_to_f32(h.y), res[3] = bf16hi_to_f32(h.y);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < left) res[i] = bf16lo_to_f32(a.residual[to + i]);
+                    }
+                }
                 float o[2][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[0][i] = o[1][i] = 0.f;
@@ -483,14 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (q < split)
 #pragma unroll
                         for (int u = 0; u < (GLU ? 2 : 1); ++u) o[u][0] += x[q][u].x, o[u][1] += x[q][u].y, o[u][2] += x[q][u].z, o[u][3] += x[q][u].w;
-                const int64_t to = (int64_t)(m0 + row) * a.N + n0 + c;
-                const int left = a.N - n0 - c;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (GLU) o[0][i] = silu(o[0][i]) * o[1][i];
-                    if (a.residual && i < left) o[0][i] += bf16lo_to_f32(a.residual[to + i]);
+                    if (a.residual) o[0][i] += res[i];
                 }
-                if (a.N % 4 == 0 && left > 0 && !a.out_f32) {
+                if (four && left > 0) {
                     const __nv_bfloat162 h0 = __floats2bfloat162_rn(o[0][0], o[0][1]), h1 = __floats2bfloat162_rn(o[0][2], o[0][3]);
                     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + to) = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
                 } else {

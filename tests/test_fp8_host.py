@@ -194,3 +194,8 @@ def test_workspaces(L):
         assert L.mbw_kv4_attention_shared_workspace_bytes(*args) == 0
     for d in (64, 128, 256):
         assert L.mbw_kv4_attention_shared_workspace_bytes(d, 10, 8) >= L.mbw_kv4_attention_workspace_bytes(d)
+
+
+def test_shared_attention_needs_its_length():
+    with pytest.raises(TypeError, match="shared_len"):
+        mbw.kv4_attention_shared(None, None, None, None, None)
