@@ -24,7 +24,13 @@
 // Where there are fewer tiles than pairs, k is cut between up to four pairs of a
 // cluster, whose sums are joined in order through their shared memory.
 //
-// Up to 16 rows of X are gemv_fp8.cu's.
+// What bounds it: a block of k takes a pair some 0.38 us, 650 clocks of products and, as
+// there are but two accumulators, a part of the way from a product's end to the adders
+// and back (commit 380, reading 290, arrival 250). 4096 x 3584 x 18944 is 212 us, 2620
+// TFLOP/s, of which the products alone would take 145; without the additions it takes 202,
+// without any reading of accumulators 188, and its copies alone 158 (13.8 TB/s from L2).
+//
+// Up to 128 rows of X are a second kernel's (Few below), up to 8, or 16, gemv_fp8.cu's.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -175,6 +181,7 @@ __device__ __forceinline__ void put8(const Fp8Args& a, int64_t at, float* o, int
 }
 
 constexpr int kMaxSplit = 4;  // pairs that share a tile's k
+constexpr int kFewSplit = 8;  // CTAs that share a tile's k, where a CTA takes all rows of X
 constexpr int kAdders = 8, kThreads = (4 + kAdders) * 32;
 // Registers: 168 a thread at launch; then by warpgroup 56 for the issuers and 2 x 224 for the adders, 504 = 3 x 168.
 constexpr int kRegsLaunch = 168, kRegsIssuers = 56, kRegsAdders = 224;
@@ -534,6 +541,326 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
+// Up to NX = 64 or 128 rows of X: the weights are the products' rows, 128 a CTA, and X their columns, so that no product is
+// of rows that are not there; a column of Y is a lane of the accumulator, of one weight scale a block. No pairs: X is small,
+// and a CTA has a tile of W (gated: and U's) for itself. Two or four accumulators are in turn. k is cut between up to eight
+// CTAs of a cluster.
+// What bounds it: where each SM has one tile, W's stream from HBM and the start before it (64 x 152064 x 3584 97 us, 5.6 TB/s;
+// 64 x 4608 x 3584 8.6 us, 3.5 of them a start and 2 a join); a block of k takes 0.26 us for 64 rows, the issue of products
+// and the adders' way through waits, loads and factors, and 0.42 for 128, most of it the adders'.
+template <bool GLU, int NX>
+struct Few {
+    static constexpr int MATS = GLU ? 2 : 1, STAGE = MATS * 128 * 128 + NX * 128, DEPTH = 208 * 1024 / STAGE < 8 ? 208 * 1024 / STAGE : 8;
+    static constexpr int COLS = MATS * NX, NACC = 512 / COLS < 4 ? 512 / COLS : 4;  // TMEM columns of an accumulator, accumulators
+    static constexpr int GROUP = 4 * COLS * 4;                                      // factors of four blocks by [block][matrix][row of X]
+    static constexpr int OFF_FACTOR = DEPTH * STAGE, OFF_BAR = OFF_FACTOR + kGroups * GROUP;
+    static constexpr int SMEM = OFF_BAR + (2 * DEPTH + 2 * NACC + 2 * kGroups) * 8 + 16 + 1024;
+    static_assert(SMEM <= 227 * 1024, "");
+    static_assert(COLS * 128 * 4 <= OFF_FACTOR, "sums lie over the ring, which is drained then");
+};
+
+template <bool GLU, int NX>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp8_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                        const __grid_constant__ CUtensorMap map_u, const Fp8Args a) {
+    using L = Few<GLU, NX>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (-smem_at(smem_raw) & 1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+    uint64_t *empty = full + L::DEPTH, *sfull = empty + L::DEPTH, *sempty = sfull + L::NACC, *ffull = sempty + L::NACC, *fempty = ffull + kGroups;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fempty + kGroups);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t crank, csize;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+    const int split = csize;  // CTAs that share a tile's k
+    bool ok = true;
+    auto cluster_sync = [] { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); };
+
+    if (tid == 0) {
+        for (int i = 0; i < L::DEPTH; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
+        for (int i = 0; i < L::NACC; ++i) bar_init(&sfull[i], 1), bar_init(&sempty[i], kAdders);
+        for (int i = 0; i < kGroups; ++i) bar_init(&ffull[i], 1), bar_init(&fempty[i], kAdders);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+
+    // ---- a CTA takes whole tiles of 128 columns of Y in turn, or of one tile its share of the blocks of k ----
+    const int KB = a.K / 128, tiles = (a.N + 127) / 128, first = blockIdx.x / csize, stride = gridDim.x / csize;
+    const int kb0 = (int)((long long)KB * crank / split), kb1 = (int)((long long)KB * (crank + 1) / split);
+
+    if (warp < 4) {
+        registers<kRegsIssuers>(false);
+        if (warp == 0) {
+            // -------------------------------------------------------- copies ----
+            const bool leader = elect();
+            auto weights = [&](uint32_t s, int kb, int n0) {
+                bar_expect(&full[s], L::STAGE);
+                tma_2d(smem + s * L::STAGE, &map_w, kb * 128, n0, &full[s]);
+                if (GLU) tma_2d(smem + s * L::STAGE + 128 * 128, &map_u, kb * 128, n0, &full[s]);
+            };
+            auto rows = [&](uint32_t s, int kb) { tma_2d(smem + s * L::STAGE + L::MATS * 128 * 128, &map_x, kb * 128, 0, &full[s]); };
+            uint32_t it = 0, s = 0, turn = 0;
+            for (int t = first; t < tiles && ok; t += stride) {
+                int kb = kb0;
+                if (t == first) {  // weights do not depend on the kernel before: the ring is filled with them, then X is waited for
+                    const int pre = min(L::DEPTH, kb1 - kb0);
+                    if (leader)
+                        for (int i = 0; i < pre; ++i) weights(i, kb + i, t * 128);
+                    __syncwarp();
+                    pdl_wait();
+                    if (leader)
+                        for (int i = 0; i < pre; ++i) rows(i, kb + i);
+                    __syncwarp();
+                    it = pre, kb += pre, s = pre % L::DEPTH, turn = pre / L::DEPTH;
+                }
+                for (; kb < kb1; ++kb, ++it) {
+                    if (turn) bar_wait(&empty[s], (turn - 1) & 1, ok);
+                    if (!ok) break;
+                    if (leader) weights(s, kb, t * 128), rows(s, kb);
+                    __syncwarp();
+                    if (++s == L::DEPTH) s = 0, ++turn;
+                }
+            }
+            if (!ok)  // no copy lands behind the CTA's end
+                for (uint32_t j = it > L::DEPTH ? it - L::DEPTH : 0; j < it; ++j) {
+                    bool o = true;
+                    bar_wait(&full[j % L::DEPTH], (j / L::DEPTH) & 1, o);
+                }
+        } else if (warp <= 2) {
+            // ------------------------------------------------------ products ----
+            // by two warps in turn, since the issue of a block's takes a warp longer than the tensor pipe (64 rows, blocks of one
+            // CTA: one warp 0.34 us, two 0.27)
+            const bool leader = elect();
+            constexpr uint32_t ID = idesc(128, NX);
+            const uint32_t blocks = (uint32_t)((tiles - first + stride - 1) / stride) * (uint32_t)(kb1 - kb0);
+            uint32_t s = warp - 1, turn = 0;  // the stage, and the ring's turns before it
+            for (uint32_t it = warp - 1; it < blocks; it += 2) {
+                const uint32_t b = it % L::NACC;
+                if (s >= L::DEPTH) s -= L::DEPTH, ++turn;
+                // The accumulator first: where it is free, block it - NACC has been added, so that the stage's turn before,
+                // which may have been the other warp's, is over, and the parity waited for next is this turn's.
+                static_assert(L::NACC % 2 == 0 && L::DEPTH >= L::NACC, "");
+                if (it >= L::NACC) bar_wait(&sempty[b], (it / L::NACC - 1) & 1, ok);
+                bar_wait(&full[s], turn & 1, ok);
+                fence_after();
+                if (leader) {
+                    if (ok) {
+                        const uint64_t dw = desc(smem_at(smem + s * L::STAGE)), dx = dw + L::MATS * 128 * 128 / 16;
+#pragma unroll
+                        for (int u = 0; u < L::MATS; ++u)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // 32 codes each: 32 bytes further inside the swizzle atom
+                                mma(tmem + b * L::COLS + u * NX, dw + u * 128 * 128 / 16 + 2 * k, dx + 2 * k, ID, k > 0);
+                    }
+                    commit(&sfull[b]);
+                    commit(&empty[s]);
+                }
+                __syncwarp();
+                s += 2;
+            }
+        } else {
+            // ------------------------------------------------------- factors ----
+            const bool by4 = KB % 4 == 0 && (((uintptr_t)a.xs | (uintptr_t)a.ws | (GLU ? (uintptr_t)a.us : 0)) & 15) == 0;
+            auto fetch = [&](const float* from, int kb, bool there) {
+                if (by4) return there ? *reinterpret_cast<const float4*>(from + kb) : make_float4(0.f, 0.f, 0.f, 0.f);
+                return make_float4(there ? from[kb] : 0.f, there && kb + 1 < KB ? from[kb + 1] : 0.f, there && kb + 2 < KB ? from[kb + 2] : 0.f,
+                                   there && kb + 3 < KB ? from[kb + 3] : 0.f);
+            };
+            pdl_wait();
+            uint32_t turn = 0;
+            for (int t = first; t < tiles; t += stride) {
+                const float *wsp = a.ws + (int64_t)t * KB, *usp = GLU ? a.us + (int64_t)t * KB : wsp;
+                for (int kb = kb0 & ~3; kb < kb1; kb += 4, ++turn) {
+                    const float4 ws = fetch(wsp, kb, true), us = GLU ? fetch(usp, kb, true) : ws;
+                    float4 xs[NX / 32];
+#pragma unroll
+                    for (int i = 0; i < NX / 32; ++i) xs[i] = fetch(a.xs + (int64_t)(i * 32 + lane) * KB, kb, i * 32 + lane < a.M);
+                    const uint32_t slot = turn % kGroups;
+                    if (turn >= kGroups) bar_wait(&fempty[slot], (turn / kGroups - 1) & 1, ok);
+                    float* to = reinterpret_cast<float*>(smem + L::OFF_FACTOR + slot * L::GROUP) + lane;
+#pragma unroll
+                    for (int i = 0; i < NX / 32; ++i)
+#pragma unroll
+                        for (int u = 0; u < L::MATS; ++u) {
+                            const float4 f = u ? us : ws;
+                            float* at = to + u * NX + 32 * i;
+                            at[0] = xs[i].x * f.x, at[L::COLS] = xs[i].y * f.y, at[2 * L::COLS] = xs[i].z * f.z, at[3 * L::COLS] = xs[i].w * f.w;
+                        }
+                    __syncwarp();
+                    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(&ffull[slot])) : "memory");
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------- sums by their scales ----
+        registers<kRegsAdders>(true);
+        // A thread's columns are read in pieces, the next on its way under the additions of the one before: whole blocks, or
+        // of the gated form of 128 rows, whose sums leave no registers, a quarter of one.
+        constexpr int C = NX / 2, CHUNKS = C / 32, THIRTY = L::MATS * CHUNKS;  // columns of a thread; 32s of them, in all
+        constexpr int P = THIRTY <= 2 ? THIRTY : 1, PIECES = THIRTY / P;       // 32s of a piece
+        const int quarter = warp & 3, half = (warp - 4) >> 2, r = quarter * 32 + lane;
+        const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16) + half * C;
+        auto column = [](int i) { return i / CHUNKS * NX + i % CHUNKS * 32; };  // of the i-th 32, among an accumulator's
+        float2 acc[THIRTY * 16];
+        uint32_t v[2][P * 32];
+        pdl_wait();
+        uint32_t it = 0, group = 0;
+        auto fetch = [&](uint32_t(&to)[P * 32], uint32_t at, int j) {
+#pragma unroll
+            for (int h = 0; h < P; ++h) ld<32>(to + 32 * h, at + column(j * P + h));
+        };
+        bool begun;  // the next block's first piece is on its way
+        auto block = [&](int kb, uint32_t(&v0)[P * 32], uint32_t(&v1)[P * 32]) {
+            const uint32_t b = it % L::NACC, next = (it + 1) % L::NACC;
+            if (!begun) {
+                bar_wait(&sfull[b], (it / L::NACC) & 1, ok);
+                fence_after();
+                fetch(v0, my + b * L::COLS, 0);
+            }
+            const uint32_t slot = group % kGroups;
+            if ((kb & 3) == 0 || kb == kb0) bar_wait(&ffull[slot], (group / kGroups) & 1, ok);
+            const float* f = reinterpret_cast<const float*>(smem + L::OFF_FACTOR + slot * L::GROUP) + (kb & 3) * L::COLS + half * C;
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j) {
+                auto& now = j & 1 ? v1 : v0;
+                auto& then = j & 1 ? v0 : v1;
+                const uint32_t ready = j + 1 == PIECES && kb + 1 < kb1 ? bar_ask(&sfull[next], ((it + 1) / L::NACC) & 1) : 0;
+                wait_ld<P * 32>(now);
+                if (j + 1 < PIECES) {
+                    fetch(then, my + b * L::COLS, j + 1);
+                } else {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(smem_at(&sempty[b]));
+                    begun = all_of(ready);
+                    if (begun) {
+                        fence_after();
+                        fetch(then, my + next * L::COLS, 0);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < P * 32; c += 4) {
+                    const float4 ff = *reinterpret_cast<const float4*>(f + column(j * P + c / 32) + c % 32);
+                    float2* to = acc + 16 * j * P + c / 2;
+                    to[0] = fma2(make_float2(__uint_as_float(now[c]), __uint_as_float(now[c + 1])), make_float2(ff.x, ff.y), to[0]);
+                    to[1] = fma2(make_float2(__uint_as_float(now[c + 2]), __uint_as_float(now[c + 3])), make_float2(ff.z, ff.w), to[1]);
+                }
+            }
+            if ((kb & 3) == 3 || kb + 1 == kb1) {
+                __syncwarp();
+                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(&fempty[slot])) : "memory");
+                ++group;
+            }
+            ++it;
+        };
+        for (int t = first; t < tiles; t += stride) {
+#pragma unroll
+            for (int c = 0; c < THIRTY * 16; ++c) acc[c] = make_float2(0.f, 0.f);
+            begun = false;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                block(kb, v[0], v[1]);
+                if (PIECES % 2 == 0) continue;  // the next block's first piece lies in the first again
+                if (++kb == kb1) break;
+                block(kb, v[1], v[0]);
+            }
+            if (split > 1) {  // into shared memory, [matrix][row of X][column of Y]
+                float* to = reinterpret_cast<float*>(smem) + half * C * 128 + r;
+#pragma unroll
+                for (int j = 0; j < THIRTY; ++j)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) to[(column(j) + c) * 128] = c & 1 ? acc[16 * j + c / 2].y : acc[16 * j + c / 2].x;
+            } else if (t * 128 + r < a.N) {
+                constexpr int HELD = 16;  // of the residual, ahead of the stores
+                uint16_t held[HELD];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int m = half * C + c;
+                    const int64_t to = (int64_t)m * a.N + t * 128 + r;
+                    if (c % HELD == 0)
+#pragma unroll
+                        for (int i = 0; i < HELD; ++i) held[i] = a.residual && m + i < a.M ? a.residual[to + (int64_t)i * a.N] : (uint16_t)0;
+                    float o = c & 1 ? acc[c / 2].y : acc[c / 2].x;
+                    if constexpr (GLU) o = silu(o) * (c & 1 ? acc[CHUNKS * 16 + c / 2].y : acc[CHUNKS * 16 + c / 2].x);
+                    if (a.residual) o += bf16lo_to_f32(held[c % HELD]);
+                    if (m < a.M) store_out(a.y, to, o, a.out_f32);
+                }
+            }
+        }
+    }
+    if (split > 1) {
+        // ---- the CTAs' sums in their order, each CTA a share of the rows of X ----
+        fence_before();
+        cluster_sync();
+        fence_after();
+        if (warp >= 4) {
+            const int m0 = a.M * (int)crank / split, items = (a.M * (int)(crank + 1) / split - m0) * 32;
+            const bool four = a.N % 4 == 0 && !a.out_f32 && ((uintptr_t)a.residual & 7) == 0;
+            for (int e = tid - 128; e < items; e += kAdders * 32) {
+                const int m = m0 + e / 32, c = e % 32 * 4, left = a.N - first * 128 - c;
+                const int64_t to = (int64_t)m * a.N + first * 128 + c;
+                const uint32_t at = smem_at(reinterpret_cast<float*>(smem) + m * 128 + c);
+                float res[4] = {0.f, 0.f, 0.f, 0.f};
+                if (a.residual) {
+                    if (four && left > 0) {
+                        const uint2 h = *reinterpret_cast<const uint2*>(a.residual + to);
+                        res[0] = bf16lo_to_f32(h.x), res[1] = bf16hi_to_f32(h.x), res[2] = bf16lo_to_f32(h.y), res[3] = bf16hi_to_f32(h.y);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < left) res[i] = bf16lo_to_f32(a.residual[to + i]);
+                    }
+                }
+                float4 x[kFewSplit][L::MATS];  // all on their way before the first is added
+#pragma unroll
+                for (int q = 0; q < kFewSplit; ++q) {
+                    if (q >= split) break;
+                    uint32_t from;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(q));
+#pragma unroll
+                    for (int u = 0; u < L::MATS; ++u)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(x[q][u].x), "=f"(x[q][u].y), "=f"(x[q][u].z), "=f"(x[q][u].w) : "r"(from + u * NX * 512) : "memory");
+                }
+                float o[2][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[0][i] = o[1][i] = 0.f;
+#pragma unroll
+                for (int q = 0; q < kFewSplit; ++q)
+                    if (q < split)
+#pragma unroll
+                        for (int u = 0; u < L::MATS; ++u) o[u][0] += x[q][u].x, o[u][1] += x[q][u].y, o[u][2] += x[q][u].z, o[u][3] += x[q][u].w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (GLU) o[0][i] = silu(o[0][i]) * o[1][i];
+                    if (a.residual) o[0][i] += res[i];
+                }
+                if (four && left > 0) {
+                    const __nv_bfloat162 h0 = __floats2bfloat162_rn(o[0][0], o[0][1]), h1 = __floats2bfloat162_rn(o[0][2], o[0][3]);
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + to) = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < left) store_out(a.y, to + i, o[0][i], a.out_f32);
+                }
+            }
+        }
+        cluster_sync();  // no CTA ends while another reads its sums
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
 // ------------------------------------------------------------ host side ----
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -557,29 +884,33 @@ bool encode(CUtensorMap* map, const uint8_t* base, int64_t K, int64_t rows, int 
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A tile's k is cut between pairs of a cluster where that leaves fewer blocks of k in a row: in blocks, of 0.4 us, what the
-// start of a CTA and what the join of a cluster take.
-constexpr int kStart = 8, kJoin = 8;
+// What a kernel's launches need to know of it, asked for once per device: whether it has the registers of its split, and how
+// many clusters of 1, 2, ... shares of a tile's k the device holds at once.
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const Fp8Args);
+struct Known {
+    std::atomic<int> regs{0};
+    std::atomic<int> held[16][kFewSplit];
+};
 
-template <bool GLU>
-cudaError_t launch_for(const Fp8Args& a, cudaStream_t s) {
+// Tiles whose k is cut between up to `most` shares of `unit` CTAs each, where that leaves fewer blocks of k in a row: in
+// blocks, `begin` is what the start of a CTA takes, `join` the join of a cluster.
+cudaError_t launch_cut(Kernel fn, Known& known, int smem, int unit, int most, int64_t tiles, int begin, int join, int x_rows, const Fp8Args& a,
+                       cudaStream_t s) {
     CUtensorMap mx, mw, mu;
-    if (!encode(&mx, a.X, a.K, a.M, 128) || !encode(&mw, a.W, a.K, a.N, 128) || !encode(&mu, GLU ? a.U : a.W, a.K, a.N, 128))
+    if (!encode(&mx, a.X, a.K, a.M, x_rows) || !encode(&mw, a.W, a.K, a.N, 128) || !encode(&mu, a.U ? a.U : a.W, a.K, a.N, 128))
         return cudaErrorInvalidValue;
-    auto* fn = gemm_fp8_kernel<GLU>;
-    const cudaError_t err = kv4_allow_smem((const void*)fn, kSmem);
+    const cudaError_t err = kv4_allow_smem((const void*)fn, smem);
     if (err != cudaSuccess) return err;
-    static std::atomic<int> regs{0};
-    if (!regs.load(std::memory_order_relaxed)) {
+    if (!known.regs.load(std::memory_order_relaxed)) {
         cudaFuncAttributes attr;
         const cudaError_t e = cudaFuncGetAttributes(&attr, fn);
         if (e != cudaSuccess) return e;
-        regs.store(attr.numRegs, std::memory_order_relaxed);
+        known.regs.store(attr.numRegs, std::memory_order_relaxed);
     }
-    if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return cudaErrorLaunchOutOfResources;  // the split would wait forever
+    if (known.regs.load(std::memory_order_relaxed) < kRegsLaunch) return cudaErrorLaunchOutOfResources;  // the split would wait forever
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attrs[2];
     attrs[0].id = cudaLaunchAttributeClusterDimension;
@@ -587,43 +918,60 @@ cudaError_t launch_for(const Fp8Args& a, cudaStream_t s) {
     attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attrs;
-    // Clusters of 1 to 4 pairs that the device holds at once, asked for once per device.
-    static std::atomic<int> known[16][kMaxSplit];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256)), KB = a.K / 128;
+    const int64_t KB = a.K / 128;
     int split = 1, held = 1;
     int64_t best = INT64_MAX;
-    for (int n = 1; n <= kMaxSplit && n <= KB; ++n) {
-        int h = dev < 16 ? known[dev][n - 1].load(std::memory_order_relaxed) : 0;
+    for (int n = 1; n <= most && n <= KB; ++n) {
+        int h = dev < 16 ? known.held[dev][n - 1].load(std::memory_order_relaxed) : 0;
         if (!h) {
-            attrs[0].val.clusterDim.x = 2 * n;
-            cfg.gridDim = dim3(2 * n, 1, 1);
+            attrs[0].val.clusterDim.x = unit * n;
+            cfg.gridDim = dim3(unit * n, 1, 1);
             cfg.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&h, fn, &cfg);
             if (e != cudaSuccess) return e;
             if (h < 1) h = 1;
-            if (dev < 16) known[dev][n - 1].store(h, std::memory_order_relaxed);
+            if (dev < 16) known.held[dev][n - 1].store(h, std::memory_order_relaxed);
         }
         const int64_t waves = (tiles + h - 1) / h, blocks = (KB + n - 1) / n;
-        const int64_t cost = n == 1 ? waves * blocks + kStart : waves * (blocks + kStart) + kJoin;
+        const int64_t cost = n == 1 ? waves * blocks + begin : waves * (blocks + begin) + join;
         if (cost < best) best = cost, split = n, held = h;
     }
     const int64_t clusters = split > 1 || tiles < held ? tiles : held;
-    attrs[0].val.clusterDim.x = 2 * split;
-    cfg.gridDim = dim3((unsigned)(2 * split * clusters), 1, 1);
+    attrs[0].val.clusterDim.x = unit * split;
+    cfg.gridDim = dim3((unsigned)(unit * split * clusters), 1, 1);
     cfg.numAttrs = 2;
     count_launch();
     return cudaLaunchKernelEx(&cfg, fn, mx, mw, mu, a);
 }
 
+template <bool GLU>
+cudaError_t launch_pairs(const Fp8Args& a, cudaStream_t s) {
+    static Known known;
+    const int64_t tiles = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256));
+    return launch_cut(gemm_fp8_kernel<GLU>, known, kSmem, 2, kMaxSplit, tiles, 8, 8, 128, a, s);  // a block takes 0.4 us
+}
+template <bool GLU, int NX>
+cudaError_t launch_few(const Fp8Args& a, cudaStream_t s) {
+    static Known known;
+    return launch_cut(gemm_fp8_few_kernel<GLU, NX>, known, Few<GLU, NX>::SMEM, 1, kFewSplit, ((int64_t)a.N + 127) / 128, 16, 8, NX, a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_fp8(const Fp8Args& a, cudaStream_t s) {
-    // Up to 16 rows as a stream of W on mma.sync: 16 rows, 3584 x 18944: 19.6 us against 24.2 (one row, 2048 x 2048: 2.6, 7.0).
-    if (a.M <= 16) return launch_gemv_fp8(a, s);
-    return a.U ? launch_for<true>(a, s) : launch_for<false>(a, s);
+    // Few rows as a stream of W on mma.sync, up to 8, whose products cost it no more than one row's (2048 x 2048 2.6 us, here
+    // 4.6; 18944 x 3584 14.0, 15.5), and up to 16 of smaller weights (2048 x 2048 3.1, 4.6; 4608 x 3584 6.5, 7.9; gated 5632 x
+    // 2048, 23 MB, 9.9, 10.1; but 2560 x 9728, 25 MB, 12.2, 8.8; 3584 x 18944 19.7, 15.3; gated 18944 x 3584 39, 27.5).
+    const int64_t weights = (int64_t)a.N * a.K * (a.U ? 2 : 1);
+    if (a.M <= 8 || (a.M <= 16 && weights < 20000000)) return launch_gemv_fp8(a, s);
+    // Up to 128 rows with the weights as the products' rows (128 x 3584 x 18944: 20.0 us, by pairs 26.7; 100 x 18944 x 3584
+    // gated 33, 36).
+    if (a.M <= 64) return a.U ? launch_few<true, 64>(a, s) : launch_few<false, 64>(a, s);
+    if (a.M <= 128) return a.U ? launch_few<true, 128>(a, s) : launch_few<false, 128>(a, s);
+    return a.U ? launch_pairs<true>(a, s) : launch_pairs<false>(a, s);
 }
 
 int gemm_fp8_take_fault() {

@@ -119,6 +119,54 @@ def test_gated_product_with_a_residual(m, n, k):
     check(out, want, mass * eps + want.abs() * 2.0 ** -24 + half_step(want), "in place")
 
 
+FEW = [(9, 9001, 2560), (16, 2560, 9728), (17, 3584, 1024), (24, 20011, 640), (61, 5632, 2048), (64, 21000, 384), (64, 1000, 9728),
+       (65, 20480, 512), (90, 300, 18944), (127, 2049, 1792), (128, 19600, 640), (128, 3584, 3584)]
+
+
+@pytest.mark.parametrize("m,n,k", FEW)
+def test_few_rows_of_larger_matrices(m, n, k):
+    """Weights of more than one tile a CTA, of one, and cut along k; residuals on any bytes that a tensor of bf16 lies on."""
+    g = gen(m + n + 5 * k)
+    x, xs, w, sc = operands(g, m, n, k)
+    _, _, u, su = operands(g, 1, n, k)
+    y, mass, eps = exact(x, xs, w, sc)
+    z, mass_z, _ = exact(x, xs, u, su)
+    check(mbw.gemm_fp8_b128(x, xs, w, sc), y, mass * eps + half_step(y), "bf16")
+    with mbw.output_fp32():
+        check(mbw.gemm_fp8_b128(x, xs, w, sc), y, mass * eps + 2.0 ** -149, "fp32")
+    act = y * torch.sigmoid(y)  # the tolerance is derived in test_gated_product_with_a_residual
+    tol = 1.1 * mass * eps * z.abs() + act.abs() * mass_z * eps + 1.1 * mass * mass_z * eps * eps + (act * z).abs() * 2.0 ** -20
+    for off in (0, 1, 4):
+        r = torch.randn(m * n + off, generator=g, device="cuda").bfloat16()[off:].view(m, n)
+        want = y + r.double()
+        check(mbw.gemm_fp8_b128(x, xs, w, sc, residual=r), want, mass * eps + want.abs() * 2.0 ** -24 + half_step(want), "residual")
+        want = act * z + r.double()
+        got = mbw.gemm_fp8_b128(x, xs, w, sc, residual=r, up_weights=u, up_scales=su)
+        check(got, want, tol + r.double().abs() * 2.0 ** -23 + half_step(want), "gated, residual")
+        assert torch.equal(got, mbw.gemm_fp8_b128(x, xs, w, sc, residual=r, up_weights=u, up_scales=su))
+    out = r.clone()
+    mbw.gemm_fp8_b128(x, xs, w, sc, out=out, residual=out)  # in place
+    want = y + r.double()
+    check(out, want, mass * eps + want.abs() * 2.0 ** -24 + half_step(want), "in place")
+
+
+@pytest.mark.parametrize("m", [16, 64, 100])
+def test_gated_products_one_behind_the_other(m):
+    """Every SM with a tile of its own, launches that overlap, a ring whose stages the issuing warps take in turn: always the same."""
+    g = gen(m)
+    n, k = 18944, 3584
+    x, xs, w, sc = operands(g, m, n, k)
+    _, _, u, su = operands(g, 1, n, k)
+    first = mbw.gemm_fp8_b128(x, xs, w, sc, up_weights=u, up_scales=su)
+    rest = [mbw.gemm_fp8_b128(x, xs, w, sc, up_weights=u, up_scales=su) for _ in range(40)]
+    assert all(torch.equal(first, y) for y in rest)
+    a, mass_a, eps = exact(x, xs, w[-384:], sc[-3:])
+    b, mass_b, _ = exact(x, xs, u[-384:], su[-3:])
+    want = a * torch.sigmoid(a) * b  # the tolerance is derived in test_gated_product_with_a_residual
+    tol = 1.1 * mass_a * eps * b.abs() + (a * torch.sigmoid(a)).abs() * mass_b * eps + 1.1 * mass_a * mass_b * eps * eps
+    check(first[:, -384:], want, tol + want.abs() * 2.0 ** -20 + half_step(want))
+
+
 def test_no_rows_or_no_outputs():
     x, xs, w, sc = operands(gen(1), 4, 130, 256)
     assert mbw.gemm_fp8_b128(x[:0], xs[:0], w, sc).shape == (0, 130)
