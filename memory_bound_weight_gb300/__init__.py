@@ -1,7 +1,9 @@
 """GB300 (sm_103a) weight-streaming GEMV library: y = W.x and Y = X.W^T with
 BF16, INT4 group-64, AWQ-style INT4 group-128 and symmetric per-channel INT8
-weights; and, around these products in a decode step, a 4-bit paged key/value
-cache with its attention, and the log probabilities of tokens.
+weights; products of any number of rows in 8-bit floating point with a scale
+for each block of 128; and, around these products in a decode step, a 4-bit
+paged key/value cache with its attention, also behind a prefix that requests
+share, and the log probabilities of tokens.
 
 The compute path is libmbw.so (C ABI in include/mbw.h); this package is its
 binding. Submodules ``inputs`` and ``workloads`` (synthetic data and byte
