@@ -382,31 +382,59 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_attention_kernel(Kv4AttnArgs
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float inv[2];
+            if constexpr (SHARED) {
+                // Both columns' loads go together, two parts at a time, the first beside the log sums: a join is a few loads
+                // behind one another, not a few a column and part.
+                constexpr int PARTS = 2;
+                long long at[2];
+                bool in[2];
+                float v[PARTS][2][D / 8];
+                auto fetch = [&](int p) {
+#pragma unroll
+                    for (int t = 0; t < PARTS; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int i = 0; i < D / 8; ++i)
+                                v[t][e][i] = in[e] && p + t < a.shared_parts ? __ldcg(a.shared_out + ((p + t) * all_rows + at[e]) * D + g + 8 * i) : 0.f;
+                };
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int f = f0 + 8 * nt + 2 * c + e, qi = f / gq;
+                    in[e] = f < nq * gq;
+                    at[e] = in[e] ? (long long)(q0 + qi) * a.q_heads + hh * gq + f - qi * gq : 0;
+                }
+                fetch(0);
+                const Joint j[2] = {joint(at[0], M[nt][0], L[nt][0]), joint(at[1], M[nt][1], L[nt][1])};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (a.lse && g == 0 && in[e]) a.lse[at[e]] = j[e].lse;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) o[nt][i][e] *= j[e].own, o[nt][i][2 + e] *= j[e].own;
+                }
+#pragma unroll
+                for (int p = 0; p < kKv4SharedParts; p += PARTS) {
+                    if (p >= a.shared_parts) break;
+                    if (p) fetch(p);
+#pragma unroll
+                    for (int t = 0; t < PARTS; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                o[nt][i][e] = fmaf(v[t][e][2 * i], j[e].shared[p + t], o[nt][i][e]);
+                                o[nt][i][2 + e] = fmaf(v[t][e][2 * i + 1], j[e].shared[p + t], o[nt][i][2 + e]);
+                            }
+                }
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                inv[e] = L[nt][e] == 0.f ? 0.f : 1.f / L[nt][e];
+                inv[e] = SHARED ? 1.f : L[nt][e] == 0.f ? 0.f : 1.f / L[nt][e];
                 const int f = f0 + 8 * nt + 2 * c + e, qi = f / gq;
                 if (f >= nq * gq) continue;
                 const long long row = q0 + qi;
                 const int head = hh * gq + f - qi * gq;
-                if constexpr (SHARED) {
-                    const long long at = row * a.q_heads + head;
-                    const Joint j = joint(at, M[nt][e], L[nt][e]);
-                    inv[e] = 1.f;
-                    if (a.lse && g == 0) a.lse[at] = j.lse;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) o[nt][i][e] *= j.own, o[nt][i][2 + e] *= j.own;
-#pragma unroll
-                    for (int p = 0; p < kKv4SharedParts; ++p) {
-                        if (p >= a.shared_parts) break;
-                        const float* from = a.shared_out + (p * all_rows + at) * D + g;
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            o[nt][i][e] = fmaf(__ldcg(from + 16 * i), j.shared[p], o[nt][i][e]);
-                            o[nt][i][2 + e] = fmaf(__ldcg(from + 16 * i + 8), j.shared[p], o[nt][i][2 + e]);
-                        }
-                    }
-                } else if (a.lse && g == 0)
+                if (!SHARED && a.lse && g == 0)
                     a.lse[row * a.q_heads + head] =
                         L[nt][e] == 0.f ? -CUDART_INF_F : (M[nt][e] + log2f(L[nt][e]) - 2.f) * 0.69314718055994530942f;
                 if (a.out_f32) {

@@ -8,6 +8,10 @@ a block, K/128 products by a factor (itself two roundings) and as many additions
 the joining of as many parts; all relative to the sum of magnitudes, A:
 (2 128 + 4 K/128 + 4) 2^-24 A. A bf16 output adds 2^-8 of itself.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -19,6 +23,7 @@ if not torch.cuda.is_available():  # pragma: no cover - the marker keeps these o
 import memory_bound_weight_gb300 as mbw  # noqa: E402
 
 E4M3 = torch.float8_e4m3fn
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def gen(seed):
@@ -396,3 +401,36 @@ def test_compiled_calls_give_the_same_and_refuse_in_the_same_words(monkeypatch):
         mbw.gemm_fp8_b128(x, xs, w, sc)
     with mbw.output_fp32():
         assert mbw.gemm_fp8_b128(x, xs, w, sc).dtype == torch.float32
+
+
+def test_a_first_call_may_be_a_captured_one():
+    """In a process of its own: nothing that a call does once, for a kernel or a device, is refused while a stream is captured."""
+    code = """
+import torch, memory_bound_weight_gb300 as mbw
+g = torch.Generator(device="cuda").manual_seed(1)
+x, w = (torch.randn(300, 512, generator=g, device="cuda").bfloat16() for _ in range(2))
+B, hk, D, pages = 64, 2, 64, 1024
+cache = mbw.Kv4Cache(torch.zeros(pages + B, mbw.kv4_page_bytes(16, hk, D, 32), dtype=torch.uint8, device="cuda"), hk, D, 16, 32)
+b = torch.arange(B, dtype=torch.int32, device="cuda")
+table = torch.cat((torch.arange(pages, dtype=torch.int32, device="cuda").repeat(B, 1), pages + b[:, None]), 1)
+q, ctx = torch.randn(B, 16, D, generator=g, device="cuda").bfloat16(), pages * 16 + 1 + b % 16
+ws = mbw.kv4_attention_shared_workspace(D, B, 16)
+def run():
+    wq, sw = mbw.quantize_fp8_b128(w)
+    out = []
+    for m in (1, 12, 40, 100, 300):
+        xq, sx = mbw.quantize_fp8_g128(x[:m])
+        out += [mbw.gemm_fp8_b128(xq, sx, wq, sw), mbw.gemm_fp8_b128(xq, sx, wq, sw, up_weights=wq, up_scales=sw)]
+    return out + [mbw.kv4_attention_shared(cache, q, table, ctx, pages * 16, workspace=ws)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+mbw.check_device_error()
+print("the same")
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "the same" in done.stdout, done.stderr[-2000:]
