@@ -17,10 +17,10 @@
 // What bounds it: memory, for large ones (rows of 4096 x 18944: 39.8 us, 5.85 TB/s;
 // weights 18944 x 3584: 35 us, 5.8 TB/s; values back 56 us, 6.0 TB/s), and launch and a
 // chain of dependent steps for small ones (one row: 1.7 us, normed 2.6). Normed rows:
-// instructions, 16 a value, a third of them the sum in two floats (4000 x 3584: 17.8
-// us, 2.4 TB/s). What it cost on the way there: the root in 64 bits by every thread 70
-// us of those; 8 columns a lane in place of 16 (rows 19 us in place of 10.6); a branch
-// per quotient for scales out of range, and 64-bit divisions of indexes, a third more.
+// instructions and latency (4000 x 3584: 16.4 us, 2.6 TB/s; 20000 x 3328: 62 us). What
+// it cost on the way there: the roots of those 4000 rows in 64 bits by every thread 70 us;
+// 8 columns a lane in place of 16 (rows 19 us in place of 10.6); a branch per quotient for
+// scales out of range, and 64-bit divisions of indexes, a third more.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -149,6 +149,13 @@ __device__ __forceinline__ void add2(float& hi, float& lo, float x) {
     hi = s;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
 // 8 bf16 values times r and their weights, rounded to bf16, as norm_word.
 __device__ __forceinline__ uint4 normed(const uint4& v, float r, const uint4& g) {
     const uint32_t x[4] = {v.x, v.y, v.z, v.w}, w[4] = {g.x, g.y, g.z, g.w};
@@ -177,7 +184,7 @@ __device__ __forceinline__ float inverse_root(float hi, float lo, float k, float
 // mean but for 2^-40, and the codes do not hang on the order of the sum. Where the squares pass fp32 or would vanish in it
 // the sum is taken again in 64 bits.
 // ALONE: a CTA has a row; else each warp has one, which waits for no other and holds it up to 3584 columns: of many short
-// rows (alone, by warps, us: 600 x 3584 5.1, 7.3; 4000 x 3584 22.8, 17.8; 4096 x 18944 75.6, 114).
+// rows (alone, by warps, us: 600 x 3584 5.1, 7.3; 4000 x 3584 22.8, 17.8, now 16.5; 4096 x 18944 75.6, 114).
 constexpr int kManyRows = 1200, kShortRow = 4096;
 template <bool ALONE>
 __global__ void __launch_bounds__(kThreads) quantize_norm_kernel(const uint16_t* __restrict__ X, int64_t stride, uint8_t* __restrict__ Q,
@@ -213,9 +220,35 @@ __global__ void __launch_bounds__(kThreads) quantize_norm_kernel(const uint16_t*
                 add2(hi4[2 * j + 1 & 3], lo4[2 * j + 1 & 3], b * b);
             }
         };
+        if (ALONE) {
 #pragma unroll
-        for (int i = 0; i < HELD; ++i)
-            if (i < turns) add(held[i]);
+            for (int i = 0; i < HELD; ++i)
+                if (i < turns) add(held[i]);
+        } else {
+            // Two sums of pairs, begun with a power of two of at least the largest square of what is held, so that a sum is never
+            // less than what is added, and what it loses is x^2 - (s' - s), exactly: four instructions for two squares in
+            // place of 16 (4000 x 3584: 17.8 -> 16.5 us; alone, with 48 registers, 300 rows took 5.4 us in place of 4.4).
+            uint32_t largest = 0;
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) largest = largest8(largest8(largest, held[i].a), held[i].b);
+            const float above = 2.f * __uint_as_float(max(largest & 0x7F80u, largest >> 16 & 0x7F80u) << 16), start = above * above;
+            float2 sums[2] = {make_float2(start, start), make_float2(start, start)}, lost[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 minus = make_float2(-1.f, -1.f), one = make_float2(1.f, 1.f);
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                if (i < turns) {
+                    const uint32_t w[8] = {held[i].a.x, held[i].a.y, held[i].a.z, held[i].a.w, held[i].b.x, held[i].b.y, held[i].b.z, held[i].b.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 v = make_float2(bf16lo_to_f32(w[j]), bf16hi_to_f32(w[j])), before = sums[j & 1];
+                        sums[j & 1] = fma2(v, v, before);
+                        lost[j & 1] = fma2(fma2(v, v, fma2(sums[j & 1], minus, before)), one, lost[j & 1]);
+                    }
+                }
+            // exact: the sums and their beginning are multiples of the sums' last places
+            hi4[0] = sums[0].x - start, hi4[1] = sums[0].y - start, hi4[2] = sums[1].x - start, hi4[3] = sums[1].y - start;
+            lo4[0] = lost[0].x, lo4[1] = lost[0].y, lo4[2] = lost[1].x, lo4[3] = lost[1].y;
+        }
         for (int i = HELD; i < turns; ++i) add(load(i));
         float hi = hi4[0], lo = (lo4[0] + lo4[1]) + (lo4[2] + lo4[3]);
         add2(hi, lo, hi4[1]), add2(hi, lo, hi4[2]), add2(hi, lo, hi4[3]);

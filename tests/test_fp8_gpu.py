@@ -434,3 +434,24 @@ print("the same")
 """
     done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0 and "the same" in done.stdout, done.stderr[-2000:]
+
+
+def test_norm_of_many_rows():
+    """Rows by warps, whose sums begin with a power of two above their squares: the codes of the exact mean, in any order of columns."""
+    g = gen(12)
+    for k in (128, 1280, 3584, 4096):
+        x = torch.randn(1300, k, generator=g, device="cuda")
+        x[:300] *= torch.exp(4 * torch.randn(300, k, generator=g, device="cuda"))
+        x[300:400, 1:] *= 2.0 ** -30
+        x[400:500] = x[400:500].abs().sort(1).values  # what is added grows
+        x[500:510] *= 2.0 ** -50  # squares near the end of fp32's range, and past it
+        x[510:520] *= 2.0 ** 55
+        x[520:530] *= 2.0 ** -70
+        x[530] = 0
+        x = x.bfloat16()
+        wn = (1 + 0.3 * torch.randn(k, generator=g, device="cuda")).bfloat16()
+        for eps in (1e-6, 0.0):
+            r = (1 / torch.sqrt(x.double().square().mean(1, keepdim=True) + eps)).float()
+            want, scale = plain_rows((x.float() * r * wn.float()).bfloat16())
+            q, s = mbw.quantize_fp8_g128(x, norm_weight=wn, norm_eps=eps)
+            assert same(s, scale) and same(q, want)
