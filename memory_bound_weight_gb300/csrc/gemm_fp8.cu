@@ -541,16 +541,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Up to NX = 64 or 128 rows of X: the weights are the products' rows, 128 a CTA, and X their columns, so that no product is
+// Up to NX = 32, 64 or 128 rows of X: the weights are the products' rows, 128 a CTA, and X their columns, so that no product is
 // of rows that are not there; a column of Y is a lane of the accumulator, of one weight scale a block. No pairs: X is small,
 // and a CTA has a tile of W (gated: and U's) for itself. Two or four accumulators are in turn. k is cut between up to eight
 // CTAs of a cluster.
-// What bounds it: where each SM has one tile, W's stream from HBM and the start before it (64 x 152064 x 3584 97 us, 5.6 TB/s;
+// What bounds it: where each SM has one tile, W's stream from HBM and the start before it (32 x 152064 x 3584 91 us, 6.0 TB/s;
 // 64 x 4608 x 3584 8.6 us, 3.5 of them a start and 2 a join); a block of k takes 0.26 us for 64 rows, the issue of products
-// and the adders' way through waits, loads and factors, and 0.42 for 128, most of it the adders'.
+// and the adders' way through waits, loads and factors, and 0.42 for 128, most of it the adders'. (32 rows as 64: 18944 x
+// 3584 16.0 us in place of 13.9, gated 5632 x 2048 11.3 in place of 9.7.)
 template <bool GLU, int NX>
 struct Few {
-    static constexpr int MATS = GLU ? 2 : 1, STAGE = MATS * 128 * 128 + NX * 128, DEPTH = 208 * 1024 / STAGE < 8 ? 208 * 1024 / STAGE : 8;
+    static constexpr int MATS = GLU ? 2 : 1, STAGE = MATS * 128 * 128 + NX * 128, DEPTH = 208 * 1024 / STAGE;
     static constexpr int COLS = MATS * NX, NACC = 512 / COLS < 4 ? 512 / COLS : 4;  // TMEM columns of an accumulator, accumulators
     static constexpr int GROUP = 4 * COLS * 4;                                      // factors of four blocks by [block][matrix][row of X]
     static constexpr int OFF_FACTOR = DEPTH * STAGE, OFF_BAR = OFF_FACTOR + kGroups * GROUP;
@@ -705,21 +706,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         registers<kRegsAdders>(true);
         // A thread's columns are read in pieces, the next on its way under the additions of the one before: whole blocks, or
         // of the gated form of 128 rows, whose sums leave no registers, a quarter of one.
-        constexpr int C = NX / 2, CHUNKS = C / 32, THIRTY = L::MATS * CHUNKS;  // columns of a thread; 32s of them, in all
-        constexpr int P = THIRTY <= 2 ? THIRTY : 1, PIECES = THIRTY / P;       // 32s of a piece
+        constexpr int C = NX / 2, U = C < 32 ? C : 32, CHUNKS = C / U, UNITS = L::MATS * CHUNKS;  // columns of a thread; units of up to 32 of them, in all
+        constexpr int P = UNITS <= 2 ? UNITS : 1, PIECES = UNITS / P;                             // units of a piece
         const int quarter = warp & 3, half = (warp - 4) >> 2, r = quarter * 32 + lane;
         const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16) + half * C;
-        auto column = [](int i) { return i / CHUNKS * NX + i % CHUNKS * 32; };  // of the i-th 32, among an accumulator's
-        float2 acc[THIRTY * 16];
-        uint32_t v[2][P * 32];
+        auto column = [](int i) { return i / CHUNKS * NX + i % CHUNKS * U; };  // of the i-th unit, among an accumulator's
+        float2 acc[UNITS * U / 2];
+        uint32_t v[2][P * U];
         pdl_wait();
         uint32_t it = 0, group = 0;
-        auto fetch = [&](uint32_t(&to)[P * 32], uint32_t at, int j) {
+        auto fetch = [&](uint32_t(&to)[P * U], uint32_t at, int j) {
 #pragma unroll
-            for (int h = 0; h < P; ++h) ld<32>(to + 32 * h, at + column(j * P + h));
+            for (int h = 0; h < P; ++h) ld<U>(to + U * h, at + column(j * P + h));
         };
         bool begun;  // the next block's first piece is on its way
-        auto block = [&](int kb, uint32_t(&v0)[P * 32], uint32_t(&v1)[P * 32]) {
+        auto block = [&](int kb, uint32_t(&v0)[P * U], uint32_t(&v1)[P * U]) {
             const uint32_t b = it % L::NACC, next = (it + 1) % L::NACC;
             if (!begun) {
                 bar_wait(&sfull[b], (it / L::NACC) & 1, ok);
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto& now = j & 1 ? v1 : v0;
                 auto& then = j & 1 ? v0 : v1;
                 const uint32_t ready = j + 1 == PIECES && kb + 1 < kb1 ? bar_ask(&sfull[next], ((it + 1) / L::NACC) & 1) : 0;
-                wait_ld<P * 32>(now);
+                wait_ld<P * U>(now);
                 if (j + 1 < PIECES) {
                     fetch(then, my + b * L::COLS, j + 1);
                 } else {
@@ -748,9 +749,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < P * 32; c += 4) {
-                    const float4 ff = *reinterpret_cast<const float4*>(f + column(j * P + c / 32) + c % 32);
-                    float2* to = acc + 16 * j * P + c / 2;
+                for (int c = 0; c < P * U; c += 4) {
+                    const float4 ff = *reinterpret_cast<const float4*>(f + column(j * P + c / U) + c % U);
+                    float2* to = acc + (j * P * U + c) / 2;
                     to[0] = fma2(make_float2(__uint_as_float(now[c]), __uint_as_float(now[c + 1])), make_float2(ff.x, ff.y), to[0]);
                     to[1] = fma2(make_float2(__uint_as_float(now[c + 2]), __uint_as_float(now[c + 3])), make_float2(ff.z, ff.w), to[1]);
                 }
@@ -764,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (int t = first; t < tiles; t += stride) {
 #pragma unroll
-            for (int c = 0; c < THIRTY * 16; ++c) acc[c] = make_float2(0.f, 0.f);
+            for (int c = 0; c < UNITS * U / 2; ++c) acc[c] = make_float2(0.f, 0.f);
             begun = false;
             for (int kb = kb0; kb < kb1; ++kb) {
                 block(kb, v[0], v[1]);
@@ -775,9 +776,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (split > 1) {  // into shared memory, [matrix][row of X][column of Y]
                 float* to = reinterpret_cast<float*>(smem) + half * C * 128 + r;
 #pragma unroll
-                for (int j = 0; j < THIRTY; ++j)
+                for (int j = 0; j < UNITS; ++j)
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) to[(column(j) + c) * 128] = c & 1 ? acc[16 * j + c / 2].y : acc[16 * j + c / 2].x;
+                    for (int c = 0; c < U; ++c) to[(column(j) + c) * 128] = c & 1 ? acc[(j * U + c) / 2].y : acc[(j * U + c) / 2].x;
             } else if (t * 128 + r < a.N) {
                 constexpr int HELD = 16;  // of the residual, ahead of the stores
                 uint16_t held[HELD];
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < HELD; ++i) held[i] = a.residual && m + i < a.M ? a.residual[to + (int64_t)i * a.N] : (uint16_t)0;
                     float o = c & 1 ? acc[c / 2].y : acc[c / 2].x;
-                    if constexpr (GLU) o = silu(o) * (c & 1 ? acc[CHUNKS * 16 + c / 2].y : acc[CHUNKS * 16 + c / 2].x);
+                    if constexpr (GLU) o = silu(o) * (c & 1 ? acc[(C + c) / 2].y : acc[(C + c) / 2].x);
                     if (a.residual) o += bf16lo_to_f32(held[c % HELD]);
                     if (m < a.M) store_out(a.y, to, o, a.out_f32);
                 }
@@ -963,12 +964,13 @@ cudaError_t launch_few(const Fp8Args& a, cudaStream_t s) {
 
 cudaError_t launch_gemm_fp8(const Fp8Args& a, cudaStream_t s) {
     // Few rows as a stream of W on mma.sync, up to 8, whose products cost it no more than one row's (2048 x 2048 2.6 us, here
-    // 4.6; 18944 x 3584 14.0, 15.5), and up to 16 of smaller weights (2048 x 2048 3.1, 4.6; 4608 x 3584 6.5, 7.9; gated 5632 x
-    // 2048, 23 MB, 9.9, 10.1; but 2560 x 9728, 25 MB, 12.2, 8.8; 3584 x 18944 19.7, 15.3; gated 18944 x 3584 39, 27.5).
+    // 4.5; 18944 x 3584 14.0, 14.0), and up to 16 of smaller weights (2048 x 2048 3.1, 4.5; 4608 x 3584 6.5, 8.0; gated 5632 x
+    // 2048, 23 MB, 9.9, 9.7; 2560 x 9728, 25 MB, 12.2, 8.4; 3584 x 18944 19.7, 15.2; gated 18944 x 3584 39, 25.6).
     const int64_t weights = (int64_t)a.N * a.K * (a.U ? 2 : 1);
     if (a.M <= 8 || (a.M <= 16 && weights < 20000000)) return launch_gemv_fp8(a, s);
     // Up to 128 rows with the weights as the products' rows (128 x 3584 x 18944: 20.0 us, by pairs 26.7; 100 x 18944 x 3584
     // gated 33, 36).
+    if (a.M <= 32) return a.U ? launch_few<true, 32>(a, s) : launch_few<false, 32>(a, s);
     if (a.M <= 64) return a.U ? launch_few<true, 64>(a, s) : launch_few<false, 64>(a, s);
     if (a.M <= 128) return a.U ? launch_few<true, 128>(a, s) : launch_few<false, 128>(a, s);
     return a.U ? launch_pairs<true>(a, s) : launch_pairs<false>(a, s);

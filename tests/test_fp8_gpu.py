@@ -124,7 +124,7 @@ def test_gated_product_with_a_residual(m, n, k):
     check(out, want, mass * eps + want.abs() * 2.0 ** -24 + half_step(want), "in place")
 
 
-FEW = [(9, 9001, 2560), (16, 2560, 9728), (17, 3584, 1024), (24, 20011, 640), (61, 5632, 2048), (64, 21000, 384), (64, 1000, 9728),
+FEW = [(9, 9001, 2560), (16, 2560, 9728), (17, 3584, 1024), (24, 20011, 640), (32, 1000, 9728), (33, 2050, 1280), (61, 5632, 2048), (64, 21000, 384), (64, 1000, 9728),
        (65, 20480, 512), (90, 300, 18944), (127, 2049, 1792), (128, 19600, 640), (128, 3584, 3584)]
 
 
@@ -155,7 +155,7 @@ def test_few_rows_of_larger_matrices(m, n, k):
     check(out, want, mass * eps + want.abs() * 2.0 ** -24 + half_step(want), "in place")
 
 
-@pytest.mark.parametrize("m", [16, 64, 100])
+@pytest.mark.parametrize("m", [16, 33, 64, 100])
 def test_gated_products_one_behind_the_other(m):
     """Every SM with a tile of its own, launches that overlap, a ring whose stages the issuing warps take in turn: always the same."""
     g = gen(m)
