@@ -893,10 +893,14 @@ struct Known {
     std::atomic<int> held[16][kFewSplit];
 };
 
-// Tiles whose k is cut between up to `most` shares of `unit` CTAs each, where that leaves fewer blocks of k in a row: in
-// blocks, `begin` is what the start of a CTA takes, `join` the join of a cluster.
-cudaError_t launch_cut(Kernel fn, Known& known, int smem, int unit, int most, int64_t tiles, int begin, int join, int x_rows, const Fp8Args& a,
-                       cudaStream_t s) {
+// What the parts of a launch take, in ns: a block of k, the start of a CTA, the join of a cluster, and of it each share. (Without
+// a time for each share, 64 x 3584 x 3584 took 8.4 us in clusters of 5, now 7.3 of 4; 64 x 2048 x 2048 5.5 of 6, now 4.8 of 4.)
+struct Times {
+    int block, start, join, share;
+};
+
+// Tiles whose k is cut between up to `most` shares of `unit` CTAs each, where that takes less time.
+cudaError_t launch_cut(Kernel fn, Known& known, int smem, int unit, int most, int64_t tiles, const Times& of, int x_rows, const Fp8Args& a, cudaStream_t s) {
     CUtensorMap mx, mw, mu;
     if (!encode(&mx, a.X, a.K, a.M, x_rows) || !encode(&mw, a.W, a.K, a.N, 128) || !encode(&mu, a.U ? a.U : a.W, a.K, a.N, 128))
         return cudaErrorInvalidValue;
@@ -937,7 +941,7 @@ cudaError_t launch_cut(Kernel fn, Known& known, int smem, int unit, int most, in
             if (dev < 16) known.held[dev][n - 1].store(h, std::memory_order_relaxed);
         }
         const int64_t waves = (tiles + h - 1) / h, blocks = (KB + n - 1) / n;
-        const int64_t cost = n == 1 ? waves * blocks + begin : waves * (blocks + begin) + join;
+        const int64_t cost = n == 1 ? waves * blocks * of.block + of.start : waves * (blocks * of.block + of.start) + of.join + n * of.share;
         if (cost < best) best = cost, split = n, held = h;
     }
     const int64_t clusters = split > 1 || tiles < held ? tiles : held;
@@ -952,12 +956,14 @@ template <bool GLU>
 cudaError_t launch_pairs(const Fp8Args& a, cudaStream_t s) {
     static Known known;
     const int64_t tiles = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256));
-    return launch_cut(gemm_fp8_kernel<GLU>, known, kSmem, 2, kMaxSplit, tiles, 8, 8, 128, a, s);  // a block takes 0.4 us
+    return launch_cut(gemm_fp8_kernel<GLU>, known, kSmem, 2, kMaxSplit, tiles, {375, 3000, 3000, 0}, 128, a, s);
 }
 template <bool GLU, int NX>
 cudaError_t launch_few(const Fp8Args& a, cudaStream_t s) {
     static Known known;
-    return launch_cut(gemm_fp8_few_kernel<GLU, NX>, known, Few<GLU, NX>::SMEM, 1, kFewSplit, ((int64_t)a.N + 127) / 128, 16, 8, NX, a, s);
+    constexpr int BLOCK = (NX == 32 ? 230 : NX == 64 ? 260 : 420) * (GLU ? 8 : 5) / 5;
+    return launch_cut(gemm_fp8_few_kernel<GLU, NX>, known, Few<GLU, NX>::SMEM, 1, kFewSplit, ((int64_t)a.N + 127) / 128, {BLOCK, 4000, 1000, 260}, NX,
+                      a, s);
 }
 
 }  // namespace
