@@ -50,8 +50,16 @@ __device__ __forceinline__ void ld32(uint32_t* v, const void* p) {
     asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]) : "l"(p));
 }
+// The same from 16-byte boundaries.
+__device__ __forceinline__ void ld16x2(uint32_t* v, const void* p) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[4 * i]), "=r"(v[4 * i + 1]), "=r"(v[4 * i + 2]), "=r"(v[4 * i + 3]) : "l"(static_cast<const uint8_t*>(p) + 16 * i));
+}
 
-template <int NT, bool GLU>
+// WIDE: X lies on 32 bytes, which its rows and blocks then do too; else on 16.
+template <int NT, bool GLU, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) gemv_fp8_kernel(const Fp8Args a, const int split) {
     using S = Shape<NT>;
     constexpr int SETS = GLU ? 2 : 1, ROUND = S::ROUND, SUMS = S::SUMS, AHEAD = S::AHEAD;
@@ -107,7 +115,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_fp8_kernel(const Fp8Args a, 
         for (int i = 0; i < NT; ++i) {
             const int m = 8 * i + g;
             if (m < a.M) {
-                ld32(x[i], a.X + (int64_t)m * a.K + kb * 128 + 32 * c);
+                const uint8_t* at = a.X + (int64_t)m * a.K + kb * 128 + 32 * c;
+                if (WIDE)
+                    ld32(x[i], at);
+                else
+                    ld16x2(x[i], at);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) x[i][q] = 0;
@@ -221,11 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_fp8_kernel(const Fp8Args a, 
     }
 }
 
-template <int NT, bool GLU>
+template <int NT, bool GLU, bool WIDE>
 cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
     using S = Shape<NT>;
     constexpr int SETS = GLU ? 2 : 1;
-    auto* fn = gemv_fp8_kernel<NT, GLU>;
+    auto* fn = gemv_fp8_kernel<NT, GLU, WIDE>;
     const cudaError_t err = kv4_allow_smem((const void*)fn, S::SMEM);
     if (err != cudaSuccess) return err;
     const int sms = device_sm_count();
@@ -272,11 +284,17 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, fn, a, (const int)split);
 }
 
+template <int NT, bool WIDE>
+cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
+    return a.U ? launch<NT, true, WIDE>(a, s) : launch<NT, false, WIDE>(a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_gemv_fp8(const Fp8Args& a, cudaStream_t s) {
-    if (a.M <= 8) return a.U ? launch<1, true>(a, s) : launch<1, false>(a, s);
-    return a.U ? launch<2, true>(a, s) : launch<2, false>(a, s);
+    const bool wide = ((uintptr_t)a.X & 31) == 0;
+    if (a.M <= 8) return wide ? launch<1, true>(a, s) : launch<1, false>(a, s);
+    return wide ? launch<2, true>(a, s) : launch<2, false>(a, s);
 }
 
 }  // namespace mbw
