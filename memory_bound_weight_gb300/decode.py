@@ -15,7 +15,8 @@ decoding of a few requests whose prompts differ in length. Per layer:
 and behind the last one logits = W_head . norm(x) and token_logprobs. A step for
 one token of every request is captured into a CUDA graph and replayed: the
 lengths, positions and slots it works on are device tensors that it moves on
-itself.
+itself. (The length of a shared beginning, below, is not: a captured step is
+refused behind prompts that share less.)
 
 With --weights fp8 each product is one of 8-bit floating point operands with a
 scale for each block of 128: quantize_fp8_g128 (with the norm where there is one)
@@ -206,14 +207,21 @@ class Decoder:
         return r
 
     def counted(self, replay):
+        """A captured step as a call. It holds the number of tokens that the requests shared when it was captured; with fewer, or
+        none, it would have them attend to another's pages. (With more it attends to the others as to each request's own.)"""
+        shared = self.shared
+
         def counted_replay():
+            if shared > self.shared:
+                raise ValueError(f"captured for {shared} tokens that all requests share, which now share {self.shared}: capture anew")
             self.advance()
             replay()
 
         return counted_replay
 
     def graph(self, top_k=1):
-        """step() as a CUDA graph: (replay, its TokenLogprobs, overwritten by each replay). One place has to be left."""
+        """step() as a CUDA graph: (replay, its TokenLogprobs, overwritten by each replay). One place has to be left. Replays
+        follow further prompts, but for those that share fewer tokens than when it was captured, behind which they raise."""
         keep, longest = (self.ctx.clone(), self.ids.clone()), self.longest
         self.advance()  # refused before anything runs
         self.longest = longest
