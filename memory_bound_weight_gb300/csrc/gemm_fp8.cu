@@ -58,7 +58,10 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_at(bar)), "r"(bytes) : "memory");
 }
-// A bounded wait by a warp. Who has given up once waits no more: every role then runs to its end.
+// A bounded wait by a warp, whose lanes give up together (the last round of some may see what that of others did not). Who
+// has given up once waits no more, and every role comes to its end: the issuers of copies and of products issue nothing
+// more, and neither they nor the adders, who go on over what is there, give anything back: the others then give up by
+// themselves, and nobody takes a barrier's phase for one that it is not.
 __device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, bool& ok) {
     bool got = !ok;
     for (int i = 0; i < MBW_WAIT_LIMIT && !got; ++i) {
@@ -67,8 +70,7 @@ __device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, bool& o
                      : "=r"(r) : "r"(smem_at(bar)), "r"(parity) : "memory");
         got = r != 0;
     }
-    if (!got) atomicExch(&g_f8_fault, 1), ok = false;
-    __syncwarp();
+    if (!__all_sync(0xFFFFFFFFu, got)) atomicExch(&g_f8_fault, 1), ok = false;
 }
 // Whether a phase is over, without waiting; to be looked at later (all_of), when the answer is there.
 __device__ __forceinline__ uint32_t bar_ask(uint64_t* bar, uint32_t parity) {
@@ -85,8 +87,26 @@ __device__ __forceinline__ bool elect() {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+template <int CTAS = 1>
 __device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_at(bar)) : "memory");
+    if (CTAS == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_at(bar)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_at(bar)) : "memory");
+}
+// The end of a warp that issues products, whoever has given up: its own are complete before the TMEM they write is released.
+template <int CTAS = 1>
+__device__ __forceinline__ void drain_products(uint64_t* bar, bool leader) {
+    if (leader) commit<CTAS>(bar);
+    __syncwarp();
+    bool ok = true;
+    bar_wait(bar, 0, ok);
+}
+// The end of a warp that issues copies, likewise: the last turn of each stage, of `it` in all, is over on `bars`, so that no copy
+// lands behind the CTA's end, or on the sums that take the ring's place.
+__device__ __forceinline__ void drain_copies(uint64_t* bars, uint32_t it, uint32_t depth) {
+    bool ok = true;
+    for (uint32_t j = it > depth ? it - depth : 0; j < it; ++j) bar_wait(&bars[j % depth], (j / depth) & 1, ok);
 }
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_at(dst)),
@@ -189,7 +209,7 @@ static_assert(4 * kRegsIssuers + kAdders * kRegsAdders <= (4 + kAdders) * kRegsL
 constexpr int kStage = 2 * 128 * 128, kDepth = 6;
 // Factors of four blocks of k by [block][row], two each: of the columns of the even CTA's W and of the odd one's W or U.
 constexpr int kGroups = 4, kGroup = 4 * 128 * 8;
-constexpr int kOffFactor = kDepth * kStage, kOffBar = kOffFactor + kGroups * kGroup, kSmem = kOffBar + (2 * kDepth + 8 + 2 * kGroups) * 8 + 16 + 1024;
+constexpr int kOffFactor = kDepth * kStage, kOffBar = kOffFactor + kGroups * kGroup, kSmem = kOffBar + (2 * kDepth + 8 + 2 * kGroups + 2) * 8 + 16 + 1024;
 constexpr int kPitch = 260;  // floats of a row that the CTAs of a cluster are joined in: 4 to spread the banks
 static_assert(kSmem <= 227 * 1024, "");
 static_assert(128 * kPitch * 4 <= kOffFactor, "over the ring, which is drained then");
@@ -211,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = smem_raw + (-smem_at(smem_raw) & 1023);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // the even CTA's count both of the pair
     uint64_t *empty = full + kDepth, *sfull = empty + kDepth, *sempty = sfull + 4;  // sempty: the even CTA's count both
-    uint64_t *ffull = sempty + 4, *fempty = ffull + kGroups;  // of factors
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fempty + kGroups);
+    uint64_t *ffull = sempty + 4, *fempty = ffull + kGroups, *done = fempty + kGroups;  // of factors; of all products
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t crank, csize;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
@@ -225,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kDepth; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 2);
         for (int i = 0; i < 4; ++i) bar_init(&sfull[i], 1), bar_init(&sempty[i], kAdders);
         for (int i = 0; i < kGroups; ++i) bar_init(&ffull[i], 1), bar_init(&fempty[i], kAdders);
+        bar_init(&done[0], 1), bar_init(&done[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -294,11 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
-            if (!ok && rank == 0)  // no copy lands behind the pair's end: both CTAs' complete here
-                for (uint32_t j = it > kDepth ? it - kDepth : 0; j < it; ++j) {
-                    bool o = true;
-                    bar_wait(&full[j % kDepth], (j / kDepth) & 1, o);
-                }
+            // Both CTAs' copies complete on the even one's `full`; the odd one, which has none, waits for its stages' products.
+            drain_copies(rank == 0 ? full : empty, it, kDepth);
         } else if (warp <= 2) {
             if (rank == 0) {
             const int h = warp - 1;
@@ -311,32 +329,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                              : "memory");
             };
             uint32_t it = 0, s = 0, turn = 0, there = 0;  // the stage, the ring's turns before it, and whether it is full
-            for (long long t = first; t < tiles; t += stride)
+            for (long long t = first; t < tiles && ok; t += stride)
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const uint32_t b = it & 1;
                     const uint32_t free = it < 2 ? 1u : bar_ask(&sempty[2 * b + h], (it / 2 - 1) & 1);
                     if (!all_of(there)) bar_wait(&full[s], turn & 1, ok);
                     if (!all_of(free)) bar_wait(&sempty[2 * b + h], (it / 2 - 1) & 1, ok);
+                    if (!ok) break;
                     fence_after();
                     const uint32_t cur = s;
                     if (++s == kDepth) s = 0, ++turn;
                     there = bar_ask(&full[s], turn & 1);  // the next one's answer comes under the products' issue
                     if (leader) {
-                        if (ok) {
-                            const uint64_t da = desc(smem_at(smem + cur * kStage)), db = da + (128 + 64 * h) * 128 / 16;
+                        const uint64_t da = desc(smem_at(smem + cur * kStage)), db = da + (128 + 64 * h) * 128 / 16;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)  // 32 codes each: 32 bytes further inside the swizzle atom
-                                asm volatile(
-                                    "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(
-                                        tmem + b * 256 + h * 128),
-                                    "l"(da + 2 * k), "l"(db + 2 * k), "r"(ID), "r"(k > 0 ? 1u : 0u)
-                                    : "memory");
-                        }
+                        for (int k = 0; k < 4; ++k)  // 32 codes each: 32 bytes further inside the swizzle atom
+                            asm volatile(
+                                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+                                    tmem + b * 256 + h * 128),
+                                "l"(da + 2 * k), "l"(db + 2 * k), "r"(ID), "r"(k > 0 ? 1u : 0u)
+                                : "memory");
                         commit2(&sfull[2 * b + h]);
                         commit2(&empty[cur]);
                     }
                     __syncwarp();
                 }
+            drain_products<2>(&done[h], leader);
             }
         } else {
             // ------------------------------------------------------- factors ----
@@ -420,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) bar_arrive(sempty0 + 16 * b);
+                        if (lane == 0 && ok) bar_arrive(sempty0 + 16 * b);
                         if (kb + 1 < kb1) ready = bar_ask(&sfull[2 * (b ^ 1) + half], ((it + 1) / 2) & 1);
                     }
                     const float2 ff = j >= 2 ? make_float2(now.y, now.y) : make_float2(now.x, now.x);
@@ -437,9 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (split > 1) {  // into shared memory, [row][column]
                 asm volatile("bar.sync 1, %0;" ::"n"(kAdders * 32) : "memory");  // both halves' products have read the ring
                 float* to = reinterpret_cast<float*>(smem) + r * kPitch + half * 64;
+                if (ok)  // else copies may be on their way there
 #pragma unroll
-                for (int c = 0; c < 128; c += 4)
-                    *reinterpret_cast<float4*>(to + (c >= 64 ? 64 + c : c)) = make_float4(acc[c / 2].x, acc[c / 2].y, acc[c / 2 + 1].x, acc[c / 2 + 1].y);
+                    for (int c = 0; c < 128; c += 4)
+                        *reinterpret_cast<float4*>(to + (c >= 64 ? 64 + c : c)) = make_float4(acc[c / 2].x, acc[c / 2].y, acc[c / 2 + 1].x, acc[c / 2 + 1].y);
             } else if (row) {
                 const int64_t to = (int64_t)m * a.N + n0;
                 constexpr int COLUMNS = GLU ? 64 : 128;
@@ -555,7 +574,7 @@ struct Few {
     static constexpr int COLS = MATS * NX, NACC = 512 / COLS < 4 ? 512 / COLS : 4;  // TMEM columns of an accumulator, accumulators
     static constexpr int GROUP = 4 * COLS * 4;                                      // factors of four blocks by [block][matrix][row of X]
     static constexpr int OFF_FACTOR = DEPTH * STAGE, OFF_BAR = OFF_FACTOR + kGroups * GROUP;
-    static constexpr int SMEM = OFF_BAR + (2 * DEPTH + 2 * NACC + 2 * kGroups) * 8 + 16 + 1024;
+    static constexpr int SMEM = OFF_BAR + (2 * DEPTH + 2 * NACC + 2 * kGroups + 2) * 8 + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "");
     static_assert(COLS * 128 * 4 <= OFF_FACTOR, "sums lie over the ring, which is drained then");
 };
@@ -569,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = smem_raw + (-smem_at(smem_raw) & 1023);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
     uint64_t *empty = full + L::DEPTH, *sfull = empty + L::DEPTH, *sempty = sfull + L::NACC, *ffull = sempty + L::NACC, *fempty = ffull + kGroups;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fempty + kGroups);
+    uint64_t* done = fempty + kGroups;  // of all products
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t crank, csize;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
@@ -582,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < L::DEPTH; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
         for (int i = 0; i < L::NACC; ++i) bar_init(&sfull[i], 1), bar_init(&sempty[i], kAdders);
         for (int i = 0; i < kGroups; ++i) bar_init(&ffull[i], 1), bar_init(&fempty[i], kAdders);
+        bar_init(&done[0], 1), bar_init(&done[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -631,11 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++s == L::DEPTH) s = 0, ++turn;
                 }
             }
-            if (!ok)  // no copy lands behind the CTA's end
-                for (uint32_t j = it > L::DEPTH ? it - L::DEPTH : 0; j < it; ++j) {
-                    bool o = true;
-                    bar_wait(&full[j % L::DEPTH], (j / L::DEPTH) & 1, o);
-                }
+            drain_copies(full, it, L::DEPTH);
         } else if (warp <= 2) {
             // ------------------------------------------------------ products ----
             // by two warps in turn, since the issue of a block's takes a warp longer than the tensor pipe (64 rows, blocks of one
@@ -652,22 +669,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 static_assert(L::NACC % 2 == 0 && L::DEPTH >= L::NACC, "");
                 if (it >= L::NACC) bar_wait(&sempty[b], (it / L::NACC - 1) & 1, ok);
                 bar_wait(&full[s], turn & 1, ok);
+                if (!ok) break;
                 fence_after();
                 if (leader) {
-                    if (ok) {
-                        const uint64_t dw = desc(smem_at(smem + s * L::STAGE)), dx = dw + L::MATS * 128 * 128 / 16;
+                    const uint64_t dw = desc(smem_at(smem + s * L::STAGE)), dx = dw + L::MATS * 128 * 128 / 16;
 #pragma unroll
-                        for (int u = 0; u < L::MATS; ++u)
+                    for (int u = 0; u < L::MATS; ++u)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)  // 32 codes each: 32 bytes further inside the swizzle atom
-                                mma(tmem + b * L::COLS + u * NX, dw + u * 128 * 128 / 16 + 2 * k, dx + 2 * k, ID, k > 0);
-                    }
+                        for (int k = 0; k < 4; ++k)  // 32 codes each: 32 bytes further inside the swizzle atom
+                            mma(tmem + b * L::COLS + u * NX, dw + u * 128 * 128 / 16 + 2 * k, dx + 2 * k, ID, k > 0);
                     commit(&sfull[b]);
                     commit(&empty[s]);
                 }
                 __syncwarp();
                 s += 2;
             }
+            drain_products(&done[warp - 1], leader);
         } else {
             // ------------------------------------------------------- factors ----
             const bool by4 = KB % 4 == 0 && (((uintptr_t)a.xs | (uintptr_t)a.ws | (GLU ? (uintptr_t)a.us : 0)) & 15) == 0;
@@ -741,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(smem_at(&sempty[b]));
+                    if (lane == 0 && ok) bar_arrive(smem_at(&sempty[b]));
                     begun = all_of(ready);
                     if (begun) {
                         fence_after();
@@ -775,10 +792,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (split > 1) {  // into shared memory, [matrix][row of X][column of Y]
                 float* to = reinterpret_cast<float*>(smem) + half * C * 128 + r;
+                if (ok)  // else copies may be on their way there
 #pragma unroll
-                for (int j = 0; j < UNITS; ++j)
+                    for (int j = 0; j < UNITS; ++j)
 #pragma unroll
-                    for (int c = 0; c < U; ++c) to[(column(j) + c) * 128] = c & 1 ? acc[(j * U + c) / 2].y : acc[(j * U + c) / 2].x;
+                        for (int c = 0; c < U; ++c) to[(column(j) + c) * 128] = c & 1 ? acc[(j * U + c) / 2].y : acc[(j * U + c) / 2].x;
             } else if (t * 128 + r < a.N) {
                 constexpr int HELD = 16;  // of the residual, ahead of the stores
                 uint16_t held[HELD];
