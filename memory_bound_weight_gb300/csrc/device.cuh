@@ -197,6 +197,13 @@ __device__ __forceinline__ const float* tile_rscale(const GemvArgs& a, int t) {
     return (gated<FZ>(a) && (t & 1)) ? a.rscale2 : a.rscale;
 }
 
+// A barrier of all threads of the cluster, and what they wrote before it is there behind it. The instructions are a warp's, whose
+// lanes come from loops that they leave one by one.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // The CTA's logical tile range [t0, t0 + nt) of row-group `cg` of `G`: whole
 // output tiles, and whole gate/up pairs under the gated epilogue.
 template <int FZ>

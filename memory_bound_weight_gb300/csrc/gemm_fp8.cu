@@ -239,7 +239,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
     const int rank = crank & 1, split = csize / 2;  // of the pair; pairs that share a tile's k
     bool ok = true;
-    auto cluster_sync = [] { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); };
 
     if (tid == 0) {
         for (int i = 0; i < kDepth; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 2);
@@ -426,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) fg[i] = from[128 * i];
                     __syncwarp();
                     if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(&fempty[slot])) : "memory");
+                    __syncwarp();  // the wait for loads below is the warp's
                     ++group;
                 }
                 const float2 now = kb & 2 ? (kb & 1 ? fg[3] : fg[2]) : (kb & 1 ? fg[1] : fg[0]);
@@ -596,7 +596,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
     const int split = csize;  // CTAs that share a tile's k
     bool ok = true;
-    auto cluster_sync = [] { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); };
 
     if (tid == 0) {
         for (int i = 0; i < L::DEPTH; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);

@@ -377,10 +377,6 @@ __device__ __forceinline__ uint32_t tc_cluster_rank() {
     return r;
 }
 
-__device__ __forceinline__ void tc_cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 template <int NT, int C, int BPS>
 __global__ void __launch_bounds__(192, 1)
     gemm_tc2_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
@@ -431,7 +427,7 @@ __global__ void __launch_bounds__(192, 1)
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     // the peer's barriers exist before any remote arrive or multicast commit reaches them
-    tc_cluster_sync_all();
+    cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
 
@@ -604,7 +600,7 @@ __global__ void __launch_bounds__(192, 1)
         cluster.sync();
     } else {
         // both CTAs are done with the pair's TMEM before it is released
-        tc_cluster_sync_all();
+        cluster_sync();
     }
     if (warp == 1) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_fp8_kernel(const Fp8Args a, 
     flush(nt);
 
     if (split > 1) {
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        cluster_sync();
         const int total = nt / SETS * SUMS, e0 = (int)((long long)total * rank / split), e1 = (int)((long long)total * (rank + 1) / split);
         for (int e = e0 + tid; e < e1; e += kThreads) {
             const int t = e / SUMS, i = e % SUMS, m = i / 16, row = (p0 + t) * 16 + i % 16;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_fp8_kernel(const Fp8Args a, 
             store(m, row, v[0], v[SETS - 1]);
         }
         // no CTA leaves while another reads its sums
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        cluster_sync();
     }
 }
 

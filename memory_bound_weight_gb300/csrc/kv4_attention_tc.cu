@@ -597,9 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(Kv4AttnAr
             if (sh_last[i]) join(sh_items_cut[i]);
     };
 
-    // SHARED, items of several pieces: behind it the pieces' sums lie in the CTAs' shared memory, behind the second no CTA
-    // reads another's. Every thread of the cluster comes to both.
-    auto cluster_sync = [] { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); };
+    // SHARED, items of several pieces: behind the first cluster_sync the pieces' sums lie in the CTAs' shared memory, behind the
+    // second no CTA reads another's. Every thread of the cluster comes to both.
     constexpr int PITCH = D + 4;  // floats of a row there, over K's stages
     static_assert(kRows * PITCH * 4 <= kStages * L::K_BYTES, "");
     float* sums = reinterpret_cast<float*>(smem);
