@@ -166,8 +166,12 @@ class Decoder:
             self.ctx.zero_()
             self.ctx[:1] = common
             at = torch.arange(common, device=dev)
-            self.forward(torch.tensor(prompts[0][:common], device=dev), torch.zeros_like(at), at,
-                         torch.tensor([0] + [common] * len(n), dtype=torch.int32, device=dev), None)
+            try:
+                self.forward(torch.tensor(prompts[0][:common], device=dev), torch.zeros_like(at), at,
+                             torch.tensor([0] + [common] * len(n), dtype=torch.int32, device=dev), None)
+            except BaseException:  # nobody shares what is not there: the next prompts find each request in its own pages
+                self.table.copy_(self.own_table)
+                raise
             self.shared = common
         starts = [0]
         for x in n:

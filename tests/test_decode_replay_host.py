@@ -1,5 +1,6 @@
-"""A captured step of the decode example is refused, on the host, behind prompts that share fewer tokens than those it was
-captured for: their length is part of what was captured, and the pages it names would be another request's."""
+"""The decode example's shared beginnings, on the host. A captured step is refused behind prompts that share fewer tokens than
+those it was captured for: their length is part of what was captured, and the pages it names would be another request's. Where
+the beginning's own pass fails, no request is left in another's pages."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -55,3 +56,18 @@ def test_a_step_captured_without_one_follows_any_prompt(decoder):
         decoder.prompt(prompts(shared), share=share)
         replay()
     assert replayed == [64, 16, 0]
+
+
+def test_a_beginning_that_fails_leaves_each_request_in_its_own_pages(decoder, monkeypatch):
+    def fails(*a):
+        raise RuntimeError("no memory")
+
+    with monkeypatch.context() as m:
+        m.setattr(decoder, "forward", fails, raising=False)
+        with pytest.raises(RuntimeError, match="no memory"):
+            decoder.prompt(prompts(48), share=True)
+    assert decoder.shared == 0 and torch.equal(decoder.table, decoder.own_table)
+    decoder.prompt(prompts(48))
+    assert torch.equal(decoder.table, decoder.own_table)
+    decoder.prompt(prompts(48), share=True)
+    assert decoder.shared == 48 and (decoder.table[:, :3] == decoder.table[:1, :3]).all()
