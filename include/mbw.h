@@ -320,13 +320,17 @@ mbw_status gemv_fused_awq_g128(const uint8_t *Wq, const void *scales, const uint
  * gemm_fp8_b128 -- Y = X . W^T of operands in 8-bit floating point with a scale
  * for each block of 128 (above), any number of rows, one token or a prompt:
  *   y[m][n] = sum_b x_scales[m][b] w_scales[n/128][b] sum_{k in b} Xq[m][k] Wq[n][k]
- * Sums and factors are fp32 (a product of two scales below 2^-126 loses digits).
+ * Sums and factors are fp32 (a product of two scales below 2^-126 loses digits, one
+ * beyond fp32's range makes an infinity, or of a sum of zero a NaN).
  *   Xq : uint8 [M][K]     x_scales : fp32 [M][K/128]
  *   Wq : uint8 [N][K]     w_scales : fp32 [ceil(N/128)][K/128]
  *   Y  : bf16 [M][N] (fp32 under the fp32 hook)
  * fusion (NULL: none): residual (may be Y), and with up_weights and up_scales,
  * a second matrix of the same layout, the gated form silu(X.W^T) * (X.U^T) of a
- * feed-forward block in one kernel; norm_weight and up_zeros must be NULL.
+ * feed-forward block in one kernel; norm_weight and up_zeros must be NULL. silu is
+ * within 2^-20 of itself (below -87, where it is smaller than 2^-119, it may be 0),
+ * with an exact quotient for few rows and an approximate one for many, so that a
+ * row's last bits differ between small and large batches.
  * Wq and up_weights 32-byte aligned, Xq, Y and workspace 16-byte. No variant
  * needs a workspace.
  */
@@ -450,11 +454,19 @@ size_t mbw_kv4_attention_workspace_bytes(int32_t head_dim);
  * same shared_len tokens, in the same pages: the first shared_len / page_size
  * entries of the requests' block table rows are equal as far as each request's
  * length goes (what is left of shared_len lies in each request's own pages).
- * The result is that of mbw_kv4_attention up to the order of sums; the shared
- * pages are read and multiplied once for all requests, by the row of the longest.
- * workspace: mbw_kv4_attention_shared_workspace_bytes(head_dim, T, q_heads)
- * bytes, otherwise as mbw_kv4_attention's. Smaller or NULL: shared pages are
- * read for each request.
+ * The shared pages are read and multiplied once for all requests, by the row of
+ * the longest, where the head dimension is 64 or 128, a request has fewer than 96
+ * query rows (queries x q_heads / kv_heads) on average, the workspace holds
+ * mbw_kv4_attention_shared_workspace_bytes(head_dim, T, q_heads) bytes (otherwise
+ * it is as mbw_kv4_attention's), and to read them for every request is estimated
+ * to take longer. Else (smaller or NULL workspace, head dimension 256, ...) the
+ * call is mbw_kv4_attention's. The estimate is made from the sizes alone, with all
+ * of shared_len whatever the window: behind a window that hides most of the prefix
+ * mbw_kv4_attention is the faster call.
+ * The result is that of mbw_kv4_attention but for the order of sums and two
+ * roundings of what is read once for all, those that chunks of a prompt have: of a
+ * key or value s n + m its centred part s (n - 8) is rounded to fp16, by at most
+ * 2^-11 of itself, and so are the weights.
  */
 mbw_status mbw_kv4_attention_shared(const mbw_kv4_cache *cache, const void *q, int64_t q_stride, void *out,
                                     int64_t out_stride, float *lse, const int32_t *block_table, int64_t table_stride,

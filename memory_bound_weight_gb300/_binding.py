@@ -737,9 +737,13 @@ def kv4_attention_shared_workspace(head_dim, tokens, q_heads, device="cuda"):
 def kv4_attention_shared(cache, q, block_table, ctx_lens, shared_len, q_starts=None, scale=None, window=0, out=None,
                          return_lse=False, workspace=None):
     """kv4_attention for requests that begin with the same shared_len tokens in the same pages: the first shared_len //
-    page_size entries of the rows of block_table are equal, as far as each request's length goes. The shared pages are
-    read and multiplied once for the queries of all requests. The other arguments and the result are kv4_attention's.
-    workspace: from kv4_attention_shared_workspace; without one, shared pages are read for each request."""
+    page_size entries of the rows of block_table are equal, as far as each request's length goes. The other arguments are
+    kv4_attention's. The shared pages are read and multiplied once for the queries of all requests where head_dim is 64 or
+    128, a request has fewer than 96 query rows per KV head on average, workspace is one of kv4_attention_shared_workspace
+    for as many tokens, and to read them for each request is estimated to take longer (of all of shared_len: behind a window
+    that hides most of it kv4_attention is the faster call); else the call is kv4_attention. The result is kv4_attention's but
+    for the order of sums and for roundings of what is read once, those of chunks of a prompt: of a key or value s n + m the
+    part s (n - 8), and the weights, are rounded to fp16."""
     if shared_len is None:
         raise TypeError("shared_len must be a number of tokens")
     if _fast is None:
@@ -804,7 +808,7 @@ def _matrix(t, name, dtype, shape):
 
 
 def quantize_fp8_g128(X, norm_weight=None, norm_eps=1e-6):
-    """Activations bf16 (M, K) (rows may be apart) -> (Xq float8_e4m3fn (M, K), x_scales fp32 (M, K/128)): per row and
+    """Activations bf16 (M, K) (rows may be apart, by multiples of 8) -> (Xq float8_e4m3fn (M, K), x_scales fp32 (M, K/128)): per row and
     128 columns scale = max|x| / 448, code = e4m3(x / scale). With norm_weight bf16 (K,), of the RMS-normed rows."""
     if _fast is None:
         _load_fast()

@@ -1334,6 +1334,8 @@ size_t kv4_attention_shared_workspace(int head_dim, int64_t T, int64_t q_heads) 
 
 cudaError_t launch_kv4_attention_shared(const Kv4AttnArgs& a, int shared_len, cudaStream_t s) {
     const int64_t gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
+    // From kWideRows on the call's own tokens are the tcgen05 kernel's, which joins no part that is there already; 256 dimensions
+    // do not fit the shared part's kernel. Both take the plain call, which reads the shared pages for every request.
     if (a.head_dim == 256 || rows >= kWideRows || a.ws_bytes < kv4_attention_shared_workspace(a.head_dim, a.T, a.q_heads)) return launch_kv4_attention(a, s);
     const size_t plain = (kv4_attention_workspace(a.head_dim) + 15) / 16 * 16;
     Kv4AttnArgs b = a;

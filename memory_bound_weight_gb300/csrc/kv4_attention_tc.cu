@@ -1243,6 +1243,8 @@ cudaError_t plan_kv4_attention_prefix(const Kv4AttnArgs& a, int shared_len, Kv4S
     // would take longer than this kernel, 12 us and 1.25 a tile of keys, and what its SMs leave undone of the other's start
     // where that one has many items. Measured, plain and shared, us: Qwen3-4B's heads, 8192 tokens, 2, 4, 8 and 64 requests:
     // 13.8 19.0, 18.7 26.7, 26.0 31.4, 114.9 42.5; Qwen2.5-7B's, 12 of 2 to 5 queries, 30000 tokens: 132 53; 64, 512: 14.5 31.3.
+    // A window is not looked at: 64 requests behind 8192 tokens, windows of 64, 256, 1024, 2048, 4096 and none: 9.2 21.0, 13.5 28.7,
+    // 23.0 30.5, 35.8 32.0, 61.1 34.1, 112.8 38.8.
     const int64_t with = a.B < a.T ? a.B : a.T, gq = a.q_heads / a.kv_heads, rows = ((int64_t)a.T * gq + a.B - 1) / a.B;
     const double read = (double)with * ((rows + 7) / 8) * a.kv_heads * shared_len * (a.head_dim + 8 * (a.head_dim / a.group)) / 4900.0;
     const int64_t waves = (items * best + sms - 1) / sms, tiles = (units + best - 1) / best * waves;

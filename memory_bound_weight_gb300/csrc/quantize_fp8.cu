@@ -184,7 +184,10 @@ __device__ __forceinline__ float inverse_root(float hi, float lo, float k, float
 // mean but for 2^-40, and the codes do not hang on the order of the sum. Where the squares pass fp32 or would vanish in it
 // the sum is taken again in 64 bits.
 // ALONE: a CTA has a row; else each warp has one, which waits for no other and holds it up to 3584 columns: of many short
-// rows (alone, by warps, us: 600 x 3584 5.1, 7.3; 4000 x 3584 22.8, 17.8, now 16.5; 4096 x 18944 75.6, 114).
+// rows. Alone and by warps, us: 800 rows of 2048 6.2, 5.7, of 3584 6.7, 7.5; 1200 rows of 2048 7.8, 6.0, of 3584 8.6, 8.2, of
+// 4096 (whose end a warp reads twice) 8.9, 9.3, of 5120 10.8, 12.3; 4000 rows of 1024 18.5, 8.7, of 3584 22.9, 16.5, of 4096
+// 23.4, 19.4, of 5120 29.0, 24.7, of 8192 33.7, 43.3. The bounds are those of 3584 and 4096 columns: narrower rows would go by
+// warps from 500 to 800 rows on, and wider ones of up to 5120 from some 2000 on.
 constexpr int kManyRows = 1200, kShortRow = 4096;
 template <bool ALONE>
 __global__ void __launch_bounds__(kThreads) quantize_norm_kernel(const uint16_t* __restrict__ X, int64_t stride, uint8_t* __restrict__ Q,

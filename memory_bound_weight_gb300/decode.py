@@ -22,7 +22,8 @@ With --weights fp8 each product is one of 8-bit floating point operands with a
 scale for each block of 128: quantize_fp8_g128 (with the norm where there is one)
 and gemm_fp8_b128, gate and up in one call. With --shared N the requests' prompts
 begin with the same N tokens, whose keys and values are computed and held once;
-attention is then kv4_attention_shared.
+attention is then kv4_attention_shared (whose workspace is sized for a step's
+tokens: the rest of the prompts, in one pass, reads the shared pages for each request).
 """
 from __future__ import annotations
 
