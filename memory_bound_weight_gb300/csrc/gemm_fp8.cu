@@ -24,11 +24,13 @@
 // Where there are fewer tiles than pairs, k is cut between up to four pairs of a
 // cluster, whose sums are joined in order through their shared memory.
 //
-// What bounds it: a block of k takes a pair some 0.38 us, 650 clocks of products and, as
+// What bounds it: a block of k takes a pair some 0.36 us, 650 clocks of products and, as
 // there are but two accumulators, a part of the way from a product's end to the adders
-// and back (commit 380, reading 290, arrival 250). 4096 x 3584 x 18944 is 212 us, 2620
-// TFLOP/s, of which the products alone would take 145; without the additions it takes 202,
-// without any reading of accumulators 188, and its copies alone 158 (13.8 TB/s from L2).
+// and back (commit 380, reading 290, arrival 250). 4096 x 3584 x 18944 is 198 us, 2810
+// TFLOP/s, of which the products alone would take 145. (As it was at 212 us, without the
+// additions it took 202, without any reading of accumulators 188, and its copies alone 158,
+// 13.8 TB/s from L2. Since then who has given up a wait leaves the loop of the products,
+// which no longer asks for each block whether it has.)
 //
 // Up to 128 rows of X are a second kernel's (Few below), up to 8, or 16, gemv_fp8.cu's.
 #include <cuda.h>
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t to = (int64_t)m * a.N + n0;
                 constexpr int COLUMNS = GLU ? 64 : 128;
                 // The residual's values are read some ahead: it may be the output, and no load is moved before a store by itself
-                // (4096 x 3584 x 18944 with a residual: 228 us one by one, 222 four ahead, 221 eight, 235 the whole row, whose
+                // (4096 x 3584 x 18944 with a residual, now 205 to 211: 228 us one by one, 222 four ahead, 221 eight, 235 the whole row, whose
                 // registers do not fit).
                 constexpr int HELD = 8;
                 uint4 held[HELD];
@@ -567,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // What bounds it: where each SM has one tile, W's stream from HBM and the start before it (32 x 152064 x 3584 91 us, 6.0 TB/s;
 // 64 x 4608 x 3584 8.6 us, 3.5 of them a start and 2 a join); a block of k takes 0.26 us for 64 rows, the issue of products
 // and the adders' way through waits, loads and factors, and 0.42 for 128, most of it the adders'. (32 rows as 64: 18944 x
-// 3584 16.0 us in place of 13.9, gated 5632 x 2048 11.3 in place of 9.7.)
+// 3584 16.0 us in place of 13.9, gated 5632 x 2048 11.3 in place of 9.7.) The gated form spills, 204 to 264 bytes a thread
+// stored at the 168 registers of its launch.
 template <bool GLU, int NX>
 struct Few {
     static constexpr int MATS = GLU ? 2 : 1, STAGE = MATS * 128 * 128 + NX * 128, DEPTH = 208 * 1024 / STAGE;
