@@ -465,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t to = (int64_t)m * a.N + n0;
                 constexpr int COLUMNS = GLU ? 64 : 128;
                 // The residual's values are read some ahead: it may be the output, and no load is moved before a store by itself
-                // (4096 x 3584 x 18944 with a residual, now 205 to 211: 228 us one by one, 222 four ahead, 221 eight, 235 the whole row, whose
-                // registers do not fit).
+                // (4096 x 3584 x 18944 with a residual, now 205 to 211 us: 228 one by one, 222 four ahead, 221 eight, 235 the whole row,
+                // whose registers do not fit).
                 constexpr int HELD = 8;
                 uint4 held[HELD];
 #pragma unroll
@@ -566,8 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of rows that are not there; a column of Y is a lane of the accumulator, of one weight scale a block. No pairs: X is small,
 // and a CTA has a tile of W (gated: and U's) for itself. Two or four accumulators are in turn. k is cut between up to eight
 // CTAs of a cluster.
-// What bounds it: where each SM has one tile, W's stream from HBM and the start before it (32 x 152064 x 3584 91 us, 6.0 TB/s;
-// 64 x 4608 x 3584 8.6 us, 3.5 of them a start and 2 a join); a block of k takes 0.26 us for 64 rows, the issue of products
+// What bounds it: where each SM has one tile, W's stream from HBM and the start before it (32 x 152064 x 3584 85 us, 6.4 TB/s;
+// 64 x 4608 x 3584 7.7 us, most of them a start and a join); a block of k takes 0.26 us for 64 rows, the issue of products
 // and the adders' way through waits, loads and factors, and 0.42 for 128, most of it the adders'. (32 rows as 64: 18944 x
 // 3584 16.0 us in place of 13.9, gated 5632 x 2048 11.3 in place of 9.7.) The gated form spills, 204 to 264 bytes a thread
 // stored at the 168 registers of its launch.
